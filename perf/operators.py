@@ -396,8 +396,7 @@ def _own(st):
         more = dict(A_dec=st["A_dec"], tau=st["tau"])
         if c["use"] == "step":
             return carve.carve_gdr_step(*x, st["S0"], **more), st["S0"]
-        if st["cu"] is not None:
-            more.update(cu_seqlens=st["cu"], max_len=st["max_len"])
+        more["cu_seqlens"] = st["cu"]
         if c["use"] == "prefill":
             out = carve.carve_gdr_fwd(*x, S0=st["S0"], save_for_bwd=False, **more)
             return out["o"], out["S_final"]
@@ -408,8 +407,7 @@ def _own(st):
     at = dict(window=c["window"], sinks=c["sinks"])
     if c["use"] == "step":
         return carve.carve_swa_step(*x, st["k_cache"], st["v_cache"], st["pos"], **at), st["k_cache"], st["v_cache"]
-    if st["cu"] is not None:
-        at.update(cu_seqlens=st["cu"], max_len=st["max_len"])
+    at["cu_seqlens"] = st["cu"]
     if c["use"] == "prefill":
         out = carve.carve_swa_fwd(*x, want_lse=False, **at)
         carve.carve_swa_fill(st["k"], st["v"], st["k_cache"], st["v_cache"], **at)
