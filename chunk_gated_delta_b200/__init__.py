@@ -8,6 +8,10 @@ CPU fallback: if libcarve.so is missing or fails to load, every call raises.
     out  = carve.carve_fwd(q, k, v, g_logit, bx, w_logit, A, B, chunk=64)
     grads = carve.carve_bwd(q, k, v, g_logit, bx, w_logit, A, B, out["saved"], dO, chunk=64)
     o = carve.carve_step(q1, k1, v1, g1, bx1, w1, A, B, S)      # one decode token, S in place
+
+The two other mixers of a hybrid stack (include/carve_mixers.h) are bound in mixers.py and
+exported here: carve_gdr_fwd / _bwd / _step, the scalar-gated delta rule, and carve_swa_fwd /
+_bwd / _fill / _step, sliding-window attention with sink tokens.
 """
 from __future__ import annotations
 
@@ -15,7 +19,8 @@ import ctypes
 import os
 
 __all__ = ["CarveError", "Dims", "load", "library_path", "carve_fwd", "carve_bwd", "carve_step",
-           "saved_bytes", "bwd_workspace_bytes", "STATUS"]
+           "saved_bytes", "bwd_workspace_bytes", "STATUS", "carve_gdr_fwd", "carve_gdr_bwd", "carve_gdr_step",
+           "carve_swa_fwd", "carve_swa_bwd", "carve_swa_fill", "carve_swa_step"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libcarve.so")
@@ -259,3 +264,7 @@ def carve_step(q, k, v, g_logit, bx, w_logit, A, B, S, mc_mode: int = 0, chunk: 
                         _stream(stream))
     _check("carve_step", rc)
     return o
+
+
+from .mixers import (carve_gdr_bwd, carve_gdr_fwd, carve_gdr_step, carve_swa_bwd, carve_swa_fill,  # noqa: E402
+                     carve_swa_fwd, carve_swa_step)

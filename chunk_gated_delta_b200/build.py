@@ -1,4 +1,4 @@
-"""Builds libcarve.so (the C-ABI library of include/carve.h) in-tree for sm_100a with nvcc.
+"""Builds libcarve.so (the C-ABI library of include/carve.h and carve_mixers.h) in-tree for sm_100a with nvcc.
 
 Each .cu file is compiled to an object in its own process (in parallel), then the objects are
 linked into the shared library; an object is rebuilt only when its source, a header or this
@@ -24,8 +24,8 @@ def sources():
 
 
 def headers():
-    return sorted(glob.glob(os.path.join(PKG, "csrc", "*.cuh"))) + [os.path.join(ROOT, "include", "carve.h"),
-                                                                     os.path.abspath(__file__)]
+    return sorted(glob.glob(os.path.join(PKG, "csrc", "*.cuh")) +
+                  glob.glob(os.path.join(ROOT, "include", "*.h"))) + [os.path.abspath(__file__)]
 
 
 def deps():

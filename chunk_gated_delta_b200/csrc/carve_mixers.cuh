@@ -1,0 +1,147 @@
+// Shared pieces of the mixers declared in include/carve_mixers.h: argument structs, sequence
+// tables and launch declarations (product code; independent of the oracle).
+#pragma once
+#include "carve_device.cuh"
+
+namespace carve {
+
+// The sequences of a call: B batch elements of T tokens each, or (cu) N sequences packed in
+// `total` rows.
+struct Seqs {
+    const int *cu;
+    long long total;
+    int N, T;
+
+    // rows [row0, row0 + len) of sequence n; a packed sequence that leaves [0, total] is empty
+    // and *bad (when given) records it
+    __device__ __forceinline__ void rows(int n, long long &row0, int &len, int *bad = nullptr) const {
+        if (!cu) {
+            row0 = (long long)n * T;
+            len = T;
+            return;
+        }
+        const int c0 = cu[n], c1 = cu[n + 1];
+        row0 = c0;
+        len = c1 - c0;
+        if (c0 < 0 || c1 < c0 || (long long)c1 > total) {
+            row0 = 0;
+            len = 0;
+            if (bad) atomicOr(bad, 1);
+        }
+    }
+
+    // Tiles of C tokens, each sequence starting its own: sequence n's tiles are numbered from
+    // tile0(n, C).  Packed, cu[n] / C + n leaves every sequence at least ceil(len / C) numbers and
+    // needs no table of lengths on the host; the numbers between two sequences' tiles stay unused.
+    __host__ __device__ __forceinline__ long long n_tiles(int C) const {
+        return cu ? total / C + N : (long long)N * ((T + C - 1) / C);
+    }
+    __device__ __forceinline__ long long tile0(int n, int C) const {
+        return cu ? cu[n] / C + n : (long long)n * ((T + C - 1) / C);
+    }
+    // the sequence n and the tile c within it that number `tile` stands for; false where it is
+    // unused.  Packed, the last n with tile0(n) <= tile is found by bisection (tile0 grows with n).
+    __device__ __forceinline__ bool find(int tile, int C, int &n, int &c, long long &row0, int &len) const {
+        if (!cu) {
+            const int per = (T + C - 1) / C;
+            n = tile / per;
+            c = tile - n * per;
+        } else {
+            int lo = 0, hi = N - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (cu[mid] / C + mid <= tile)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            n = lo;
+            c = tile - (cu[n] / C + n);
+        }
+        rows(n, row0, len);
+        return c >= 0 && (long long)c * C < len;
+    }
+};
+
+// Threads of one CTA together: records packed sequences whose offsets are out of range.
+__device__ __forceinline__ void check_seqs(const Seqs &s, int *bad) {
+    if (!s.cu) return;
+    long long r;
+    int len;
+    for (int n = threadIdx.x; n < s.N; n += blockDim.x) s.rows(n, r, len, bad);
+}
+
+struct GdrArgs {
+    Seqs seq;
+    int Hk, Hv;
+    const void *q, *k, *v, *g_logit, *w_logit;
+    const float *A_dec, *tau, *S0;
+    void *o;
+    float *S_final;
+    // backward
+    const void *dO;
+    const float *dS_final;
+    void *dq, *dk, *dv, *dg_logit, *dw_logit;
+    float *dA_dec, *dtau, *dS0;
+    char *prep, *saved, *ws;   // per-tile operands; what the forward saves beside them; backward scratch
+};
+
+struct SwaArgs {
+    Seqs seq;
+    int Hq, Hkv, d, window, sinks;
+    float scale;
+    const void *q, *k, *v;
+    void *o;
+    float *lse;
+    // backward
+    const void *dO;
+    void *dq, *dk, *dv;
+    float *delta;              // rowsum(dO * o), [rows, Hq]
+    // cache
+    void *k_cache, *v_cache;
+    const long long *pos;
+};
+
+// The window: key j of a sequence is seen by query i.
+__device__ __forceinline__ bool swa_sees(int i, int j, int window, int sinks) {
+    return j <= i && (i - j < window || j < sinks);
+}
+
+// Key tiles of BN that queries [i0, i1) of a sequence see, in order: `near` tiles from tile `lo` that
+// the window reaches, and before them the `far` first tiles that hold sinks only.
+struct KeyTiles {
+    int far, lo, near;
+    __device__ __forceinline__ KeyTiles(int i0, int i1, int BN, int window, int sinks) {
+        lo = i0 - window + 1 > 0 ? (i0 - window + 1) / BN : 0;
+        near = (i1 - 1) / BN - lo + 1;
+        const int s = sinks < i1 ? sinks : i1;
+        far = (s + BN - 1) / BN;
+        far = far < lo ? far : lo;
+    }
+    __device__ __forceinline__ int count() const { return far + near; }
+    __device__ __forceinline__ int tile(int x) const { return x < far ? x : lo + x - far; }
+};
+
+// Last query of a sequence of `len` tokens that sees a key of [j0, j1).
+__device__ __forceinline__ int last_query(int j0, int j1, int len, int window, int sinks) {
+    if (j0 < sinks) return len - 1;
+    const long long i = (long long)j1 - 1 + window - 1;
+    return i < len - 1 ? (int)i : len - 1;
+}
+
+// sizes of the delta rule's buffers for one path, in bytes
+struct GdrSizes {
+    size_t prep, saved, bwd;
+};
+GdrSizes gdr_simt_sizes(const Seqs &s, int Hv, int K, int V);
+cudaError_t launch_gdr_fwd_simt(int K, int V, bool bf16, const GdrArgs &a, bool save, cudaStream_t st);
+cudaError_t launch_gdr_bwd_simt(int K, int V, bool bf16, const GdrArgs &a, cudaStream_t st);
+cudaError_t launch_gdr_step(int K, int V, bool bf16, const GdrArgs &a, cudaStream_t st);
+cudaError_t launch_swa_fwd_simt(bool bf16, const SwaArgs &a, cudaStream_t st);
+cudaError_t launch_swa_bwd_simt(bool bf16, const SwaArgs &a, cudaStream_t st);
+cudaError_t launch_swa_fill(bool bf16, const SwaArgs &a, cudaStream_t st);
+cudaError_t launch_swa_step(bool bf16, const SwaArgs &a, cudaStream_t st);
+int gdr_take_bad_seqlens();
+int swa_take_bad_seqlens();
+
+}  // namespace carve
