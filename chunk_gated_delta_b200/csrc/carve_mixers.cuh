@@ -129,6 +129,10 @@ __device__ __forceinline__ int last_query(int j0, int j1, int len, int window, i
     return i < len - 1 ? (int)i : len - 1;
 }
 
+// Polls of a bounded barrier wait of the tensor-core kernels here (each poll may suspend the thread
+// for a while: of the order of a second, far beyond any copy or product that completes).
+constexpr uint32_t kSwaWait = 1u << 22;
+
 // sizes of the delta rule's buffers for one path, in bytes
 struct GdrSizes {
     size_t prep, saved, bwd;
@@ -139,6 +143,8 @@ cudaError_t launch_gdr_bwd_simt(int K, int V, bool bf16, const GdrArgs &a, cudaS
 cudaError_t launch_gdr_step(int K, int V, bool bf16, const GdrArgs &a, cudaStream_t st);
 cudaError_t launch_swa_fwd_simt(bool bf16, const SwaArgs &a, cudaStream_t st);
 cudaError_t launch_swa_bwd_simt(bool bf16, const SwaArgs &a, cudaStream_t st);
+cudaError_t launch_swa_fwd_tc(const SwaArgs &a, cudaStream_t st);
+int swa_fwd_take_timeout();
 cudaError_t launch_swa_fill(bool bf16, const SwaArgs &a, cudaStream_t st);
 cudaError_t launch_swa_step(bool bf16, const SwaArgs &a, cudaStream_t st);
 int gdr_take_bad_seqlens();

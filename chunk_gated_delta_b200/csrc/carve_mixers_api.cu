@@ -181,10 +181,11 @@ carve_status carve_swa_fwd(const carve_swa_dims *d, const int32_t *cu_seqlens, c
     if (!ok_elem_opt(cu_seqlens) || !ok_ptr(q, rows) || !ok_ptr(k, rows) || !ok_ptr(v, rows) || !ok_ptr(o, rows) ||
         !ok_elem_opt(lse))
         return CARVE_ERR_INVALID_ARG;
-    if (!packed && rows == 0) return CARVE_OK;
     carve::SwaArgs a = swa_args(d, cu_seqlens);
     a.q = q; a.k = k; a.v = v; a.o = o; a.lse = lse;
-    return status(carve::launch_swa_fwd_simt(d->io == CARVE_IO_BF16, a, static_cast<cudaStream_t>(stream)));
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (rows == 0) return CARVE_OK;
+    return status(d->io == CARVE_IO_BF16 ? carve::launch_swa_fwd_tc(a, cs) : carve::launch_swa_fwd_simt(false, a, cs));
 }
 
 size_t carve_swa_bwd_workspace_bytes(const carve_swa_dims *d, int packed) {

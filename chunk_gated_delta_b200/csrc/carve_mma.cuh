@@ -208,5 +208,7 @@ __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap *map) {
 // box = [box_rows tokens, 1 head, inner channels]; elem_bytes 2 (bf16) or 4 (fp32).
 cudaError_t make_token_tile_map(CUtensorMap *map, const void *base, int elem_bytes, int inner, int H,
                                 long long rows, int box_rows);
+cudaError_t make_operand_tile_map(CUtensorMap *map, const void *base, int channels, int H, long long rows,
+                                  int box_rows);
 
 }  // namespace carve

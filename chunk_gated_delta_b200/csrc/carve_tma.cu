@@ -35,6 +35,22 @@ cudaError_t make_token_tile_map(CUtensorMap *map, const void *base, int elem_byt
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Boxes of box_rows tokens x 64 channels of one head, in rows of 128 bytes with the 128-byte
+// swizzle (the tensor core's operand layout: chunk c of row r at chunk c ^ (r % 8)).
+cudaError_t make_operand_tile_map(CUtensorMap *map, const void *base, int channels, int H, long long rows,
+                                  int box_rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+    if (!enc) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {(cuuint64_t)channels, (cuuint64_t)H, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)channels * 2, (cuuint64_t)channels * 2 * H};
+    const cuuint32_t box[3] = {64u, 1u, (cuuint32_t)box_rows};
+    const cuuint32_t estr[3] = {1u, 1u, 1u};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 // The opt-in above 48 KB of dynamic shared memory is a per-device attribute of the kernel that
 // persists, so it is set on the first launch on each device only (launches stay one driver
 // call; safe to call from several threads).
