@@ -5,17 +5,16 @@
 // head when the heads pair up (the keys of one 128-row window), else 256 rows of one head.  For
 // each 128-key block that a tile sees:
 //   S = Q K^T                    tcgen05.mma, accumulator in tensor memory (128 columns)
-//   P = 2^{S scale log2 e - m}   thread = row, so maximum and sum need no exchange; a first pass
-//                                over S finds the maximum, a second one forms P (reading S twice
-//                                from tensor memory costs less than 128 scores held in registers)
-//                                and writes it as bf16 over S's columns
+//   P = 2^{S scale log2 e - m}   two threads a row, 64 scores each in registers; they exchange
+//                                their maxima through shared memory; P goes back as bf16 over S
 //   O += P V                     A = P from tensor memory, O stays in tensor memory
 // The two tiles alternate, so the tensor core works on one while the other's rows are in
 // softmax.  m is the maximum that was current when O was last rescaled: O is rescaled (a round
 // trip through registers) only when some row's maximum has grown by more than 2^8 since, which
 // keeps P below 2^8 and sums in fp32 exact to rounding; the last division removes the reference.
-// Roles: warps 0-3 and 4-7 softmax of tile 0 and 1, warp 8 copies (TMA, ring of four 128-row key or
-// value tiles), warp 9 issues the products.
+// Roles: warps 0-7 and 8-15 softmax of tile 0 and 1 (the second four of each take columns 64 ..
+// 127: four warps a scheduler hide each other's latency, one half as many took 1.7 times as
+// long), warp 16 copies (TMA, ring of four 128-row key or value tiles), warp 17 issues the products.
 //
 // Blocks that a tile does not see are skipped; only blocks that a window edge or the diagonal
 // crosses are masked, by selection.  Value rows behind the sequence's end are zeroed in shared
@@ -39,14 +38,15 @@ int swa_fwd_take_timeout() {
 
 namespace {
 
-constexpr int BM = 128, BN = 128, kStages = 4, kThreadsTc = 320;
+constexpr int BM = 128, BN = 128, kStages = 4, kThreadsTc = 576;
 constexpr float kLazy = 8.f;   // growth of a row's maximum, in powers of two, that O may lag behind
 
 template <int D>
 struct FwdSmem {
     __nv_bfloat16 q[2][D / 64][BM * 64];
     __nv_bfloat16 kv[kStages][D / 64][BN * 64];
-    uint64_t qfull, kvfull[kStages], kvfree[kStages], sfull[2], pfull[2], ofull[2];
+    float part[2][2][BM];   // a row's maximum, at the end its sum, by tile and column half
+    uint64_t qfull, kvfull[kStages], kvfree[kStages], sfull[2], pfull[2], ofull[2], xbar[2][4];
     uint32_t tmem;
 };
 
@@ -89,12 +89,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(&sm.sfull[t], 1);
-            mbar_init(&sm.pfull[t], 128);
+            mbar_init(&sm.pfull[t], 256);
+            for (int i = 0; i < 4; ++i) mbar_init(&sm.xbar[t][i], 2);
             mbar_init(&sm.ofull[t], 1);
         }
         fence_mbar_init();
     }
-    if (warp == 9) tmem_alloc(&sm.tmem, 512);
+    if (warp == 17) tmem_alloc(&sm.tmem, 512);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
@@ -104,7 +105,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         return (bool)__all_sync(0xffffffffu, mbar_wait(&bar, phase & 1, kSwaWait));
     };
 
-    if (warp == 8) {
+    if (warp == 16) {
         if (lane == 0) {
             mbar_expect_tx(&sm.qfull, 2 * BM * D * 2);
             for (int t = 0; t < 2; ++t)
@@ -127,7 +128,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     mbar_wait(&sm.kvfull[i % kStages], (i / kStages) & 1, kSwaWait);
             }
         }
-    } else if (warp == 9) {
+    } else if (warp == 17) {
         constexpr uint32_t iS = umma_idesc_bf16(BM, BN), iO = umma_idesc_bf16(BM, D) | kUmmaBmn;
         int ns[2] = {0, 0}, np[2] = {0, 0};   // products S and P V issued, per tile
         auto issue_s = [&](int t, int slot) {
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     tc_fence_after_sync();
                     if (lane == 0) {
                         for (int kk = 0; kk < BN / 16; ++kk)
-                            umma_bf16_ta(tm + 256 + 128 * t, tm + 128 * t + 8 * kk,
+                            umma_bf16_ta(tm + 256 + 128 * t, tm + 128 * t + 8 * kk + (kk < 4 ? 0 : 32),
                                          umma_desc_mn(smem_u32(sm.kv[vs][0]) + 2048 * kk, BN * 128), iO, kk > 0 || np[t] > 0);
                         umma_commit(&sm.ofull[t]);
                     }
@@ -188,66 +189,77 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 if (ns[t]) wait(sm.sfull[t], ns[t] - 1);
                 if (np[t]) wait(sm.ofull[t], np[t] - 1);
             }
-    } else if (warp < 8) {
-        const int t = warp / 4, r = (warp % 4) * 32 + lane, i = w.i0[t] + r;
-        const uint32_t lanes = (uint32_t)(warp % 4) << 21;   // lane quarter in bits 16+
-        const uint32_t tS = tm + 128 * t + lanes, tO = tm + 256 + 128 * t + lanes;
+    } else {
+        const int t = warp / 8, half = (warp / 4) % 2, quarter = warp % 4, r = quarter * 32 + lane, i = w.i0[t] + r;
+        const uint32_t lanes = (uint32_t)quarter << 21;   // lane quarter in bits 16+
+        // this thread's 64 scores (and over the first 32 of them its 64 values of P), its half of O
+        const uint32_t tS = tm + 128 * t + 64 * half + lanes, tO = tm + 256 + 128 * t + (D / 2) * half + lanes;
         const bool plain = a.scale > 0.f;   // else the scores are scaled first (its sign, or zero)
         const float sc = (plain ? a.scale : 1.f) * 1.4426950408889634f;
-        float m = -INFINITY, l = 0.f;   // reference maximum (of unscaled scores) and sum
-        int nb = 0;
+        float m = -INFINITY, l = 0.f;   // reference maximum (of unscaled scores) and this half's sum
+        int nb = 0, nx = 0;
+        auto other = [&](float x) {     // exchange with the thread of the row's other half
+            sm.part[t][half][r] = x;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.xbar[t][quarter]);
+            ok = wait(sm.xbar[t][quarter], nx++);
+            return sm.part[t][1 - half][r];
+        };
         for (int b = 0; b < blocks && ok; ++b) {
             const int j0 = w.kt.tile(b) * BN;
             if (!w.sees(a, t, j0)) continue;
             ok = wait(sm.sfull[t], nb);
             if (!ok) break;
             tc_fence_after_sync();
-            // masked only where the diagonal or the window's far edge crosses the block
-            const bool edge = !(j0 + BN - 1 <= w.i0[t] && (w.i0[t] + BM - 1 - j0 < a.window || j0 + BN <= a.sinks));
-            const int hi = i - j0;                                           // seen: columns 0 .. hi that are
-            const int lo = (int)max((long long)i - a.window + 1 - j0, 0LL);  // from lo on, or before sk
-            const int sk = a.sinks - j0;
-            auto scores = [&](uint32_t *s, int x0) {   // columns x0 .. x0 + 31 as the softmax takes them
-                if (!plain) {
+            uint32_t s[64];
+            tmem_ld32(tS, s);
+            tmem_ld32(tS + 32, s + 32);
+            tmem_wait_ld();
+            tmem_tie(s);
+            tmem_tie(s + 32);
+            if (!plain) {
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) s[x] = __float_as_uint(__uint_as_float(s[x]) * a.scale);
-                }
-                if (edge) {
+                for (int x = 0; x < 64; ++x) s[x] = __float_as_uint(__uint_as_float(s[x]) * a.scale);
+            }
+            // masked only where the diagonal or the window's far edge crosses the block
+            if (!(j0 + BN - 1 <= w.i0[t] && (w.i0[t] + BM - 1 - j0 < a.window || j0 + BN <= a.sinks))) {
+                const int c0 = j0 + 64 * half, hi = i - c0;                      // seen: columns 0 .. hi that are
+                const int lo = (int)max((long long)i - a.window + 1 - c0, 0LL);  // from lo on, or before sk
+                const int sk = a.sinks - c0;
+#pragma unroll
+                for (int y = 0; y < 64; y += 32) {
+                    const int top = hi - y, from = lo - y, before = sk - y;
+                    const uint32_t past = top >= 31 ? 0xffffffffu : top < 0 ? 0u : (2u << top) - 1u;
+                    const uint32_t near = from <= 0 ? 0xffffffffu : from > 31 ? 0u : 0xffffffffu << from;
+                    const uint32_t sink = before >= 32 ? 0xffffffffu : before <= 0 ? 0u : (1u << before) - 1u;
+                    const uint32_t seen = past & (near | sink);
 #pragma unroll
                     for (int x = 0; x < 32; ++x)
-                        if (x0 + x > hi || (x0 + x < lo && x0 + x >= sk)) s[x] = 0xff800000u;   // -inf
+                        if (!((seen >> x) & 1u)) s[y + x] = 0xff800000u;   // -inf
                 }
-            };
-            uint32_t s[2][32];
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            tmem_ld32(tS, s[0]);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                tmem_wait_ld();
-                tmem_tie(s[x & 1]);
-                tmem_ld32(tS + 32 * ((x + 1) & 3), s[(x + 1) & 1]);   // the last one: the second pass's first
-                scores(s[x & 1], 32 * x);
-#pragma unroll
-                for (int y = 0; y < 32; ++y) mx[y & 3] = fmaxf(mx[y & 3], __uint_as_float(s[x & 1][y]));
             }
-            const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int x = 0; x < 64; ++x) mx[x & 3] = fmaxf(mx[x & 3], __uint_as_float(s[x]));
+            float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            mb = fmaxf(mb, other(mb));
+            if (!ok) break;
             const bool grown = (mb - m) * sc > kLazy;   // of this row alone: a row's result depends on no other
             if (__any_sync(0xffffffffu, grown)) {       // rare after the first block
                 const float m1 = grown ? mb : m, f = grown ? ex2((m - m1) * sc) : 1.f;
-                tmem_wait_ld();
-                tmem_tie(s[0]);
                 if (nb > 0) {
                     ok = wait(sm.ofull[t], nb - 1);
                     if (!ok) break;
                     tc_fence_after_sync();
-#pragma unroll
-                    for (int x = 0; x < D / 32; ++x) {
-                        tmem_ld32(tO + 32 * x, s[1]);
+#pragma unroll 1
+                    for (int x = 0; x < D / 2; x += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(tO + x, o);
                         tmem_wait_ld();
-                        tmem_tie(s[1]);
+                        tmem_tie16(o);
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) s[1][y] = __float_as_uint(__uint_as_float(s[1][y]) * f);
-                        tmem_st32(tO + 32 * x, s[1]);
+                        for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                        tmem_st16(tO + x, o);
                     }
                 }
                 l *= f;
@@ -256,38 +268,30 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             const float base = m == -INFINITY ? 0.f : m * sc;
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                tmem_wait_ld();
-                tmem_tie(s[x & 1]);
-                if (x < 3) tmem_ld32(tS + 32 * (x + 1), s[(x + 1) & 1]);
-                scores(s[x & 1], 32 * x);
-                uint32_t p[16];
-#pragma unroll
-                for (int y = 0; y < 32; y += 2) {
-                    const float p0 = ex2(fmaf(__uint_as_float(s[x & 1][y]), sc, -base));
-                    const float p1 = ex2(fmaf(__uint_as_float(s[x & 1][y + 1]), sc, -base));
-                    sum[y & 2] += p0;
-                    sum[(y & 2) + 1] += p1;
-                    p[y / 2] = pack_bf16(p0, p1);
-                }
-                tmem_st16(tS + 16 * x, p);   // columns whose scores (of 32 x and before) have been read
+            for (int x = 0; x < 64; x += 2) {
+                const float p0 = ex2(fmaf(__uint_as_float(s[x]), sc, -base)), p1 = ex2(fmaf(__uint_as_float(s[x + 1]), sc, -base));
+                sum[x & 2] += p0;
+                sum[(x & 2) + 1] += p1;
+                s[x / 2] = pack_bf16(p0, p1);
             }
             l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tmem_st32(tS, s);
             tmem_wait_st();
             tc_fence_before_sync();
             mbar_arrive(&sm.pfull[t]);
             ++nb;
         }
         if (ok && nb > 0) {
-            ok = wait(sm.ofull[t], nb - 1);
+            l += other(l);
+            ok = ok && wait(sm.ofull[t], nb - 1);
             tc_fence_after_sync();
             const float inv = 1.f / l;
             const size_t at = (size_t)(w.row0 + i) * a.Hq + w.h[t];
-            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.o) + at * D;
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.o) + at * D + (D / 2) * half;
 #pragma unroll
-            for (int x = 0; x < D / 32; ++x) {
+            for (int x = 0; x < D / 2; x += 32) {
                 uint32_t o[32];
-                tmem_ld32(tO + 32 * x, o);
+                tmem_ld32(tO + x, o);
                 tmem_wait_ld();
                 tmem_tie(o);
                 if (ok && i < w.i1[t]) {
@@ -298,18 +302,18 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                         v.y = pack_bf16(__uint_as_float(o[y + 2]) * inv, __uint_as_float(o[y + 3]) * inv);
                         v.z = pack_bf16(__uint_as_float(o[y + 4]) * inv, __uint_as_float(o[y + 5]) * inv);
                         v.w = pack_bf16(__uint_as_float(o[y + 6]) * inv, __uint_as_float(o[y + 7]) * inv);
-                        *reinterpret_cast<uint4 *>(out + 32 * x + y) = v;
+                        *reinterpret_cast<uint4 *>(out + x + y) = v;
                     }
                 }
             }
-            if (ok && a.lse && i < w.i1[t]) a.lse[at] = (m * sc + log2f(l)) * 0.6931471805599453f;
+            if (ok && a.lse && half == 0 && i < w.i1[t]) a.lse[at] = (m * sc + log2f(l)) * 0.6931471805599453f;
         }
     }
     if (!ok && lane == 0) atomicOr(&g_swa_timeout, 1);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    if (warp == 9) tmem_dealloc(tm, 512);
+    if (warp == 17) tmem_dealloc(tm, 512);
 }
 
 template <int D>
