@@ -22,6 +22,7 @@ int tc_bwd_take_bad_seqlens();
 int gdr_take_bad_seqlens();
 int swa_take_bad_seqlens();
 int swa_fwd_take_timeout();
+int swa_bwd_take_timeout();
 cudaError_t launch_selftest_timeout(uint32_t iterations, cudaStream_t st);
 cudaError_t launch_bwd_simt(int K, int V, bool bf16, const BwdArgs &a, float *dA, float *dB, cudaStream_t st);
 cudaError_t launch_fwd_exact(int K, int V, bool bf16, const FwdArgs &a, cudaStream_t st);
@@ -306,7 +307,7 @@ carve_status carve_step(const carve_dims *d, const void *q, const void *k, const
 carve_status carve_check(void *stream) {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return CARVE_ERR_CUDA;
     const int t = carve::tc_fwd_take_timeout() | carve::tc_bwd_take_timeout() | carve::step_take_timeout() |
-                  carve::swa_fwd_take_timeout();
+                  carve::swa_fwd_take_timeout() | carve::swa_bwd_take_timeout();
     const int bad = carve::simt_take_bad_seqlens() | carve::tc_fwd_take_bad_seqlens() | carve::tc_bwd_take_bad_seqlens() |
                     carve::gdr_take_bad_seqlens() | carve::swa_take_bad_seqlens();
     return t ? CARVE_ERR_TIMEOUT : bad ? CARVE_ERR_INVALID_ARG : CARVE_OK;

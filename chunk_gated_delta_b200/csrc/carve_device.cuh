@@ -72,6 +72,8 @@ __device__ __forceinline__ void content_signal(const float *Bh, const float *Ah,
 
 // Host: raise `kern`'s dynamic shared-memory limit to `bytes` on the current device, once.
 cudaError_t set_smem_once(const void *kern, int bytes);
+// Host: streaming multiprocessors of the current device.
+int sm_count();
 
 // Records of the tensor-core path, per (unit, gate chunk), in floats:
 //   saved by the forward: m (128), z (R), Delta (128), mean q (128), dw (1), 3 pad

@@ -96,7 +96,7 @@ struct SwaArgs {
     // backward
     const void *dO;
     void *dq, *dk, *dv;
-    float *delta;              // rowsum(dO * o), [rows, Hq]
+    float *delta;              // rowsum(dO * o), [rows, Hq] (tensor-core path: see there)
     // cache
     void *k_cache, *v_cache;
     const long long *pos;
@@ -111,6 +111,7 @@ __device__ __forceinline__ bool swa_sees(int i, int j, int window, int sinks) {
 // the window reaches, and before them the `far` first tiles that hold sinks only.
 struct KeyTiles {
     int far, lo, near;
+    KeyTiles() = default;
     __device__ __forceinline__ KeyTiles(int i0, int i1, int BN, int window, int sinks) {
         lo = i0 - window + 1 > 0 ? (i0 - window + 1) / BN : 0;
         near = (i1 - 1) / BN - lo + 1;
@@ -141,10 +142,12 @@ GdrSizes gdr_simt_sizes(const Seqs &s, int Hv, int K, int V);
 cudaError_t launch_gdr_fwd_simt(int K, int V, bool bf16, const GdrArgs &a, bool save, cudaStream_t st);
 cudaError_t launch_gdr_bwd_simt(int K, int V, bool bf16, const GdrArgs &a, cudaStream_t st);
 cudaError_t launch_gdr_step(int K, int V, bool bf16, const GdrArgs &a, cudaStream_t st);
-cudaError_t launch_swa_fwd_simt(bool bf16, const SwaArgs &a, cudaStream_t st);
-cudaError_t launch_swa_bwd_simt(bool bf16, const SwaArgs &a, cudaStream_t st);
+cudaError_t launch_swa_fwd_simt(const SwaArgs &a, cudaStream_t st);
+cudaError_t launch_swa_bwd_simt(const SwaArgs &a, cudaStream_t st);
 cudaError_t launch_swa_fwd_tc(const SwaArgs &a, cudaStream_t st);
+cudaError_t launch_swa_bwd_tc(const SwaArgs &a, cudaStream_t st);
 int swa_fwd_take_timeout();
+int swa_bwd_take_timeout();
 cudaError_t launch_swa_fill(bool bf16, const SwaArgs &a, cudaStream_t st);
 cudaError_t launch_swa_step(bool bf16, const SwaArgs &a, cudaStream_t st);
 int gdr_take_bad_seqlens();

@@ -185,12 +185,13 @@ carve_status carve_swa_fwd(const carve_swa_dims *d, const int32_t *cu_seqlens, c
     a.q = q; a.k = k; a.v = v; a.o = o; a.lse = lse;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if (rows == 0) return CARVE_OK;
-    return status(d->io == CARVE_IO_BF16 ? carve::launch_swa_fwd_tc(a, cs) : carve::launch_swa_fwd_simt(false, a, cs));
+    return status(d->io == CARVE_IO_BF16 ? carve::launch_swa_fwd_tc(a, cs) : carve::launch_swa_fwd_simt(a, cs));
 }
 
 size_t carve_swa_bwd_workspace_bytes(const carve_swa_dims *d, int packed) {
     if (check(d, true, packed != 0) != CARVE_OK) return 0;
-    return up(sizeof(float) * (size_t)rows_of(d, packed != 0) * d->Hq) + 256;
+    // two floats a row and head (the CUDA-core path uses one)
+    return up(2 * sizeof(float) * (size_t)rows_of(d, packed != 0) * d->Hq) + 256;
 }
 
 carve_status carve_swa_bwd(const carve_swa_dims *d, const int32_t *cu_seqlens, const void *q,
@@ -209,7 +210,8 @@ carve_status carve_swa_bwd(const carve_swa_dims *d, const int32_t *cu_seqlens, c
     carve::SwaArgs a = swa_args(d, cu_seqlens);
     a.q = q; a.k = k; a.v = v; a.o = const_cast<void *>(o); a.lse = const_cast<float *>(lse);
     a.dO = dO; a.dq = dq; a.dk = dk; a.dv = dv; a.delta = static_cast<float *>(workspace);
-    return status(carve::launch_swa_bwd_simt(d->io == CARVE_IO_BF16, a, static_cast<cudaStream_t>(stream)));
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    return status(d->io == CARVE_IO_BF16 ? carve::launch_swa_bwd_tc(a, cs) : carve::launch_swa_bwd_simt(a, cs));
 }
 
 carve_status carve_swa_fill(const carve_swa_dims *d, const int32_t *cu_seqlens, const void *k,

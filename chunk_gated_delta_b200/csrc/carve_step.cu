@@ -376,7 +376,7 @@ int step_take_timeout() {
     return v;
 }
 
-static int sm_count() {
+int sm_count() {
     static int cached[64] = {0};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;

@@ -257,13 +257,11 @@ cudaError_t bwd_t(const SwaArgs &a, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_swa_fwd_simt(bool bf16, const SwaArgs &a, cudaStream_t st) {
-    if (a.d == 64) return bf16 ? fwd_t<64, __nv_bfloat16>(a, st) : fwd_t<64, float>(a, st);
-    return bf16 ? fwd_t<128, __nv_bfloat16>(a, st) : fwd_t<128, float>(a, st);
+cudaError_t launch_swa_fwd_simt(const SwaArgs &a, cudaStream_t st) {
+    return a.d == 64 ? fwd_t<64, float>(a, st) : fwd_t<128, float>(a, st);
 }
-cudaError_t launch_swa_bwd_simt(bool bf16, const SwaArgs &a, cudaStream_t st) {
-    if (a.d == 64) return bf16 ? bwd_t<64, __nv_bfloat16>(a, st) : bwd_t<64, float>(a, st);
-    return bf16 ? bwd_t<128, __nv_bfloat16>(a, st) : bwd_t<128, float>(a, st);
+cudaError_t launch_swa_bwd_simt(const SwaArgs &a, cudaStream_t st) {
+    return a.d == 64 ? bwd_t<64, float>(a, st) : bwd_t<128, float>(a, st);
 }
 
 }  // namespace carve

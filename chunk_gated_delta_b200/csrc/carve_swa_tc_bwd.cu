@@ -1,0 +1,391 @@
+// Sliding-window attention with sink tokens, backward, on the 5th-generation tensor core (bf16;
+// include/carve_mixers.h).
+//
+// With lse and delta_i = sum_c dO_ic o_ic from the forward's results,
+//   p_ij = e^{scale q_i.k_j - lse_i},  ds_ij = p_ij (dO_i.v_j - delta_i)
+//   dv_j = sum_i p_ij dO_i,  dk_j = scale sum_i ds_ij q_i,  dq_i = scale sum_j ds_ij k_j
+// Two passes of one kernel, so that every sum stays in one accumulator in a fixed order (one pass
+// with dq summed by atomics needs 5 products instead of 7, but its results would depend on the
+// order of arrival).  A unit holds 128 rows (KEYS: keys with dk, dv; else queries with dq) as two
+// resident operand tiles R1, R2 and streams the other side in tiles C1, C2 of 64:
+//             R1   R2   C1   C2
+//   KEYS      k    v    q    dO     over the query heads of the key head
+//   else      q    dO   k    v
+//   S = R1 C1^T, dP = R2 C2^T   accumulators in tensor memory, two buffers
+//   P, dS                       thread = row, 64 columns; back to tensor memory as bf16 over S, dP
+//   acc1 += dS C1 (dk or dq),  acc2 += P C2 (dv)   A from tensor memory, C's rows contracted
+// Roles: warps 0-3 and 4-7 form P, dS of the even and odd column tiles, warp 8 copies, warp 9 issues
+// the products: S, dP of the tile after next go out while the other buffer is being worked on.
+// Persistent: a CTA walks its units with one set of running phases; R is double-buffered, so the next
+// unit's copies and first products overlap the last one's epilogue.
+#include "carve_mixers.cuh"
+#include "carve_umma.cuh"
+
+namespace carve {
+
+__device__ int g_swa_bwd_timeout;   // set when a bounded wait gives up (never expected)
+
+int swa_bwd_take_timeout() {
+    int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_swa_bwd_timeout, sizeof(int)) != cudaSuccess) return 0;
+    if (v) {
+        const int z = 0;
+        cudaMemcpyToSymbol(g_swa_bwd_timeout, &z, sizeof(int));
+    }
+    return v;
+}
+
+namespace {
+
+constexpr int BR = 128, BC = 64, kStages = 3, kThreadsTc = 320;
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int D>
+struct BwdSmem {
+    __nv_bfloat16 r[2][2][D / 64][BR * 64];        // [buffer][R1, R2]
+    __nv_bfloat16 c[kStages][2][D / 64][BC * 64];  // [stage][C1, C2]
+    float2 ld[kStages][BC];                        // (lse log2 e, delta) of the columns (KEYS)
+    uint64_t rfull[2], rfree[2], cfull[kStages], cfree[kStages], sfull[2], dfull[2], accfull, accfree;
+    uint32_t tmem;
+};
+
+// (lse log2 e, delta) of every row and query head, [Hq][rows]: 16 lanes a (row, head), 16 bytes each
+template <int D>
+__global__ void __launch_bounds__(256) swa_rows(SwaArgs a, long long rows) {
+    constexpr int L = D / 8;
+    const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) / L;   // row * Hq + head
+    const int x = threadIdx.x % L;
+    float s = 0.f;
+    if (i < rows * a.Hq) {
+        const uint4 o = reinterpret_cast<const uint4 *>(a.o)[i * L + x], g = reinterpret_cast<const uint4 *>(a.dO)[i * L + x];
+        const uint32_t ow[4] = {o.x, o.y, o.z, o.w}, gw[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            s += __uint_as_float(ow[y] << 16) * __uint_as_float(gw[y] << 16);
+            s += __uint_as_float(ow[y] & 0xffff0000u) * __uint_as_float(gw[y] & 0xffff0000u);
+        }
+    }
+#pragma unroll
+    for (int off = L / 2; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    if (x == 0 && i < rows * a.Hq)
+        reinterpret_cast<float2 *>(a.delta)[(i % a.Hq) * rows + i / a.Hq] = make_float2(a.lse[i] * kLog2e, s);
+}
+
+// A unit: 128 rows of one sequence and head, and its column tiles.
+template <bool KEYS>
+struct Unit {
+    long long row0;
+    int len, r0, r1, head;   // rows r0 .. r1 - 1, their head
+    int n, per, c0;          // column tiles in all; KEYS: per query head, from tile c0
+    KeyTiles kt;
+    __device__ __forceinline__ bool set(const SwaArgs &a, int u) {
+        const int heads = KEYS ? a.Hkv : a.Hq;
+        int s, c;
+        if (!a.seq.find(u / heads, BR, s, c, row0, len)) return false;
+        head = u % heads;
+        r0 = c * BR;
+        r1 = min(r0 + BR, len);
+        if (KEYS) {
+            c0 = r0 / BC;
+            per = last_query(r0, r1, len, a.window, a.sinks) / BC - c0 + 1;
+            n = per * (a.Hq / a.Hkv);
+        } else {
+            kt = KeyTiles(r0, r1, BC, a.window, a.sinks);
+            n = kt.count();
+        }
+        return true;
+    }
+    __device__ __forceinline__ int col0(int b) const { return (KEYS ? c0 + b % per : kt.tile(b)) * BC; }
+    __device__ __forceinline__ int col_head(const SwaArgs &a, int b) const {
+        const int share = a.Hq / a.Hkv;
+        return KEYS ? head * share + b / per : head / share;
+    }
+};
+
+template <int D, bool KEYS>
+__global__ void __launch_bounds__(kThreadsTc, 1)
+    swa_tc_bwd(SwaArgs a, const __grid_constant__ CUtensorMap mr1, const __grid_constant__ CUtensorMap mr2,
+               const __grid_constant__ CUtensorMap mc1, const __grid_constant__ CUtensorMap mc2, int units, long long rows) {
+    extern __shared__ __align__(16) unsigned char raw[];
+    BwdSmem<D> &sm = *reinterpret_cast<BwdSmem<D> *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    constexpr int KH = D / 64;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.rfull[i], 1);
+            mbar_init(&sm.rfree[i], 1);
+            mbar_init(&sm.sfull[i], 1);
+            mbar_init(&sm.dfull[i], 128);
+        }
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&sm.cfull[i], KEYS ? 33 : 1);
+            mbar_init(&sm.cfree[i], 1);
+        }
+        mbar_init(&sm.accfull, 1);
+        mbar_init(&sm.accfree, 256);
+        fence_mbar_init();
+    }
+    if (warp == 9) tmem_alloc(&sm.tmem, 512);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tm = sm.tmem;   // S buffers at 0, 64; dP at 128, 192; acc1 at 256, acc2 at 384
+    bool ok = true;
+    auto wait = [&](uint64_t &bar, int phase) {   // by a whole warp
+        return (bool)__all_sync(0xffffffffu, mbar_wait(&bar, phase & 1, kSwaWait));
+    };
+    Unit<KEYS> w;
+    int nu = 0, nc = 0;   // units and column tiles so far
+
+    if (warp == 8) {
+        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            if (!w.set(a, u)) continue;
+            const int x = nu & 1;
+            if (nu >= 2) ok = wait(sm.rfree[x], nu / 2 - 1);
+            if (!ok) break;
+            if (lane == 0) {
+                mbar_expect_tx(&sm.rfull[x], 2 * BR * D * 2);
+                for (int y = 0; y < KH; ++y) {
+                    tma_load_3d(sm.r[x][0][y], &mr1, 64 * y, w.head, (int)w.row0 + w.r0, &sm.rfull[x]);
+                    tma_load_3d(sm.r[x][1][y], &mr2, 64 * y, w.head, (int)w.row0 + w.r0, &sm.rfull[x]);
+                }
+            }
+            ++nu;
+            for (int b = 0; b < w.n; ++b) {
+                const int s = nc % kStages, c0 = w.col0(b), h = w.col_head(a, b);
+                if (nc >= kStages) ok = wait(sm.cfree[s], nc / kStages - 1);
+                if (!ok) break;
+                if (lane == 0) {
+                    mbar_expect_tx(&sm.cfull[s], 2 * BC * D * 2);
+                    for (int y = 0; y < KH; ++y) {
+                        tma_load_3d(sm.c[s][0][y], &mc1, 64 * y, h, (int)w.row0 + c0, &sm.cfull[s]);
+                        tma_load_3d(sm.c[s][1][y], &mc2, 64 * y, h, (int)w.row0 + c0, &sm.cfull[s]);
+                    }
+                }
+                if (KEYS) {
+                    const float2 *src = reinterpret_cast<const float2 *>(a.delta) + (size_t)h * rows + w.row0;
+#pragma unroll
+                    for (int i = lane; i < BC; i += 32) sm.ld[s][i] = c0 + i < w.len ? src[c0 + i] : make_float2(0.f, 0.f);
+                    mbar_arrive(&sm.cfull[s]);
+                }
+                ++nc;
+            }
+        }
+        if (!ok) {   // the copies in flight land before the CTA leaves
+            for (int i = max(0, nu - 2); i < nu; ++i) wait(sm.rfull[i & 1], i / 2);
+            for (int i = max(0, nc - kStages); i < nc; ++i) wait(sm.cfull[i % kStages], i / kStages);
+        }
+    } else if (warp == 9) {
+        constexpr uint32_t iS = umma_idesc_bf16(BR, BC), iA = umma_idesc_bf16(BR, D) | kUmmaBmn;
+        // S, dP of column tile number c (of all) with rows in buffer x: waits for the tile, zeroes its
+        // rows behind the sequence's end (they meet P = dS = 0 in the sums)
+        auto issue_s = [&](int c, int x, int there) {
+            const int s = c % kStages;
+            ok = wait(sm.cfull[s], c / kStages);
+            if (!ok) return;
+            if (there < BC) {
+                for (int y = 0; y < 2 * KH; ++y)
+                    for (int i = there * 8 + lane; i < BC * 8; i += 32)
+                        reinterpret_cast<uint4 *>(sm.c[s][y / KH][y % KH])[i] = make_uint4(0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            tc_fence_after_sync();
+            if (lane == 0) {
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        umma_bf16(tm + 128 * y + 64 * (c & 1), umma_desc(smem_u32(sm.r[x][y][kk / 4]) + 32 * (kk % 4)),
+                                  umma_desc(smem_u32(sm.c[s][y][kk / 4]) + 32 * (kk % 4)), iS, kk > 0);
+                umma_commit(&sm.sfull[c & 1]);
+            }
+            __syncwarp();
+        };
+        int done = 0;   // column tiles whose S, dP were issued
+        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            if (!w.set(a, u)) continue;
+            const int x = nu & 1;
+            ok = wait(sm.rfull[x], nu / 2);
+            for (int b = 0; b < min(2, w.n) && ok; ++b) {
+                issue_s(nc + b, x, w.len - w.col0(b));
+                if (ok) ++done;
+            }
+            for (int b = 0; b < w.n && ok; ++b, ++nc) {
+                ok = wait(sm.dfull[nc & 1], nc / 2);
+                if (ok && b == 0 && nu > 0) ok = wait(sm.accfree, nu - 1);
+                if (!ok) break;
+                tc_fence_after_sync();
+                if (lane == 0) {
+                    const int s = nc % kStages;
+#pragma unroll
+                    for (int kk = 0; kk < BC / 16; ++kk)
+                        umma_bf16_ta(tm + 256, tm + 128 + 64 * (nc & 1) + 8 * kk,
+                                     umma_desc_mn(smem_u32(sm.c[s][0][0]) + 2048 * kk, BC * 128), iA, b > 0 || kk > 0);
+                    if (KEYS) {
+#pragma unroll
+                        for (int kk = 0; kk < BC / 16; ++kk)
+                            umma_bf16_ta(tm + 384, tm + 64 * (nc & 1) + 8 * kk,
+                                         umma_desc_mn(smem_u32(sm.c[s][1][0]) + 2048 * kk, BC * 128), iA, b > 0 || kk > 0);
+                    }
+                    umma_commit(&sm.cfree[s]);
+                    if (b == w.n - 1) {
+                        umma_commit(&sm.rfree[x]);
+                        umma_commit(&sm.accfull);
+                    }
+                }
+                __syncwarp();
+                if (b + 2 < w.n) {
+                    issue_s(nc + 2, x, w.len - w.col0(b + 2));
+                    if (ok) ++done;
+                }
+            }
+            ++nu;
+        }
+        if (!ok) {   // products in flight finish before the tensor memory is freed
+            for (int i = max(0, done - 2); i < done; ++i) wait(sm.sfull[i & 1], i / 2);
+            for (int i = max(0, nc - kStages); i < nc; ++i) wait(sm.cfree[i % kStages], i / kStages);
+        }
+    } else {
+        const int g = warp / 4, quarter = warp % 4, t = quarter * 32 + lane;
+        const uint32_t lanes = (uint32_t)quarter << 21;
+        const uint32_t tS = tm + 64 * g + lanes, tP = tm + 128 + 64 * g + lanes;
+        const float sc = a.scale * kLog2e;
+        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            if (!w.set(a, u)) continue;
+            const int row = w.r0 + t;   // of the sequence
+            float2 mine = make_float2(0.f, 0.f);
+            if (!KEYS && row < w.r1) mine = reinterpret_cast<const float2 *>(a.delta)[(size_t)w.head * rows + w.row0 + row];
+            for (int b = 0; b < w.n && ok; ++b, ++nc) {
+                if ((nc & 1) != g) continue;
+                const int c0 = w.col0(b);
+                ok = wait(sm.sfull[g], nc / 2);
+                if (!ok) break;
+                tc_fence_after_sync();
+                // masked only where the diagonal, the window's far edge or the end crosses the tile
+                const int i0 = KEYS ? c0 : w.r0, i1 = KEYS ? c0 + BC : w.r0 + BR, j0 = KEYS ? w.r0 : c0, j1 = KEYS ? w.r0 + BR : c0 + BC;
+                const bool edge = !(j1 - 1 <= i0 && (i1 - 1 - j0 < a.window || j1 <= a.sinks) && i1 <= w.len);
+                const float2 *ld = sm.ld[nc % kStages];
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t s[32], d[32];
+                    tmem_ld32(tS + 32 * half, s);
+                    tmem_ld32(tP + 32 * half, d);
+                    tmem_wait_ld();
+                    tmem_tie(s);
+                    tmem_tie(d);
+                    uint32_t seen = 0xffffffffu;
+                    if (edge) {   // bit x: column c0 + 32 half + x
+                        const int y = c0 + 32 * half;
+                        if (KEYS) {   // queries from this key on, below its window's end (a sink: any), below len
+                            const int from = row - y;
+                            const long long end = row < a.sinks ? (long long)w.len : min((long long)w.len, (long long)row + a.window);
+                            const long long n = end - y;
+                            seen = from <= 0 ? 0xffffffffu : from > 31 ? 0u : 0xffffffffu << from;
+                            seen &= n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << (int)n) - 1u;
+                        } else {      // keys up to this query, from its window's start on or sinks
+                            const int top = row - y, before = a.sinks - y;
+                            const long long from = (long long)row - a.window + 1 - y;
+                            const uint32_t near = from <= 0 ? 0xffffffffu : from > 31 ? 0u : 0xffffffffu << (int)from;
+                            const uint32_t sink = before >= 32 ? 0xffffffffu : before <= 0 ? 0u : (1u << before) - 1u;
+                            seen = (top >= 31 ? 0xffffffffu : top < 0 ? 0u : (2u << top) - 1u) & (near | sink);
+                        }
+                    }
+                    uint32_t pk[16], dk[16];
+#pragma unroll
+                    for (int x = 0; x < 32; x += 2) {
+                        float p[2], e[2];
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const float2 c = KEYS ? ld[32 * half + x + y] : mine;
+                            p[y] = ex2(fmaf(__uint_as_float(s[x + y]), sc, -c.x));
+                            e[y] = p[y] * (__uint_as_float(d[x + y]) - c.y);
+                            if (edge && !((seen >> (x + y)) & 1u)) p[y] = e[y] = 0.f;
+                        }
+                        pk[x / 2] = pack_bf16(p[0], p[1]);
+                        dk[x / 2] = pack_bf16(e[0], e[1]);
+                    }
+                    if (KEYS) tmem_st16(tS + 16 * half, pk);
+                    tmem_st16(tP + 16 * half, dk);
+                }
+                tmem_wait_st();
+                tc_fence_before_sync();
+                mbar_arrive(&sm.dfull[g]);
+            }
+            if (!ok) break;
+            ok = wait(sm.accfull, nu);
+            if (!ok) break;
+            ++nu;
+            tc_fence_after_sync();
+            // KEYS: warps 0-3 write dv, 4-7 dk; else both write half the channels of dq
+            constexpr int W = KEYS ? D : D / 2;
+            const uint32_t src = tm + lanes + (KEYS ? (g == 0 ? 384 : 256) : 256 + W * g);
+            const float f = KEYS && g == 0 ? 1.f : a.scale;
+            const size_t at = ((size_t)(w.row0 + row) * (KEYS ? a.Hkv : a.Hq) + w.head) * D;
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(KEYS ? (g == 0 ? a.dv : a.dk) : a.dq) + at + (KEYS ? 0 : W * g);
+#pragma unroll
+            for (int x = 0; x < W; x += 32) {
+                uint32_t o[32];
+                tmem_ld32(src + x, o);
+                tmem_wait_ld();
+                tmem_tie(o);
+                if (row < w.r1) {
+#pragma unroll
+                    for (int y = 0; y < 32; y += 8) {
+                        uint4 v;
+                        v.x = pack_bf16(__uint_as_float(o[y]) * f, __uint_as_float(o[y + 1]) * f);
+                        v.y = pack_bf16(__uint_as_float(o[y + 2]) * f, __uint_as_float(o[y + 3]) * f);
+                        v.z = pack_bf16(__uint_as_float(o[y + 4]) * f, __uint_as_float(o[y + 5]) * f);
+                        v.w = pack_bf16(__uint_as_float(o[y + 6]) * f, __uint_as_float(o[y + 7]) * f);
+                        *reinterpret_cast<uint4 *>(out + x + y) = v;
+                    }
+                }
+            }
+            tc_fence_before_sync();
+            mbar_arrive(&sm.accfree);
+        }
+    }
+    if (!ok && lane == 0) atomicOr(&g_swa_bwd_timeout, 1);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    if (warp == 9) tmem_dealloc(tm, 512);
+}
+
+template <int D, bool KEYS>
+cudaError_t pass(const SwaArgs &a, const CUtensorMap &r1, const CUtensorMap &r2, const CUtensorMap &c1, const CUtensorMap &c2,
+                 long long rows, cudaStream_t st) {
+    auto kern = swa_tc_bwd<D, KEYS>;
+    const int bytes = (int)sizeof(BwdSmem<D>) + 1024;
+    const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), bytes);
+    if (e != cudaSuccess) return e;
+    const int units = (int)(a.seq.n_tiles(BR) * (KEYS ? a.Hkv : a.Hq)), sms = sm_count();
+    kern<<<units < sms ? units : sms, kThreadsTc, bytes, st>>>(a, r1, r2, c1, c2, units, rows);
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t bwd_t(const SwaArgs &a, cudaStream_t st) {
+    const long long rows = a.seq.cu ? a.seq.total : (long long)a.seq.N * a.seq.T;
+    const void *base[4] = {a.q, a.k, a.v, a.dO};
+    CUtensorMap big[4], small[4];   // boxes of 128 and 64 rows of q, k, v, dO
+    for (int i = 0; i < 4; ++i) {
+        const int H = i == 1 || i == 2 ? a.Hkv : a.Hq;
+        cudaError_t e = make_operand_tile_map(&big[i], base[i], D, H, rows, BR);
+        if (e == cudaSuccess) e = make_operand_tile_map(&small[i], base[i], D, H, rows, BC);
+        if (e != cudaSuccess) return e;
+    }
+    swa_rows<D><<<(unsigned)((rows * a.Hq * (D / 8) + 255) / 256), 256, 0, st>>>(a, rows);
+    cudaError_t e = pass<D, true>(a, big[1], big[2], small[0], small[3], rows, st);
+    if (e == cudaSuccess) e = pass<D, false>(a, big[0], big[3], small[1], small[2], rows, st);
+    return e;
+}
+
+}  // namespace
+
+cudaError_t launch_swa_bwd_tc(const SwaArgs &a, cudaStream_t st) {
+    return a.d == 64 ? bwd_t<64>(a, st) : bwd_t<128>(a, st);
+}
+
+}  // namespace carve
