@@ -492,6 +492,10 @@ __global__ void __launch_bounds__(256) gdr_reduce_decay(const float *p, long lon
     }
 }
 
+void launch_gdr_reduce_decay(const float *p, long long tiles, int Hv, float *dA_dec, float *dtau, cudaStream_t st) {
+    gdr_reduce_decay<<<Hv, 256, 0, st>>>(p, tiles, Hv, dA_dec, dtau);
+}
+
 GdrSizes gdr_simt_sizes(const Seqs &s, int Hv, int K, int V) {
     const size_t slots = (size_t)s.n_tiles(C) * Hv, per = sizeof(float) * ((size_t)V * K + C * V);
     return {sizeof(float) * slots * kPrep, slots * per, slots * (per + 2 * sizeof(float))};
@@ -521,9 +525,8 @@ cudaError_t bwd_t(const GdrArgs &a, cudaStream_t st) {
     sweep<<<a.seq.N * a.Hv * (V / 32), NT, sizeof(SweepSmem<K>), st>>>(a);
     if (tiles) grad<<<(unsigned)(tiles * a.Hk), NT, sizeof(GradSmem<K, V>), st>>>(a);
     if (a.dA_dec || a.dtau)
-        gdr_reduce_decay<<<a.Hv, 256, 0, st>>>(
-            reinterpret_cast<const float *>(a.ws) + (size_t)tiles * a.Hv * ((size_t)V * K + C * V), tiles, a.Hv,
-            a.dA_dec, a.dtau);
+        launch_gdr_reduce_decay(reinterpret_cast<const float *>(a.ws) + (size_t)tiles * a.Hv * ((size_t)V * K + C * V), tiles, a.Hv,
+                                a.dA_dec, a.dtau, st);
     return cudaGetLastError();
 }
 
@@ -535,20 +538,19 @@ cudaError_t by_shape(int K, int V, F f) {
 
 struct Fwd {
     const GdrArgs &a;
-    bool bf16, save;
+    bool save;
     cudaStream_t st;
     template <int K, int V>
     cudaError_t operator()() const {
-        return bf16 ? fwd_t<K, V, __nv_bfloat16>(a, save, st) : fwd_t<K, V, float>(a, save, st);
+        return fwd_t<K, V, float>(a, save, st);
     }
 };
 struct Bwd {
     const GdrArgs &a;
-    bool bf16;
     cudaStream_t st;
     template <int K, int V>
     cudaError_t operator()() const {
-        return bf16 ? bwd_t<K, V, __nv_bfloat16>(a, st) : bwd_t<K, V, float>(a, st);
+        return bwd_t<K, V, float>(a, st);
     }
 };
 
@@ -638,11 +640,11 @@ struct Step {
 
 }  // namespace
 
-cudaError_t launch_gdr_fwd_simt(int K, int V, bool bf16, const GdrArgs &a, bool save, cudaStream_t st) {
-    return by_shape(K, V, Fwd{a, bf16, save, st});
+cudaError_t launch_gdr_fwd_simt(int K, int V, const GdrArgs &a, bool save, cudaStream_t st) {
+    return by_shape(K, V, Fwd{a, save, st});
 }
-cudaError_t launch_gdr_bwd_simt(int K, int V, bool bf16, const GdrArgs &a, cudaStream_t st) {
-    return by_shape(K, V, Bwd{a, bf16, st});
+cudaError_t launch_gdr_bwd_simt(int K, int V, const GdrArgs &a, cudaStream_t st) {
+    return by_shape(K, V, Bwd{a, st});
 }
 cudaError_t launch_gdr_step(int K, int V, bool bf16, const GdrArgs &a, cudaStream_t st) {
     return by_shape(K, V, Step{a, bf16, st});

@@ -1,0 +1,865 @@
+// Scalar-gated delta rule, backward, on the 5th-generation tensor core (carve_gdr_tc.cuh).
+//
+// gdr_tc_bsweep: one CTA per (sequence, value head) carries dS backwards through the chunks, the
+// mirror of the forward's sweep (value channels = lanes of the accumulator, A in tensor memory, a
+// thread owns half a state row; only dO^T A takes its A from shared memory, read transposed):
+//   X = dS1 K^T (hi, lo), dO^T A    -> dU = dO^T A + e^{G_C - G} X, split
+//   dY = dU Tm (three terms)         -> -w e^G dY, split; dV = w dY; dY
+//   dS0 = e^{G_C} dS1 + (e^G dO)^T Q - (w e^G dY)^T K   (hi, lo) -> split for the next chunk
+// It leaves dS1 and dY of every chunk in bf16.
+//
+// gdr_tc_grad: with S0, U (forward) and dS1, dY known, the gradients of q, k and the gates have no
+// order: persistent CTAs take (tile, key head), all value heads of the key head in turn.  Tokens are the
+// lanes, queries in 0-63 and keys in 64-127, so that one product serves both:
+//   [dO; dY] U^T  -> P1 = D (dO U^T), P2 = -w D (dY U^T) below the diagonal, bf16
+//   [dO; dY] S0   -> dq += e^G x, dk -= w e^G x;   [.; U] dS1 -> dk += e^{G_C - G} x
+//   [P1; P2] K + [0; P1^T] Q + [0; P2^T] K  accumulated over the value heads
+// P1^T and P2^T are the same tile read along its other index; the zero block beside it fills the
+// lanes that have no part.  What bounds it is HBM: two states, U and dY a chunk and head.
+#include "carve_gdr_tc.cuh"
+
+namespace carve {
+
+__device__ int g_gdr_bwd_timeout;   // set when a bounded wait gives up (never expected)
+__device__ int g_gdr_tc_bwd_bad_seqlens;
+
+int gdr_tc_bwd_take_timeout() {
+    int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_gdr_bwd_timeout, sizeof(int)) != cudaSuccess) return 0;
+    if (v) {
+        const int z = 0;
+        cudaMemcpyToSymbol(g_gdr_bwd_timeout, &z, sizeof(int));
+    }
+    return v;
+}
+int gdr_tc_bwd_take_bad_seqlens() {
+    int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_gdr_tc_bwd_bad_seqlens, sizeof(int)) != cudaSuccess) return 0;
+    if (v) {
+        const int z = 0;
+        cudaMemcpyToSymbol(g_gdr_tc_bwd_bad_seqlens, &z, sizeof(int));
+    }
+    return v;
+}
+
+namespace {
+
+template <int K, int V>
+struct BsweepSmem {
+    __nv_bfloat16 k[2][K / 64][kC * 64], q[2][K / 64][kC * 64], dO[2][2][kC * 64];   // dO's second half zero at V = 64
+    GdrPrep p[2];
+    __nv_bfloat16 S[V * K], y[kC * V], dv[kC * V];   // on their way out
+    uint64_t full[2], free[2], sready, dready, gfull, uready, yfull, yready, sfull, Sout, Sfree, yout, yfree, drain;
+    uint32_t tmem;
+};
+
+template <int K, int V>
+__global__ void __launch_bounds__(352, 1)
+    gdr_tc_bsweep(GdrArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                  const __grid_constant__ CUtensorMap md) {
+    extern __shared__ __align__(16) unsigned char raw[];
+    typedef BsweepSmem<K, V> Smem;
+    Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    constexpr int KH = K / 64, VH = V / 64;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int h = blockIdx.x % a.Hv, n = blockIdx.x / a.Hv, hk = h / (a.Hv / a.Hk);
+    long long row0;
+    int len;
+    a.seq.rows(n, row0, len, threadIdx.x == 0 ? &g_gdr_tc_bwd_bad_seqlens : nullptr);
+    const long long t0 = a.seq.tile0(n, kC);
+    const int chunks = (len + kC - 1) / kC;
+    if (threadIdx.x == 0) {
+        for (uint64_t *b : {&sm.full[0], &sm.full[1], &sm.free[0], &sm.free[1], &sm.gfull, &sm.yfull, &sm.sfull, &sm.Sfree,
+                            &sm.yfree, &sm.drain})
+            mbar_init(b, 1);
+        for (uint64_t *b : {&sm.sready, &sm.dready, &sm.uready, &sm.yready, &sm.Sout, &sm.yout}) mbar_init(b, 256);
+        fence_mbar_init();
+    }
+    if (VH == 1) {
+        for (int i = threadIdx.x; i < 2 * kC * 8; i += blockDim.x)
+            reinterpret_cast<uint4 *>(sm.dO[i / (kC * 8)][1])[i % (kC * 8)] = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+    }
+    if (warp == 9) tmem_alloc(&sm.tmem, 512);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tm = sm.tmem;
+    // tensor memory: dS 0-127, dS hi 128, lo 192, X (then dU hi, lo) 256, dO^T A 320, dY (then
+    // -w e^G dY hi, lo) 384, e^G dO hi, lo 448
+    constexpr uint32_t cHi = 128, cLo = 192, cX = 256, cP = 320, cY = 384, cD = 448;
+    bool ok = true;
+    auto wait = [&](uint64_t &bar, int phase) {   // by a whole warp
+        return (bool)__all_sync(0xffffffffu, mbar_wait(&bar, phase & 1, kSwaWait));
+    };
+
+    if (warp == 8) {
+        int i = 0;
+        for (; i < chunks; ++i) {
+            const int s = i & 1, c = chunks - 1 - i;
+            if (i >= 2) ok = wait(sm.free[s], i / 2 - 1);
+            if (!ok) break;
+            if (lane == 0) {
+                const int row = (int)(row0 + (long long)c * kC);
+                mbar_expect_tx(&sm.full[s], 2 * kC * K * 2 + kC * V * 2 + sizeof(GdrPrep));
+                for (int x = 0; x < VH; ++x) tma_load_3d(sm.dO[s][x], &md, 64 * x, h, row, &sm.full[s]);
+                bulk_g2s(&sm.p[s], reinterpret_cast<const GdrPrep *>(a.prep) + (size_t)(t0 + c) * a.Hv + h, sizeof(GdrPrep),
+                         &sm.full[s]);
+                for (int x = 0; x < KH; ++x) tma_load_3d(sm.k[s][x], &mk, 64 * x, hk, row, &sm.full[s]);
+                for (int x = 0; x < KH; ++x) tma_load_3d(sm.q[s][x], &mq, 64 * x, hk, row, &sm.full[s]);
+            }
+        }
+        if (!ok)
+            for (int j = max(0, i - 2); j < i; ++j) wait(sm.full[j & 1], j / 2);
+    } else if (warp == 9) {
+        constexpr uint32_t iN64 = umma_idesc_bf16(128, 64), iS = umma_idesc_bf16(128, K) | kUmmaBmn;
+        for (int i = 0; i < chunks; ++i) {
+            const int s = i & 1, c = chunks - 1 - i;
+            if (!(ok = wait(sm.full[s], i / 2))) break;
+            if (len - c * kC < kC) {   // rows behind the end meet zero factors, so they have to be finite
+                zero_rows(sm.k[s], len - c * kC, KH, kTile64, lane);
+                zero_rows(sm.q[s], len - c * kC, KH, kTile64, lane);
+                zero_rows(sm.dO[s], len - c * kC, VH, kTile64, lane);
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            if (lane == 0) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    umma_bf16(tm + cP, umma_desc_mn(smem_u32(sm.dO[s][0]) + 2048 * kk, kTile64),
+                              umma_desc_mn(smem_u32(sm.p[s].A) + 2048 * kk, kTile64), iN64 | kUmmaAmn | kUmmaBmn, kk > 0);
+            }
+            __syncwarp();
+            if (!(ok = wait(sm.sready, i))) break;
+            tc_fence_after_sync();
+            if (lane == 0) {
+#pragma unroll
+                for (int lo = 0; lo < 2; ++lo)
+#pragma unroll
+                    for (int kk = 0; kk < K / 16; ++kk)
+                        umma_bf16_ta(tm + cX, tm + (lo ? cLo : cHi) + 8 * kk, umma_desc(smem_u32(sm.k[s][kk / 4]) + 32 * (kk % 4)),
+                                     iN64, lo > 0 || kk > 0);
+                umma_commit(&sm.gfull);
+            }
+            __syncwarp();
+            if (!(ok = wait(sm.dready, i))) break;
+            tc_fence_after_sync();
+            if (lane == 0) {
+#pragma unroll
+                for (int lo = 0; lo < 2; ++lo)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_bf16_ta(tm, tm + cD + half_col(kk) + 16 * lo, umma_desc_mn(smem_u32(sm.q[s][0]) + 2048 * kk, kTile64),
+                                     iS, 1);
+            }
+            __syncwarp();
+            if (!(ok = wait(sm.uready, i))) break;
+            tc_fence_after_sync();
+            if (lane == 0) {
+                const uint32_t th = smem_u32(sm.p[s].t_hi), tl = smem_u32(sm.p[s].t_lo);
+#pragma unroll
+                for (int x = 0; x < 3; ++x)   // dU hi Tm hi, dU lo Tm hi, dU hi Tm lo
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_bf16_ta(tm + cY, tm + cX + half_col(kk) + (x == 1 ? 16 : 0),
+                                     umma_desc_mn((x == 2 ? tl : th) + 2048 * kk, kTile64), iN64 | kUmmaBmn, x > 0 || kk > 0);
+                umma_commit(&sm.yfull);
+            }
+            __syncwarp();
+            if (!(ok = wait(sm.yready, i))) break;
+            tc_fence_after_sync();
+            if (lane == 0) {
+#pragma unroll
+                for (int lo = 0; lo < 2; ++lo)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_bf16_ta(tm, tm + cY + half_col(kk) + 16 * lo, umma_desc_mn(smem_u32(sm.k[s][0]) + 2048 * kk, kTile64),
+                                     iS, 1);
+                umma_commit(&sm.sfull);
+                umma_commit(&sm.free[s]);
+            }
+            __syncwarp();
+        }
+        if (lane == 0) umma_commit(&sm.drain);   // products in flight finish before the tensor memory is freed
+        __syncwarp();
+        wait(sm.drain, 0);
+    } else if (warp == 10) {
+        typedef GdrKeep<K, V> Keep;
+        Keep *keep = reinterpret_cast<Keep *>(a.ws) + (size_t)t0 * a.Hv + h;
+        for (int i = 0; i < chunks && ok; ++i) {
+            const int c = chunks - 1 - i;
+            if (!(ok = wait(sm.Sout, i))) break;
+            if (lane == 0) {
+                bulk_s2g(keep[(size_t)c * a.Hv].S, sm.S, sizeof(sm.S));
+                bulk_commit();
+                bulk_wait_read<0>();
+                mbar_arrive(&sm.Sfree);
+            }
+            __syncwarp();
+            if (!(ok = wait(sm.yout, i))) break;
+            if (lane == 0) bulk_s2g(keep[(size_t)c * a.Hv].x, sm.y, sizeof(sm.y));
+            for (int t = lane; t < min(kC, len - c * kC); t += 32)
+                bulk_s2g(static_cast<__nv_bfloat16 *>(a.dv) + ((size_t)(row0 + (long long)c * kC + t) * a.Hv + h) * V,
+                         sm.dv + t * V, V * 2);
+            bulk_commit();
+            bulk_wait_read<0>();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.yfree);
+        }
+        bulk_wait<0>();
+    } else {
+        const int half = warp / 4, quarter = warp % 4, r = quarter * 32 + lane;
+        const uint32_t tl = tm + ((uint32_t)quarter << 21);
+        const int x0 = half * (K / 2), c32 = half * 32;   // this thread's columns of dS, its tokens
+        const bool live = r < V;                          // value row (others carry zeros)
+        const size_t st = (((size_t)n * a.Hv + h) * V + (live ? r : 0)) * K + x0;
+        float S[K / 2];
+#pragma unroll
+        for (int x = 0; x < K / 2; x += 4) {
+            const float4 y = live && a.dS_final ? *reinterpret_cast<const float4 *>(a.dS_final + st + x) : make_float4(0.f, 0.f, 0.f, 0.f);
+            S[x] = y.x;
+            S[x + 1] = y.y;
+            S[x + 2] = y.z;
+            S[x + 3] = y.w;
+        }
+        for (int i = 0; i < chunks && ok; ++i) {
+            const int s = i & 1, c = chunks - 1 - i, m = min(kC, len - c * kC);
+            const GdrPrep &p = sm.p[s];
+            // dS1 as operands, the accumulator scaled by e^{G_C}
+            if (!(ok = wait(sm.full[s], i / 2))) break;
+            {
+                const float gl = p.eG[kC - 1];
+                uint32_t hi[K / 4], lo[K / 4], sc[K / 2];
+#pragma unroll
+                for (int x = 0; x < K / 4; ++x) split_pair(S[2 * x], S[2 * x + 1], hi[x], lo[x]);
+#pragma unroll
+                for (int x = 0; x < K / 2; ++x) sc[x] = __float_as_uint(S[x] * gl);
+#pragma unroll
+                for (int x = 0; x < K / 4; x += 16) {
+                    tmem_st16(tl + cHi + x0 / 2 + x, hi + x);
+                    tmem_st16(tl + cLo + x0 / 2 + x, lo + x);
+                }
+#pragma unroll
+                for (int x = 0; x < K / 2; x += 32) tmem_st32(tl + x0 + x, sc + x);
+                tmem_wait_st();
+                tc_fence_before_sync();
+                mbar_arrive(&sm.sready);
+                if (i > 0 && !(ok = wait(sm.Sfree, i - 1))) break;
+                if (live)
+#pragma unroll
+                    for (int x = 0; x < K / 4; x += 4)
+                        *reinterpret_cast<uint4 *>(sm.S + op_off(r, x0 + 2 * x, V)) = make_uint4(hi[x], hi[x + 1], hi[x + 2], hi[x + 3]);
+                fence_proxy_async_smem();
+                mbar_arrive(&sm.Sout);
+            }
+            uint32_t x[32], y[16], z[16];
+            // e^G dO, transposed
+            const __nv_bfloat16 *dO = sm.dO[s][0];
+#pragma unroll
+            for (int t = 0; t < 32; t += 2) {
+                float g[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    g[e] = c32 + t + e < m && live ? p.eG[c32 + t + e] * __bfloat162float(dO[op_off(c32 + t + e, r, kC)]) : 0.f;
+                split_pair(g[0], g[1], y[t / 2], z[t / 2]);
+            }
+            tmem_st16(tl + cD + c32, y);
+            tmem_st16(tl + cD + c32 + 16, z);
+            tmem_wait_st();
+            tc_fence_before_sync();
+            mbar_arrive(&sm.dready);
+            // dU
+            if (!(ok = wait(sm.gfull, i))) break;
+            tc_fence_after_sync();
+            uint32_t pa[32];
+            tmem_ld32(tl + cX + c32, x);
+            tmem_ld32(tl + cP + c32, pa);
+            tmem_wait_ld();
+            tmem_tie(x);
+            tmem_tie(pa);
+#pragma unroll
+            for (int t = 0; t < 32; t += 2) {
+                const float u0 = __uint_as_float(pa[t]) + p.eK[c32 + t] * __uint_as_float(x[t]);
+                const float u1 = __uint_as_float(pa[t + 1]) + p.eK[c32 + t + 1] * __uint_as_float(x[t + 1]);
+                split_pair(u0, u1, y[t / 2], z[t / 2]);
+            }
+            tmem_st16(tl + cX + c32, y);   // over the columns of X that this thread has read
+            tmem_st16(tl + cX + c32 + 16, z);
+            tmem_wait_st();
+            tc_fence_before_sync();
+            mbar_arrive(&sm.uready);
+            // dY
+            if (!(ok = wait(sm.yfull, i))) break;
+            tc_fence_after_sync();
+            tmem_ld32(tl + cY + c32, x);
+            tmem_wait_ld();
+            tmem_tie(x);
+#pragma unroll
+            for (int t = 0; t < 32; t += 2)
+                split_pair(-p.w[c32 + t] * p.eG[c32 + t] * __uint_as_float(x[t]),
+                           -p.w[c32 + t + 1] * p.eG[c32 + t + 1] * __uint_as_float(x[t + 1]), y[t / 2], z[t / 2]);
+            tmem_st16(tl + cY + c32, y);
+            tmem_st16(tl + cY + c32 + 16, z);
+            tmem_wait_st();
+            tc_fence_before_sync();
+            float w[32];   // (the stage may be refilled after the arrival)
+#pragma unroll
+            for (int t = 0; t < 32; ++t) w[t] = p.w[c32 + t];
+            mbar_arrive(&sm.yready);
+            if (i > 0 && !(ok = wait(sm.yfree, i - 1))) break;
+            if (live)
+#pragma unroll
+                for (int t = 0; t < 32; ++t) {
+                    const float dy = __uint_as_float(x[t]);
+                    sm.y[op_off(c32 + t, r, kC)] = __float2bfloat16_rn(dy);
+                    sm.dv[(c32 + t) * V + r] = __float2bfloat16_rn(w[t] * dy);
+                }
+            fence_proxy_async_smem();
+            mbar_arrive(&sm.yout);
+            // dS0
+            if (!(ok = wait(sm.sfull, i))) break;
+            tc_fence_after_sync();
+#pragma unroll
+            for (int x = 0; x < K / 2; x += 32) tmem_ld32(tl + x0 + x, reinterpret_cast<uint32_t *>(S) + x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < K / 2; x += 32) tmem_tie(reinterpret_cast<uint32_t *>(S) + x);
+        }
+        if (ok && a.dS0 && live)
+#pragma unroll
+            for (int x = 0; x < K / 2; x += 4)
+                *reinterpret_cast<float4 *>(a.dS0 + st + x) = make_float4(S[x], S[x + 1], S[x + 2], S[x + 3]);
+    }
+    if (!ok && lane == 0) atomicOr(&g_gdr_bwd_timeout, 1);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    if (warp == 9) tmem_dealloc(tm, 512);
+}
+
+template <int K, int V>
+struct GradSmem {
+    __nv_bfloat16 d[2][V / 64][192 * 64];   // [stage]: dO, dY, U
+    __nv_bfloat16 S0[V * K], S1[V * K];     // S0, dS1
+    __nv_bfloat16 qk[K / 64][128 * 64];     // Q, K
+    __nv_bfloat16 P[192 * 64];              // zeros, P1, P2
+    float vec[2][4][kC];                    // [stage]: e^G, e^{G_C - G}, w, G
+    float dg[2][128], dw[2][kC], kb[2][kC], tot[128], col[8][32], last[4];   // partial sums of a head
+    uint64_t qkfull, qkfree, dfull[2], dfree[2], s0full, s0free, s1full, s1free, Dfull, Dfree, xfull, xfree, yfull, yfree,
+        pready, pfull, afree, gready, gfree, drain;
+    uint32_t tmem;
+};
+
+// sum of the products of eight bf16 pairs
+__device__ __forceinline__ float dot8(uint4 a, uint4 b, float acc) {
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        acc = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), acc);
+        acc = fmaf(__uint_as_float(x[i] & 0xffff0000u), __uint_as_float(y[i] & 0xffff0000u), acc);
+    }
+    return acc;
+}
+
+// lane l returns the sum over the warp's lanes of their x[l]
+__device__ __forceinline__ float column_sum(float (&x)[32], int lane) {
+#pragma unroll
+    for (int w = 16; w >= 1; w >>= 1) {
+        const bool up = lane & w;
+#pragma unroll
+        for (int i = 0; i < w; ++i) {
+            const float keep = up ? x[i + w] : x[i], give = up ? x[i] : x[i + w];
+            x[i] = keep + __shfl_xor_sync(0xffffffffu, give, w);
+        }
+    }
+    return x[0];
+}
+
+template <int K, int V>
+__global__ void __launch_bounds__(352, 1)
+    gdr_tc_grad(GdrArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                const __grid_constant__ CUtensorMap md) {
+    extern __shared__ __align__(16) unsigned char raw[];
+    typedef GradSmem<K, V> Smem;
+    typedef GdrKeep<K, V> Keep;
+    Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    constexpr int KH = K / 64, VH = V / 64;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, share = a.Hv / a.Hk;
+    if (threadIdx.x == 0) {
+        for (uint64_t *b : {&sm.qkfull, &sm.dfull[0], &sm.dfull[1], &sm.s0full, &sm.s1full, &sm.Dfull, &sm.xfull, &sm.yfull,
+                            &sm.pfull, &sm.gfree, &sm.drain})
+            mbar_init(b, 1);
+        for (uint64_t *b : {&sm.Dfree, &sm.xfree, &sm.pready, &sm.afree, &sm.gready}) mbar_init(b, 256);
+        for (uint64_t *b : {&sm.qkfree, &sm.dfree[0], &sm.dfree[1]}) mbar_init(b, 257);   // readers and the products
+        for (uint64_t *b : {&sm.s0free, &sm.s1free}) mbar_init(b, 129);
+        mbar_init(&sm.yfree, 128);
+        fence_mbar_init();
+    }
+    for (int i = threadIdx.x; i < kC * 8; i += blockDim.x) reinterpret_cast<uint4 *>(sm.P)[i] = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+    if (warp == 9) tmem_alloc(&sm.tmem, 512);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tm = sm.tmem;
+    constexpr uint32_t cX = 0, cY = 128, cA = 256, cD = 384, cKK = 448;
+    bool ok = true;
+    auto wait = [&](uint64_t &bar, int phase) {   // by a whole warp
+        return (bool)__all_sync(0xffffffffu, mbar_wait(&bar, phase & 1, kSwaWait));
+    };
+    const long long items = a.seq.n_tiles(kC) * a.Hk;
+    int it = 0, j = 0;   // items and heads so far (those of used tiles)
+
+    if (warp == 8) {
+        for (long long w = blockIdx.x; w < items && ok; w += gridDim.x) {
+            const int tile = (int)(w / a.Hk), hk = (int)(w % a.Hk);
+            int n, c, len;
+            long long row;
+            if (!a.seq.find(tile, kC, n, c, row, len)) continue;
+            row += (long long)c * kC;
+            for (int g = 0; g < share && ok; ++g, ++j) {
+                const int s = j & 1, h = hk * share + g;
+                const size_t slot = (size_t)tile * a.Hv + h;
+                const Keep *fwd = reinterpret_cast<const Keep *>(a.saved) + slot, *bwd = reinterpret_cast<const Keep *>(a.ws) + slot;
+                if (j >= 2 && !(ok = wait(sm.dfree[s], j / 2 - 1))) break;
+                if (lane == 0) {
+                    mbar_expect_tx(&sm.dfull[s], 3 * kC * V * 2 + sizeof(sm.vec[0]));
+                    bulk_g2s(sm.vec[s], reinterpret_cast<const GdrPrep *>(a.prep)[slot].eG, sizeof(sm.vec[0]), &sm.dfull[s]);
+                    for (int x = 0; x < VH; ++x) {
+                        tma_load_3d(sm.d[s][x], &md, 64 * x, h, (int)row, &sm.dfull[s]);
+                        bulk_g2s(sm.d[s][x] + kC * 64, bwd->x + x * kC * 64, kTile64, &sm.dfull[s]);
+                        bulk_g2s(sm.d[s][x] + 2 * kC * 64, fwd->x + x * kC * 64, kTile64, &sm.dfull[s]);
+                    }
+                }
+                __syncwarp();
+                if (g == 0) {
+                    if (it > 0 && !(ok = wait(sm.qkfree, it - 1))) break;
+                    if (lane == 0) {
+                        mbar_expect_tx(&sm.qkfull, 2 * kC * K * 2);
+                        for (int x = 0; x < KH; ++x) {
+                            tma_load_3d(sm.qk[x], &mq, 64 * x, hk, (int)row, &sm.qkfull);
+                            tma_load_3d(sm.qk[x] + kC * 64, &mk, 64 * x, hk, (int)row, &sm.qkfull);
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (j > 0 && !(ok = wait(sm.s0free, j - 1))) break;
+                if (lane == 0) {
+                    mbar_expect_tx(&sm.s0full, sizeof(sm.S0));
+                    bulk_g2s(sm.S0, fwd->S, sizeof(sm.S0), &sm.s0full);
+                }
+                __syncwarp();
+                if (j > 0 && !(ok = wait(sm.s1free, j - 1))) break;
+                if (lane == 0) {
+                    mbar_expect_tx(&sm.s1full, sizeof(sm.S1));
+                    bulk_g2s(sm.S1, bwd->S, sizeof(sm.S1), &sm.s1full);
+                }
+                __syncwarp();
+            }
+            ++it;
+        }
+        // every copy has landed before the memory is given back (those not issued wait in vain, with a limit)
+        if (!ok) {
+            for (int i = max(0, j - 1); i <= j; ++i) wait(sm.dfull[i & 1], i / 2);
+            wait(sm.qkfull, it);
+            wait(sm.s0full, j);
+            wait(sm.s1full, j);
+        }
+    } else if (warp == 9) {
+        constexpr uint32_t iN64 = umma_idesc_bf16(128, 64), iK = umma_idesc_bf16(128, K) | kUmmaBmn;
+        const uint32_t P = smem_u32(sm.P), qk = smem_u32(sm.qk[0]);
+        for (long long w = blockIdx.x; w < items && ok; w += gridDim.x) {
+            const int tile = (int)(w / a.Hk);
+            int n, c, len;
+            long long row;
+            if (!a.seq.find(tile, kC, n, c, row, len)) continue;
+            for (int g = 0; g < share && ok; ++g, ++j) {
+                const int s = j & 1;
+                if (g == 0) {
+                    if (!(ok = wait(sm.qkfull, it))) break;
+                    if (len - c * kC < kC) {   // rows behind the end meet zero factors, so they have to be finite
+                        zero_rows(sm.qk[0], len - c * kC, KH, 2 * kTile64, lane);
+                        zero_rows(sm.qk[0] + kC * 64, len - c * kC, KH, 2 * kTile64, lane);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                }
+                if (j > 0 && !(ok = wait(sm.Dfree, j - 1))) break;
+                tc_fence_after_sync();
+                if (g == 0 && lane == 0) {
+#pragma unroll
+                    for (int kk = 0; kk < K / 16; ++kk) {
+                        const uint32_t x = qk + 2 * kTile64 * (kk / 4) + 32 * (kk % 4);
+                        umma_bf16(tm + cKK, umma_desc(x), umma_desc(x + kTile64), iN64, kk > 0);
+                    }
+                }
+                __syncwarp();
+                if (!(ok = wait(sm.dfull[s], j / 2))) break;
+                const uint32_t d = smem_u32(sm.d[s][0]);
+                if (lane == 0) {
+#pragma unroll
+                    for (int kk = 0; kk < V / 16; ++kk) {
+                        const uint32_t x = d + 3 * kTile64 * (kk / 4) + 32 * (kk % 4);
+                        umma_bf16(tm + cD, umma_desc(x), umma_desc(x + 2 * kTile64), iN64, kk > 0);
+                    }
+                    umma_commit(&sm.Dfull);
+                }
+                __syncwarp();
+                if (!(ok = wait(sm.s0full, j))) break;
+                if (j > 0 && !(ok = wait(sm.xfree, j - 1))) break;
+                tc_fence_after_sync();
+                if (lane == 0) {
+#pragma unroll
+                    for (int kk = 0; kk < V / 16; ++kk)
+                        umma_bf16(tm + cX, umma_desc(d + 3 * kTile64 * (kk / 4) + 32 * (kk % 4)),
+                                  umma_desc_mn(smem_u32(sm.S0) + 2048 * kk, V * 128), iK, kk > 0);
+                    umma_commit(&sm.xfull);
+                    umma_commit(&sm.s0free);
+                }
+                __syncwarp();
+                if (!(ok = wait(sm.s1full, j))) break;
+                if (j > 0 && !(ok = wait(sm.yfree, j - 1))) break;
+                tc_fence_after_sync();
+                if (lane == 0) {
+#pragma unroll
+                    for (int kk = 0; kk < V / 16; ++kk)   // [dY; U] dS1, of which the lanes of U count
+                        umma_bf16(tm + cY, umma_desc(d + kTile64 + 3 * kTile64 * (kk / 4) + 32 * (kk % 4)),
+                                  umma_desc_mn(smem_u32(sm.S1) + 2048 * kk, V * 128), iK, kk > 0);
+                    umma_commit(&sm.yfull);
+                    umma_commit(&sm.s1free);
+                    umma_commit(&sm.dfree[s]);
+                }
+                __syncwarp();
+                if (!(ok = wait(sm.pready, j))) break;
+                if (g == 0 && it > 0 && !(ok = wait(sm.afree, it - 1))) break;
+                tc_fence_after_sync();
+                if (lane == 0) {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)   // [P1; P2] K
+                        umma_bf16(tm + cA, umma_desc(P + kTile64 + 32 * kk), umma_desc_mn(qk + kTile64 + 2048 * kk, 2 * kTile64), iK,
+                                  g > 0 || kk > 0);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)   // [0; P1^T] Q
+                        umma_bf16(tm + cA, umma_desc_mn(P + 2048 * kk, kTile64), umma_desc_mn(qk + 2048 * kk, 2 * kTile64),
+                                  iK | kUmmaAmn, 1);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)   // [0; P2^T] K
+                        umma_bf16(tm + cA, umma_desc_mn(P + 2048 * kk, 2 * kTile64),
+                                  umma_desc_mn(qk + kTile64 + 2048 * kk, 2 * kTile64), iK | kUmmaAmn, 1);
+                    umma_commit(&sm.pfull);
+                    if (g == share - 1) umma_commit(&sm.qkfree);
+                }
+                __syncwarp();
+            }
+            ++it;
+        }
+        if (lane == 0) umma_commit(&sm.drain);
+        __syncwarp();
+        wait(sm.drain, 0);
+    } else if (warp == 10) {
+        // gate gradients from the partial sums: lane = tokens lane and lane + 32.  The gradient of log a_t
+        // is the sum over every path that crosses the decay of token t, each term as it is (rows minus
+        // columns of a cumulative sum would cancel): queries and keys r >= t that read the start state,
+        // keys s < t that reach the end, S0 itself, and pairs r >= t > s.
+        float *part = a.dA_dec || a.dtau ? reinterpret_cast<float *>(a.ws + (size_t)a.seq.n_tiles(kC) * a.Hv * sizeof(Keep)) : nullptr;
+        for (long long wk = blockIdx.x; wk < items && ok; wk += gridDim.x) {
+            const int tile = (int)(wk / a.Hk), hk = (int)(wk % a.Hk);
+            int n, c, len;
+            long long row;
+            if (!a.seq.find(tile, kC, n, c, row, len)) {
+                if (part)   // unused numbers count as zero in the fixed-order sums
+                    for (int i = lane; i < 2 * share; i += 32) part[((size_t)tile * a.Hv + hk * share) * 2 + i] = 0.f;
+                continue;
+            }
+            row += (long long)c * kC;
+            const int m = min(kC, len - c * kC);
+            for (int g = 0; g < share && ok; ++g, ++j) {
+                const int h = hk * share + g;
+                const float amp = decay_amp(a.A_dec, h), bias = a.tau ? a.tau[h] : 0.f;
+                float x[2], w[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int t = lane + 32 * e;
+                    const size_t at = (size_t)(row + (t < m ? t : 0)) * a.Hv + h;
+                    x[e] = ld_io(static_cast<const __nv_bfloat16 *>(a.g_logit) + at) + bias;
+                    w[e] = sigmoid_f(ld_io(static_cast<const __nv_bfloat16 *>(a.w_logit) + at));
+                }
+                if (!(ok = wait(sm.gready, j))) break;
+                float G[2], B[2], dw[2], T[2], C[2];   // row sums; sums of key rows; ...; pairs: row totals of s < 32, columns
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int t = lane + 32 * e;
+                    G[e] = sm.dg[0][t] + sm.dg[1][t] + sm.dg[0][t + 64] + sm.dg[1][t + 64];
+                    B[e] = sm.kb[0][t] + sm.kb[1][t];
+                    dw[e] = sm.dw[0][t] + sm.dw[1][t];
+                    T[e] = sm.tot[t] + sm.tot[t + 64];
+                    C[e] = sm.col[4 * e][lane] + sm.col[4 * e + 1][lane] + sm.col[4 * e + 2][lane] + sm.col[4 * e + 3][lane];
+                }
+                const float last = sm.last[0] + sm.last[1] + sm.last[2] + sm.last[3];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.gfree);
+                // suffix sums of G (over 64) and of T (over its upper half), exclusive prefix of B
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const float g0 = __shfl_down_sync(0xffffffffu, G[0], off), g1 = __shfl_down_sync(0xffffffffu, G[1], off);
+                    const float t1 = __shfl_down_sync(0xffffffffu, T[1], off);
+                    const float b0 = __shfl_up_sync(0xffffffffu, B[0], off), b1 = __shfl_up_sync(0xffffffffu, B[1], off);
+                    if (lane + off < 32) {
+                        G[0] += g0;
+                        G[1] += g1;
+                        T[1] += t1;
+                    }
+                    if (lane >= off) {
+                        B[0] += b0;
+                        B[1] += b1;
+                    }
+                }
+                const float all1 = __shfl_sync(0xffffffffu, G[1], 0), all0 = __shfl_sync(0xffffffffu, B[0], 31);
+                float b0 = __shfl_up_sync(0xffffffffu, B[0], 1), b1 = __shfl_up_sync(0xffffffffu, B[1], 1);
+                b0 = lane ? b0 : 0.f;
+                b1 = (lane ? b1 : 0.f) + all0;
+                const float gr[2] = {G[0] + all1 + b0 + last + C[0], G[1] + b1 + last + C[1] + T[1]};
+                float dlog = 0.f, damp = 0.f;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int t = lane + 32 * e;
+                    if (t < m) {
+                        const size_t at = (size_t)(row + t) * a.Hv + h;
+                        const float dl = -amp * sigmoid_f(x[e]) * gr[e];
+                        dlog += dl;
+                        damp += -amp * softplus_f(x[e]) * gr[e];
+                        st_io(static_cast<__nv_bfloat16 *>(a.dg_logit) + at, dl);
+                        st_io(static_cast<__nv_bfloat16 *>(a.dw_logit) + at, dw[e] * w[e] * (1.f - w[e]));
+                    }
+                }
+                if (part) {
+#pragma unroll
+                    for (int off = 16; off >= 1; off >>= 1) {
+                        dlog += __shfl_xor_sync(0xffffffffu, dlog, off);
+                        damp += __shfl_xor_sync(0xffffffffu, damp, off);
+                    }
+                    if (lane == 0) {
+                        part[((size_t)tile * a.Hv + h) * 2] = damp;
+                        part[((size_t)tile * a.Hv + h) * 2 + 1] = dlog;
+                    }
+                }
+            }
+        }
+    } else {
+        const int half = warp / 4, quarter = warp % 4, r = quarter * 32 + lane, t = r % kC;
+        const bool key = r >= kC;   // lane of a key (the same for a whole warp)
+        const uint32_t tl = tm + ((uint32_t)quarter << 21);
+        const int x0 = half * (K / 2), s0 = half * 32, v0 = half * (V / 2);
+        float acc[K / 2];
+        for (long long wk = blockIdx.x; wk < items && ok; wk += gridDim.x) {
+            const int tile = (int)(wk / a.Hk), hk = (int)(wk % a.Hk);
+            int n, c, len;
+            long long row;
+            if (!a.seq.find(tile, kC, n, c, row, len)) continue;
+            row += (long long)c * kC;
+            const int m = min(kC, len - c * kC);
+            const bool here = t < m;
+#pragma unroll
+            for (int x = 0; x < K / 2; ++x) acc[x] = 0.f;
+            for (int g = 0; g < share && ok; ++g, ++j) {
+                const int s = j & 1, h = hk * share + g;
+                uint4 v[V / 16];   // this key's values, half of the channels
+#pragma unroll
+                for (int i = 0; i < V / 16; ++i)
+                    v[i] = key && here ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.v) +
+                                                                              ((size_t)(row + t) * a.Hv + h) * V + v0) + i)
+                                       : make_uint4(0u, 0u, 0u, 0u);
+                if (!(ok = wait(sm.dfull[s], j / 2))) break;
+                const float *eG = sm.vec[s][0], *eK = sm.vec[s][1], *vw = sm.vec[s][2], *G = sm.vec[s][3];
+                const float wt = vw[t];
+                float dw = 0.f, dg, kb = 0.f, run = 0.f;
+                // pairs of the chunk
+                if (!(ok = wait(sm.Dfull, j))) break;
+                tc_fence_after_sync();
+                {
+                    uint32_t D[32], kk[32], p[16];
+                    tmem_ld32(tl + cD + s0, D);
+                    tmem_ld32(tl + cKK + s0, kk);
+                    tmem_wait_ld();
+                    tmem_tie(D);
+                    tmem_tie(kk);
+                    tc_fence_before_sync();
+                    mbar_arrive(&sm.Dfree);
+                    const float Gt = G[t];
+                    float pr[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const int u = s0 + e;
+                        const bool below = here && u < t;
+                        float y = below || (here && !key && u == t) ? __expf(Gt - G[u]) * __uint_as_float(D[e]) : 0.f;
+                        const float b = below ? __uint_as_float(kk[e]) : 0.f;
+                        if (key) {
+                            y = -y;
+                            dw = fmaf(y, b, dw);
+                            y *= wt;
+                        }
+                        pr[e] = y * b;
+                        D[e] = __float_as_uint(y);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) p[e] = pack_bf16(__uint_as_float(D[2 * e]), __uint_as_float(D[2 * e + 1]));
+                    if (j > 0 && !(ok = wait(sm.pfull, j - 1))) break;
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4)
+                        *reinterpret_cast<uint4 *>(sm.P + kC * 64 + op_off(r, s0 + 2 * e, 128)) = make_uint4(p[e], p[e + 1], p[e + 2], p[e + 3]);
+                    fence_proxy_async_smem();
+                    mbar_arrive(&sm.pready);
+                    // sums over s before u, for u up to t; then over the warp's tokens
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const float y = pr[e];
+                        pr[e] = s0 + e <= t ? run : 0.f;
+                        run += y;
+                    }
+                    const float cs = column_sum(pr, lane);
+                    if (j > 0 && !(ok = wait(sm.gfree, j - 1))) break;
+                    sm.col[warp][lane] = cs;
+                    if (half == 0) sm.tot[r] = run;
+                }
+                // start state
+                if (!(ok = wait(sm.xfull, j))) break;
+                tc_fence_after_sync();
+                {
+                    uint32_t x[K / 2];
+#pragma unroll
+                    for (int i = 0; i < K / 2; i += 32) tmem_ld32(tl + cX + x0 + i, x + i);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < K / 2; i += 32) tmem_tie(x + i);
+                    tc_fence_before_sync();
+                    mbar_arrive(&sm.xfree);
+                    const float f = eG[t], f2 = key ? -wt : 1.f;
+                    float d = 0.f;
+#pragma unroll
+                    for (int i = 0; i < K / 2; i += 8) {
+                        const uint4 y = *reinterpret_cast<const uint4 *>(sm.qk[0] + op_off(r, x0 + i, 128));
+                        const uint32_t yy[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float z = here ? f * __uint_as_float(x[i + e]) : 0.f;
+                            const float b = __uint_as_float(e % 2 ? yy[e / 2] & 0xffff0000u : yy[e / 2] << 16);
+                            d = fmaf(z, here ? b : 0.f, d);
+                            acc[i + e] = fmaf(f2, z, acc[i + e]);
+                        }
+                    }
+                    dg = f2 * d;
+                    dw -= d;
+                }
+                if (key) {   // end state; the values
+                    if (!(ok = wait(sm.yfull, j))) break;
+                    tc_fence_after_sync();
+                    uint32_t x[K / 2];
+#pragma unroll
+                    for (int i = 0; i < K / 2; i += 32) tmem_ld32(tl + cY + x0 + i, x + i);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < K / 2; i += 32) tmem_tie(x + i);
+                    tc_fence_before_sync();
+                    mbar_arrive(&sm.yfree);
+                    const float f = here ? eK[t] : 0.f;
+#pragma unroll
+                    for (int i = 0; i < K / 2; i += 8) {
+                        const uint4 y = *reinterpret_cast<const uint4 *>(sm.qk[0] + op_off(r, x0 + i, 128));
+                        const uint32_t yy[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float z = f * __uint_as_float(x[i + e]);
+                            const float b = __uint_as_float(e % 2 ? yy[e / 2] & 0xffff0000u : yy[e / 2] << 16);
+                            kb = fmaf(z, here ? b : 0.f, kb);
+                            acc[i + e] += z;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < V / 16; ++i)
+                        dw = dot8(*reinterpret_cast<const uint4 *>(sm.d[s][0] + op_off(r, v0 + 8 * i, 192)), v[i], dw);
+                    sm.dw[half][t] = dw;
+                    sm.kb[half][t] = kb;
+                } else {   // <S0, dS1>: both are laid out alike
+                    if (!(ok = wait(sm.s0full, j))) break;
+                    if (!(ok = wait(sm.s1full, j))) break;
+                    const int at = half * 64 + quarter * 32 + lane;
+                    float y = 0.f;
+#pragma unroll 4
+                    for (int i = at; i < V * K / 8; i += 128)
+                        y = dot8(reinterpret_cast<const uint4 *>(sm.S0)[i], reinterpret_cast<const uint4 *>(sm.S1)[i], y);
+                    mbar_arrive(&sm.s0free);
+                    mbar_arrive(&sm.s1free);
+#pragma unroll
+                    for (int off = 16; off >= 1; off >>= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
+                    if (lane == 0) sm.last[half * 2 + quarter] = y * eG[kC - 1];
+                }
+                sm.dg[half][r] = dg;
+                mbar_arrive(&sm.gready);
+                mbar_arrive(&sm.dfree[s]);
+                if (g == share - 1) mbar_arrive(&sm.qkfree);
+            }
+            if (!ok) break;
+            if (!(ok = wait(sm.pfull, j - 1))) break;
+            tc_fence_after_sync();
+            uint32_t x[K / 2];
+#pragma unroll
+            for (int i = 0; i < K / 2; i += 32) tmem_ld32(tl + cA + x0 + i, x + i);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < K / 2; i += 32) tmem_tie(x + i);
+            tc_fence_before_sync();
+            mbar_arrive(&sm.afree);
+            if (here) {
+                uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(key ? a.dk : a.dq) +
+                                                       ((size_t)(row + t) * a.Hk + hk) * K + x0);
+#pragma unroll
+                for (int i = 0; i < K / 2; i += 8) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2)
+                        o[e / 2] = pack_bf16(acc[i + e] + __uint_as_float(x[i + e]), acc[i + e + 1] + __uint_as_float(x[i + e + 1]));
+                    out[i / 8] = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+            }
+            ++it;
+        }
+    }
+    if (!ok && lane == 0) atomicOr(&g_gdr_bwd_timeout, 1);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    if (warp == 9) tmem_dealloc(tm, 512);
+}
+
+template <int K, int V>
+cudaError_t bwd_t(const GdrArgs &a, cudaStream_t st) {
+    const long long rows = a.seq.cu ? a.seq.total : (long long)a.seq.N * a.seq.T;
+    CUtensorMap mq{}, mk{}, md{};
+    auto sweep = gdr_tc_bsweep<K, V>;
+    auto grad = gdr_tc_grad<K, V>;
+    const int sb = (int)sizeof(BsweepSmem<K, V>) + 1024, gb = (int)sizeof(GradSmem<K, V>) + 1024;
+    cudaError_t e = set_smem_once(reinterpret_cast<const void *>(sweep), sb);
+    if (e == cudaSuccess) e = set_smem_once(reinterpret_cast<const void *>(grad), gb);
+    if (rows > 0) {   // without rows no tile is copied; the sweep hands the states on
+        if (e == cudaSuccess) e = make_operand_tile_map(&mq, a.q, K, a.Hk, rows, kC);
+        if (e == cudaSuccess) e = make_operand_tile_map(&mk, a.k, K, a.Hk, rows, kC);
+        if (e == cudaSuccess) e = make_operand_tile_map(&md, a.dO, V, a.Hv, rows, kC);
+    }
+    if (e != cudaSuccess) return e;
+    sweep<<<a.seq.N * a.Hv, 352, sb, st>>>(a, mq, mk, md);
+    const long long tiles = a.seq.n_tiles(kC), items = tiles * a.Hk;
+    if (items) grad<<<(unsigned)(items < sm_count() ? items : sm_count()), 352, gb, st>>>(a, mq, mk, md);
+    if (a.dA_dec || a.dtau)
+        launch_gdr_reduce_decay(reinterpret_cast<const float *>(a.ws + (size_t)tiles * a.Hv * sizeof(GdrKeep<K, V>)), tiles, a.Hv,
+                                a.dA_dec, a.dtau, st);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_gdr_bwd_tc(int K, int V, const GdrArgs &a, cudaStream_t st) {
+    if (K == 64) return V == 64 ? bwd_t<64, 64>(a, st) : bwd_t<64, 128>(a, st);
+    return V == 64 ? bwd_t<128, 64>(a, st) : bwd_t<128, 128>(a, st);
+}
+
+}  // namespace carve

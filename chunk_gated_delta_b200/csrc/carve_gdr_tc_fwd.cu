@@ -1,0 +1,620 @@
+// Scalar-gated delta rule, forward, on the 5th-generation tensor core (carve_gdr_tc.cuh).
+//
+// gdr_tc_prep: one CTA per (tile, key head) forms [Q; K] K^T with one M = 128 product and, for each
+// value head of the key head, the decayed A and M, Tm by blocked inversion in fp32, and the gate
+// vectors.  It needs no state, so all tiles run at once.
+//
+// gdr_tc_sweep: one CTA per (sequence, value head) carries the state through the chunks.  The state is
+// a tensor-memory accumulator with the value channels as its 128 lanes, so every product of the
+// recurrence has A in tensor memory (what the last step produced) and B in shared memory (K, Q, Tm or
+// A as copied), and a thread owns half a state row:
+//   G = S K^T (hi, lo), Q S^T       -> R = w (v - e^G G), split
+//   U = R Tm^T (three terms)        -> e^{G_C - G} U, split; U
+//   S += (e^{G_C - G} U) K (hi, lo)  -> S split for the next chunk, S scaled by its e^{G_C}
+//   O = e^G Q S^T + U A^T            off the chain
+// The chain of one chunk is three products and three register passes; what bounds the sweep is
+// their latency (B H units on 148 SMs, one chain each), not the tensor core's rate or HBM.
+// Warps 0-7 register passes, 8 copies in (TMA and bulk, two stages), 9 products, 10 copies out.
+#include "carve_gdr_tc.cuh"
+
+namespace carve {
+
+__device__ int g_gdr_timeout;   // set when a bounded wait gives up (never expected)
+__device__ int g_gdr_tc_bad_seqlens;
+
+int gdr_tc_fwd_take_timeout() {
+    int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_gdr_timeout, sizeof(int)) != cudaSuccess) return 0;
+    if (v) {
+        const int z = 0;
+        cudaMemcpyToSymbol(g_gdr_timeout, &z, sizeof(int));
+    }
+    return v;
+}
+int gdr_tc_fwd_take_bad_seqlens() {
+    int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_gdr_tc_bad_seqlens, sizeof(int)) != cudaSuccess) return 0;
+    if (v) {
+        const int z = 0;
+        cudaMemcpyToSymbol(g_gdr_tc_bad_seqlens, &z, sizeof(int));
+    }
+    return v;
+}
+
+namespace {
+
+constexpr int LM = 68;   // row stride of the fp32 64 x 64 matrices
+
+template <int K>
+struct PrepSmem {
+    union {
+        __nv_bfloat16 qk[K / 64][128 * 64];   // [Q; K], rows 0-63 and 64-127
+        struct {
+            union {
+                float M[kC][LM];
+                __nv_bfloat16 t[2][kC * 64];   // Tm hi, lo on their way out
+            };
+            float X[kC][LM];
+        };
+    };
+    __nv_bfloat16 A[kC * 64];
+    float eG[kC], eK[kC], w[kC], G[kC];
+    uint64_t full, done;
+    uint32_t tmem;
+};
+
+// X = (I + M)^-1 for a strictly lower-triangular M (64 x 64), X zero on entry; M is overwritten.
+// 16 x 16 diagonal blocks by substitution, then off-diagonal blocks by T21 = -T22 (M21 T11), first of
+// size 16, then of size 32.  128 threads.
+__device__ __forceinline__ void invert64(float (*M)[LM], float (*X)[LM]) {
+    const int tid = threadIdx.x;
+    if (tid < kC) {
+        const int o = tid / 16 * 16, c = tid % 16;
+        float acc[16];
+#pragma unroll
+        for (int t = 0; t < 16; ++t) acc[t] = 0.f;
+#pragma unroll
+        for (int s = 0; s < 16; ++s) {
+            const float x = (s == c ? 1.f : 0.f) - acc[s];
+            X[o + s][o + c] = x;
+#pragma unroll
+            for (int t = s + 1; t < 16; ++t) acc[t] += M[o + t][o + s] * x;
+        }
+    }
+    __syncthreads();
+    {
+        const int o = tid / 64 * 32, i = tid % 64 / 4, j = tid % 4 * 4;
+        float y[4] = {};
+#pragma unroll
+        for (int s = 0; s < 16; ++s) {
+            const float m = M[o + 16 + i][o + s];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] += m * X[o + s][o + j + e];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) M[o + 16 + i][o + j + e] = y[e];
+        __syncthreads();
+        float z[4] = {};
+#pragma unroll
+        for (int s = 0; s < 16; ++s) {
+            const float x = X[o + 16 + i][o + 16 + s];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[e] -= x * M[o + 16 + s][o + j + e];
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) X[o + 16 + i][o + j + e] = z[e];
+    }
+    __syncthreads();
+    {
+        const int i = tid / 4, j = tid % 4 * 8;
+        float y[8] = {};
+#pragma unroll 8
+        for (int s = 0; s < 32; ++s) {
+            const float m = M[32 + i][s];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] += m * X[s][j + e];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) M[32 + i][j + e] = y[e];
+        __syncthreads();
+        float z[8] = {};
+#pragma unroll 8
+        for (int s = 0; s < 32; ++s) {
+            const float x = X[32 + i][32 + s];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] -= x * M[32 + s][j + e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) X[32 + i][j + e] = z[e];
+    }
+    __syncthreads();
+}
+
+template <int K>
+__global__ void __launch_bounds__(128) gdr_tc_prep(GdrArgs a, const __grid_constant__ CUtensorMap mq,
+                                                   const __grid_constant__ CUtensorMap mk) {
+    extern __shared__ __align__(16) unsigned char raw[];
+    PrepSmem<K> &sm = *reinterpret_cast<PrepSmem<K> *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    const int tile = blockIdx.x / a.Hk, hk = blockIdx.x % a.Hk, share = a.Hv / a.Hk;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    int n, c, len;
+    long long row;
+    if (!a.seq.find(tile, kC, n, c, row, len)) return;
+    row += (long long)c * kC;
+    const int m = min(kC, len - c * kC);
+    if (tid == 0) {
+        mbar_init(&sm.full, 1);
+        mbar_init(&sm.done, 1);
+        fence_mbar_init();
+    }
+    if (warp == 0) tmem_alloc(&sm.tmem, 64);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tm = sm.tmem;
+    bool ok = true;
+    if (warp == 0) {
+        if (lane == 0) {
+            mbar_expect_tx(&sm.full, 128 * K * 2);
+            for (int x = 0; x < K / 64; ++x) {
+                tma_load_3d(sm.qk[x], &mq, 64 * x, hk, (int)row, &sm.full);
+                tma_load_3d(sm.qk[x] + kC * 64, &mk, 64 * x, hk, (int)row, &sm.full);
+            }
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.full, 0, kSwaWait));
+        if (ok && lane == 0) {
+#pragma unroll
+            for (int kk = 0; kk < K / 16; ++kk)
+                umma_bf16(tm, umma_desc(smem_u32(sm.qk[kk / 4]) + 32 * (kk % 4)),
+                          umma_desc(smem_u32(sm.qk[kk / 4]) + kTile64 + 32 * (kk % 4)), umma_idesc_bf16(128, 64), kk > 0);
+            umma_commit(&sm.done);
+        }
+        __syncwarp();
+    }
+    ok = ok && mbar_wait(&sm.done, 0, kSwaWait);
+    if (__syncthreads_or(!ok)) {   // give up together, with the copy landed and the product finished
+        if (tid == 0) {
+            atomicOr(&g_gdr_timeout, 1);
+            mbar_wait(&sm.full, 0, kSwaWait);
+        }
+        __syncthreads();
+        if (warp == 0) tmem_dealloc(tm, 64);
+        return;
+    }
+    tc_fence_after_sync();
+    // row tid of [Q; K] K^T: q_t.k_s for tid = t < 64, k_t.k_s for tid = 64 + t
+    uint32_t g[64];
+    tmem_ld32(tm + ((uint32_t)warp << 21), g);
+    tmem_ld32(tm + ((uint32_t)warp << 21) + 32, g + 32);
+    tmem_wait_ld();
+    tmem_tie(g);
+    tmem_tie(g + 32);
+    const int t = tid % kC;
+    for (int h = hk * share; h < (hk + 1) * share; ++h) {
+        if (tid == 0) bulk_wait_read<0>();   // the last head's copies out have left the buffers
+        __syncthreads();
+        if (tid < kC) {   // gates and the running sum of log a; rows behind the end: log a = 0, w = 0
+            float la = 0.f, w = 0.f;
+            if (tid < m) {
+                const size_t at = (size_t)(row + tid) * a.Hv + h;
+                const float x = ld_io(static_cast<const __nv_bfloat16 *>(a.g_logit) + at) + (a.tau ? a.tau[h] : 0.f);
+                la = -decay_amp(a.A_dec, h) * softplus_f(x);
+                w = sigmoid_f(ld_io(static_cast<const __nv_bfloat16 *>(a.w_logit) + at));
+            }
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const float up = __shfl_up_sync(0xffffffffu, la, off);
+                if (lane >= off) la += up;
+            }
+            sm.G[tid] = la;
+            sm.w[tid] = w;
+        }
+        __syncthreads();
+        if (tid >= 32 && tid < kC) sm.G[tid] += sm.G[31];
+        __syncthreads();
+        if (tid < kC) {
+            sm.eG[tid] = expf(sm.G[tid]);
+            sm.eK[tid] = expf(sm.G[kC - 1] - sm.G[tid]);
+        }
+        const float Gt = sm.G[t], wt = sm.w[t];
+        if (tid < kC) {
+#pragma unroll
+            for (int s = 0; s < kC; s += 8) {
+                uint32_t p[4];
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    const float x0 = s + e <= t && t < m ? __expf(Gt - sm.G[s + e]) * __uint_as_float(g[s + e]) : 0.f;
+                    const float x1 = s + e + 1 <= t && t < m ? __expf(Gt - sm.G[s + e + 1]) * __uint_as_float(g[s + e + 1]) : 0.f;
+                    p[e / 2] = pack_bf16(x0, x1);
+                }
+                *reinterpret_cast<uint4 *>(sm.A + op_off(t, s, kC)) = make_uint4(p[0], p[1], p[2], p[3]);
+                *reinterpret_cast<float4 *>(&sm.X[t][s]) = *reinterpret_cast<float4 *>(&sm.X[t][s + 4]) = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < kC; s += 4) {
+                float x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[e] = s + e < t && t < m ? wt * expf(Gt - sm.G[s + e]) * __uint_as_float(g[s + e]) : 0.f;
+                *reinterpret_cast<float4 *>(&sm.M[t][s]) = make_float4(x[0], x[1], x[2], x[3]);
+            }
+        }
+        __syncthreads();
+        invert64(sm.M, sm.X);
+        {   // Tm into two bf16 terms
+            const int r = tid / 2, c0 = tid % 2 * 32;
+#pragma unroll
+            for (int x = c0; x < c0 + 32; x += 8) {
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) split_pair(sm.X[r][x + 2 * e], sm.X[r][x + 2 * e + 1], hi[e], lo[e]);
+                *reinterpret_cast<uint4 *>(sm.t[0] + op_off(r, x, kC)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(sm.t[1] + op_off(r, x, kC)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+        }
+        fence_proxy_async_smem();
+        __syncthreads();
+        if (tid == 0) {
+            GdrPrep *out = reinterpret_cast<GdrPrep *>(a.prep) + (size_t)tile * a.Hv + h;
+            bulk_s2g(out->t_hi, sm.t, sizeof(sm.t));
+            bulk_s2g(out->A, sm.A, sizeof(sm.A));
+            bulk_s2g(out->eG, sm.eG, 4 * sizeof(sm.eG));
+            bulk_commit();
+        }
+    }
+    if (tid == 0) bulk_wait<0>();
+    __syncthreads();
+    if (warp == 0) tmem_dealloc(tm, 64);
+}
+
+template <int K, int V, bool SAVE>
+struct SweepSmem {
+    __nv_bfloat16 k[2][K / 64][kC * 64], q[2][K / 64][kC * 64];
+    GdrPrep p[2];
+    __nv_bfloat16 v[2][kC * V];                     // plain rows
+    __nv_bfloat16 S[SAVE ? V * K : 8], u[SAVE ? kC * V : 8], o[kC * V];   // on their way out
+    uint64_t full[2], free[2], sready, gfull, qfull, rready, ufull, uready, sfull, ofull, ofree;
+    uint64_t Sout, Sfree, uout, ufree, oout;
+    uint32_t tmem;
+};
+
+template <int K, int V, bool SAVE>
+__global__ void __launch_bounds__(352, 1)
+    gdr_tc_sweep(GdrArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                 const __grid_constant__ CUtensorMap mv) {
+    extern __shared__ __align__(16) unsigned char raw[];
+    typedef SweepSmem<K, V, SAVE> Smem;
+    Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    constexpr int KH = K / 64;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int h = blockIdx.x % a.Hv, n = blockIdx.x / a.Hv, hk = h / (a.Hv / a.Hk);
+    long long row0;
+    int len;
+    a.seq.rows(n, row0, len, threadIdx.x == 0 ? &g_gdr_tc_bad_seqlens : nullptr);
+    const long long t0 = a.seq.tile0(n, kC);
+    const int chunks = (len + kC - 1) / kC;
+    if (threadIdx.x == 0) {
+        for (uint64_t *b : {&sm.full[0], &sm.full[1], &sm.free[0], &sm.free[1], &sm.gfull, &sm.qfull, &sm.ufull, &sm.sfull,
+                            &sm.ofull, &sm.Sfree, &sm.ufree, &sm.ofree})
+            mbar_init(b, 1);
+        for (uint64_t *b : {&sm.sready, &sm.rready, &sm.uready, &sm.Sout, &sm.uout, &sm.oout}) mbar_init(b, 256);
+        fence_mbar_init();
+    }
+    if (warp == 9) tmem_alloc(&sm.tmem, 512);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tm = sm.tmem;
+    // tensor memory: S 0-127, S hi 128, S lo 192, G (then R hi, lo) 256, Q S (then O) 320, U (then
+    // e^{G_C - G} U hi, lo) 384, U as bf16 448
+    constexpr uint32_t cHi = 128, cLo = 192, cG = 256, cO = 320, cU = 384, cUb = 448;
+    bool ok = true;
+    auto wait = [&](uint64_t &bar, int phase) {   // by a whole warp
+        return (bool)__all_sync(0xffffffffu, mbar_wait(&bar, phase & 1, kSwaWait));
+    };
+
+    if (warp == 8) {
+        int c = 0;
+        for (; c < chunks; ++c) {
+            const int s = c & 1;
+            if (c >= 2) ok = wait(sm.free[s], c / 2 - 1);
+            if (!ok) break;
+            if (lane == 0) {
+                const int row = (int)(row0 + (long long)c * kC);
+                mbar_expect_tx(&sm.full[s], 2 * kC * K * 2 + kC * V * 2 + sizeof(GdrPrep));
+                for (int x = 0; x < KH; ++x) tma_load_3d(sm.k[s][x], &mk, 64 * x, hk, row, &sm.full[s]);
+                bulk_g2s(&sm.p[s], reinterpret_cast<const GdrPrep *>(a.prep) + (size_t)(t0 + c) * a.Hv + h, sizeof(GdrPrep),
+                         &sm.full[s]);
+                tma_load_3d(sm.v[s], &mv, 0, h, row, &sm.full[s]);
+                for (int x = 0; x < KH; ++x) tma_load_3d(sm.q[s][x], &mq, 64 * x, hk, row, &sm.full[s]);
+            }
+        }
+        if (!ok)
+            for (int i = max(0, c - 2); i < c; ++i) wait(sm.full[i & 1], i / 2);
+    } else if (warp == 9) {
+        constexpr uint32_t iN64 = umma_idesc_bf16(128, 64), iS = umma_idesc_bf16(128, K) | kUmmaBmn;
+        int c = 0;
+        for (; c < chunks; ++c) {
+            const int s = c & 1;
+            if (!(ok = wait(sm.full[s], c / 2))) break;
+            if (len - c * kC < kC) {   // key rows behind the end meet U = 0 in the state update
+                zero_rows(sm.k[s], len - c * kC, KH, kTile64, lane);
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            if (!(ok = wait(sm.sready, c))) break;
+            tc_fence_after_sync();
+            if (lane == 0) {
+#pragma unroll
+                for (int lo = 0; lo < 2; ++lo)
+#pragma unroll
+                    for (int kk = 0; kk < K / 16; ++kk)
+                        umma_bf16_ta(tm + cG, tm + (lo ? cLo : cHi) + 8 * kk, umma_desc(smem_u32(sm.k[s][kk / 4]) + 32 * (kk % 4)),
+                                     iN64, lo > 0 || kk > 0);
+                umma_commit(&sm.gfull);
+            }
+            __syncwarp();
+            if (c > 0 && !(ok = wait(sm.ofree, c - 1))) break;
+            tc_fence_after_sync();
+            if (lane == 0) {
+#pragma unroll
+                for (int kk = 0; kk < K / 16; ++kk)
+                    umma_bf16_ta(tm + cO, tm + cHi + 8 * kk, umma_desc(smem_u32(sm.q[s][kk / 4]) + 32 * (kk % 4)), iN64, kk > 0);
+                umma_commit(&sm.qfull);
+            }
+            __syncwarp();
+            if (!(ok = wait(sm.rready, c))) break;
+            tc_fence_after_sync();
+            if (lane == 0) {
+                const uint32_t th = smem_u32(sm.p[s].t_hi), tl = smem_u32(sm.p[s].t_lo);
+#pragma unroll
+                for (int x = 0; x < 3; ++x)   // R hi Tm hi, R lo Tm hi, R hi Tm lo
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_bf16_ta(tm + cU, tm + cG + half_col(kk) + (x == 1 ? 16 : 0), umma_desc((x == 2 ? tl : th) + 32 * kk), iN64,
+                                     x > 0 || kk > 0);
+                umma_commit(&sm.ufull);
+            }
+            __syncwarp();
+            if (!(ok = wait(sm.uready, c))) break;
+            tc_fence_after_sync();
+            if (lane == 0) {
+#pragma unroll
+                for (int lo = 0; lo < 2; ++lo)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_bf16_ta(tm, tm + cU + half_col(kk) + 16 * lo, umma_desc_mn(smem_u32(sm.k[s][0]) + 2048 * kk, kTile64), iS, 1);
+                umma_commit(&sm.sfull);
+                const uint32_t A = smem_u32(sm.p[s].A);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) umma_bf16_ta(tm + cO, tm + cUb + 8 * kk, umma_desc(A + 32 * kk), iN64, 1);
+                umma_commit(&sm.ofull);
+                umma_commit(&sm.free[s]);
+            }
+            __syncwarp();
+        }
+        // products in flight finish before the tensor memory is freed
+        if (!ok)
+            for (uint64_t *b : {&sm.gfull, &sm.qfull, &sm.ufull, &sm.sfull, &sm.ofull}) {
+                if (c > 0) wait(*b, c - 1);
+                wait(*b, c);
+            }
+    } else if (warp == 10) {
+        typedef GdrKeep<K, V> Keep;
+        Keep *keep = SAVE ? reinterpret_cast<Keep *>(a.saved) + (size_t)t0 * a.Hv + h : nullptr;
+        for (int c = 0; c < chunks && ok; ++c) {
+            if (SAVE) {
+                if (!(ok = wait(sm.Sout, c))) break;
+                if (lane == 0) {
+                    bulk_s2g(keep[(size_t)c * a.Hv].S, sm.S, sizeof(sm.S));
+                    bulk_commit();
+                }
+                if (!(ok = wait(sm.uout, c))) break;
+                if (lane == 0) {
+                    bulk_s2g(keep[(size_t)c * a.Hv].x, sm.u, sizeof(sm.u));
+                    bulk_commit();
+                    bulk_wait_read<1>();
+                    mbar_arrive(&sm.Sfree);
+                }
+                __syncwarp();
+            }
+            if (!(ok = wait(sm.oout, c))) break;
+            for (int t = lane; t < min(kC, len - c * kC); t += 32)
+                bulk_s2g(static_cast<__nv_bfloat16 *>(a.o) + ((size_t)(row0 + (long long)c * kC + t) * a.Hv + h) * V, sm.o + t * V,
+                         V * 2);
+            bulk_commit();
+            bulk_wait_read<0>();
+            __syncwarp();
+            if (lane == 0) {
+                if (SAVE) mbar_arrive(&sm.ufree);
+                mbar_arrive(&sm.ofree);
+            }
+        }
+        bulk_wait<0>();
+    } else {
+        const int half = warp / 4, quarter = warp % 4, r = quarter * 32 + lane;
+        const uint32_t tl = tm + ((uint32_t)quarter << 21);
+        const int x0 = half * (K / 2), c32 = half * 32;   // this thread's columns of S, its tokens
+        const bool live = r < V;                          // value row (others carry zeros)
+        const size_t st = (((size_t)n * a.Hv + h) * V + (live ? r : 0)) * K + x0;
+        float S[K / 2];
+#pragma unroll
+        for (int x = 0; x < K / 2; x += 4) {
+            const float4 y = live && a.S0 ? *reinterpret_cast<const float4 *>(a.S0 + st + x) : make_float4(0.f, 0.f, 0.f, 0.f);
+            S[x] = y.x;
+            S[x + 1] = y.y;
+            S[x + 2] = y.z;
+            S[x + 3] = y.w;
+        }
+        // S (in registers) as the operands of chunk c, scaled accumulator, and its copy out
+        auto put_state = [&](int c) {
+            if (!(ok = wait(sm.full[c & 1], c / 2))) return;
+            const float gl = sm.p[c & 1].eG[kC - 1];
+            uint32_t hi[K / 4], lo[K / 4], sc[K / 2];
+#pragma unroll
+            for (int x = 0; x < K / 4; ++x) split_pair(S[2 * x], S[2 * x + 1], hi[x], lo[x]);
+#pragma unroll
+            for (int x = 0; x < K / 2; ++x) sc[x] = __float_as_uint(S[x] * gl);
+#pragma unroll
+            for (int x = 0; x < K / 4; x += 16) {
+                tmem_st16(tl + cHi + x0 / 2 + x, hi + x);
+                tmem_st16(tl + cLo + x0 / 2 + x, lo + x);
+            }
+#pragma unroll
+            for (int x = 0; x < K / 2; x += 32) tmem_st32(tl + x0 + x, sc + x);
+            tmem_wait_st();
+            tc_fence_before_sync();
+            mbar_arrive(&sm.sready);
+            if (SAVE) {
+                if (c > 0 && !(ok = wait(sm.Sfree, c - 1))) return;
+                if (live)
+#pragma unroll
+                    for (int x = 0; x < K / 4; x += 4)
+                        *reinterpret_cast<uint4 *>(sm.S + op_off(r, x0 + 2 * x, V)) = make_uint4(hi[x], hi[x + 1], hi[x + 2], hi[x + 3]);
+                fence_proxy_async_smem();
+                mbar_arrive(&sm.Sout);
+            }
+        };
+        if (chunks > 0) put_state(0);
+        for (int c = 0; c < chunks && ok; ++c) {
+            const GdrPrep &p = sm.p[c & 1];
+            const int m = min(kC, len - c * kC);
+            uint32_t x[32], y[16], z[16];
+            // R = w (v - e^G G)
+            if (!(ok = wait(sm.gfull, c))) break;
+            tc_fence_after_sync();
+            tmem_ld32(tl + cG + c32, x);
+            tmem_wait_ld();
+            tmem_tie(x);
+            const __nv_bfloat16 *v = sm.v[c & 1] + c32 * V + (live ? r : 0);
+#pragma unroll
+            for (int t = 0; t < 32; t += 2) {
+                float R[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    R[e] = c32 + t + e < m && live
+                               ? p.w[c32 + t + e] * (__bfloat162float(v[(t + e) * V]) - p.eG[c32 + t + e] * __uint_as_float(x[t + e]))
+                               : 0.f;
+                split_pair(R[0], R[1], y[t / 2], z[t / 2]);
+            }
+            tmem_st16(tl + cG + c32, y);   // over the columns of G that this thread has read
+            tmem_st16(tl + cG + c32 + 16, z);
+            tmem_wait_st();
+            tc_fence_before_sync();
+            mbar_arrive(&sm.rready);
+            // e^G Q S^T
+            if (!(ok = wait(sm.qfull, c))) break;
+            tc_fence_after_sync();
+            tmem_ld32(tl + cO + c32, x);
+            tmem_wait_ld();
+            tmem_tie(x);
+#pragma unroll
+            for (int t = 0; t < 32; ++t) x[t] = __float_as_uint(__uint_as_float(x[t]) * p.eG[c32 + t]);
+            tmem_st32(tl + cO + c32, x);
+            // U
+            if (!(ok = wait(sm.ufull, c))) break;
+            tc_fence_after_sync();
+            tmem_ld32(tl + cU + c32, x);
+            tmem_wait_ld();
+            tmem_tie(x);
+            uint32_t ub[16];
+#pragma unroll
+            for (int t = 0; t < 32; t += 2) {
+                const float u0 = __uint_as_float(x[t]), u1 = __uint_as_float(x[t + 1]);
+                ub[t / 2] = pack_bf16(u0, u1);
+                split_pair(u0 * p.eK[c32 + t], u1 * p.eK[c32 + t + 1], y[t / 2], z[t / 2]);
+            }
+            tmem_st16(tl + cU + c32, y);
+            tmem_st16(tl + cU + c32 + 16, z);
+            tmem_st16(tl + cUb + 16 * half, ub);
+            tmem_wait_st();
+            tc_fence_before_sync();
+            mbar_arrive(&sm.uready);
+            if (SAVE) {
+                if (c > 0 && !(ok = wait(sm.ufree, c - 1))) break;
+                if (live)
+#pragma unroll
+                    for (int t = 0; t < 32; ++t)
+                        reinterpret_cast<uint16_t *>(sm.u)[op_off(c32 + t, r, kC)] = (uint16_t)(ub[t / 2] >> (16 * (t & 1)));
+                fence_proxy_async_smem();
+                mbar_arrive(&sm.uout);
+            }
+            // the state after the chunk
+            if (!(ok = wait(sm.sfull, c))) break;
+            tc_fence_after_sync();
+#pragma unroll
+            for (int i = 0; i < K / 2; i += 32) tmem_ld32(tl + x0 + i, reinterpret_cast<uint32_t *>(S) + i);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < K / 2; i += 32) tmem_tie(reinterpret_cast<uint32_t *>(S) + i);
+            if (c + 1 < chunks) put_state(c + 1);
+            if (!ok) break;
+            // outputs
+            if (!(ok = wait(sm.ofull, c))) break;
+            tc_fence_after_sync();
+            tmem_ld32(tl + cO + c32, x);
+            tmem_wait_ld();
+            tmem_tie(x);
+            tc_fence_before_sync();
+            if (c > 0 && !(ok = wait(sm.ofree, c - 1))) break;
+            if (live)
+#pragma unroll
+                for (int t = 0; t < 32; ++t) sm.o[(c32 + t) * V + r] = __float2bfloat16_rn(__uint_as_float(x[t]));
+            fence_proxy_async_smem();
+            mbar_arrive(&sm.oout);
+        }
+        if (ok && a.S_final && live)
+#pragma unroll
+            for (int x = 0; x < K / 2; x += 4)
+                *reinterpret_cast<float4 *>(a.S_final + st + x) = make_float4(S[x], S[x + 1], S[x + 2], S[x + 3]);
+    }
+    if (!ok && lane == 0) atomicOr(&g_gdr_timeout, 1);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    if (warp == 9) tmem_dealloc(tm, 512);
+}
+
+template <int K, int V, bool SAVE>
+cudaError_t sweep_t(const GdrArgs &a, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t st) {
+    auto kern = gdr_tc_sweep<K, V, SAVE>;
+    const int bytes = (int)sizeof(SweepSmem<K, V, SAVE>) + 1024;
+    const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), bytes);
+    if (e != cudaSuccess) return e;
+    kern<<<a.seq.N * a.Hv, 352, bytes, st>>>(a, mq, mk, mv);
+    return cudaGetLastError();
+}
+
+template <int K, int V>
+cudaError_t fwd_t(const GdrArgs &a, bool save, cudaStream_t st) {
+    const long long rows = a.seq.cu ? a.seq.total : (long long)a.seq.N * a.seq.T;
+    CUtensorMap mq{}, mk{}, mv{};
+    if (rows > 0) {   // without rows no tile is copied; the sweep hands the states on
+        cudaError_t e = make_operand_tile_map(&mq, a.q, K, a.Hk, rows, kC);
+        if (e == cudaSuccess) e = make_operand_tile_map(&mk, a.k, K, a.Hk, rows, kC);
+        if (e == cudaSuccess) e = make_token_tile_map(&mv, a.v, 2, V, a.Hv, rows, kC);
+        auto prep = gdr_tc_prep<K>;
+        const int bytes = (int)sizeof(PrepSmem<K>) + 1024;
+        if (e == cudaSuccess) e = set_smem_once(reinterpret_cast<const void *>(prep), bytes);
+        if (e != cudaSuccess) return e;
+        prep<<<(unsigned)(a.seq.n_tiles(kC) * a.Hk), 128, bytes, st>>>(a, mq, mk);
+    }
+    return save ? sweep_t<K, V, true>(a, mq, mk, mv, st) : sweep_t<K, V, false>(a, mq, mk, mv, st);
+}
+
+}  // namespace
+
+GdrSizes gdr_tc_sizes(const Seqs &s, int Hv, int K, int V) {
+    const size_t slots = (size_t)s.n_tiles(kC) * Hv, keep = 2 * ((size_t)V * K + kC * V);
+    return {slots * sizeof(GdrPrep), slots * keep, slots * (keep + 2 * sizeof(float))};
+}
+
+cudaError_t launch_gdr_fwd_tc(int K, int V, const GdrArgs &a, bool save, cudaStream_t st) {
+    if (K == 64) return V == 64 ? fwd_t<64, 64>(a, save, st) : fwd_t<64, 128>(a, save, st);
+    return V == 64 ? fwd_t<128, 64>(a, save, st) : fwd_t<128, 128>(a, save, st);
+}
+
+}  // namespace carve

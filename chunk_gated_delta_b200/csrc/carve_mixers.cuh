@@ -139,8 +139,13 @@ struct GdrSizes {
     size_t prep, saved, bwd;
 };
 GdrSizes gdr_simt_sizes(const Seqs &s, int Hv, int K, int V);
-cudaError_t launch_gdr_fwd_simt(int K, int V, bool bf16, const GdrArgs &a, bool save, cudaStream_t st);
-cudaError_t launch_gdr_bwd_simt(int K, int V, bool bf16, const GdrArgs &a, cudaStream_t st);
+cudaError_t launch_gdr_fwd_simt(int K, int V, const GdrArgs &a, bool save, cudaStream_t st);
+cudaError_t launch_gdr_bwd_simt(int K, int V, const GdrArgs &a, cudaStream_t st);
+// dA_dec, dtau [Hv] from the tiles' partial sums [tiles][Hv][2], in a fixed order
+void launch_gdr_reduce_decay(const float *p, long long tiles, int Hv, float *dA_dec, float *dtau, cudaStream_t st);
+GdrSizes gdr_tc_sizes(const Seqs &s, int Hv, int K, int V);
+cudaError_t launch_gdr_fwd_tc(int K, int V, const GdrArgs &a, bool save, cudaStream_t st);
+cudaError_t launch_gdr_bwd_tc(int K, int V, const GdrArgs &a, cudaStream_t st);
 cudaError_t launch_gdr_step(int K, int V, bool bf16, const GdrArgs &a, cudaStream_t st);
 cudaError_t launch_swa_fwd_simt(const SwaArgs &a, cudaStream_t st);
 cudaError_t launch_swa_bwd_simt(const SwaArgs &a, cudaStream_t st);

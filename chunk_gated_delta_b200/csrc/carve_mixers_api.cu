@@ -72,7 +72,8 @@ long long rows_of(const D *d, bool packed) {
 
 carve::GdrSizes sizes(const carve_gdr_dims *d, bool packed) {
     static const int32_t dummy = 0;   // n_tiles asks only whether the call is packed
-    return carve::gdr_simt_sizes(seqs(d, packed ? &dummy : nullptr, packed), d->Hv, d->dk, d->dv);
+    const carve::Seqs s = seqs(d, packed ? &dummy : nullptr, packed);
+    return d->io == CARVE_IO_BF16 ? carve::gdr_tc_sizes(s, d->Hv, d->dk, d->dv) : carve::gdr_simt_sizes(s, d->Hv, d->dk, d->dv);
 }
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -123,7 +124,8 @@ carve_status carve_gdr_fwd(const carve_gdr_dims *d, const int32_t *cu_seqlens, c
     a.prep = static_cast<char *>(saved ? saved : workspace);
     if (saved) a.saved = a.prep + up(sizes(d, packed).prep);
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    return status(carve::launch_gdr_fwd_simt(d->dk, d->dv, d->io == CARVE_IO_BF16, a, saved != nullptr, cs));
+    return status(d->io == CARVE_IO_BF16 ? carve::launch_gdr_fwd_tc(d->dk, d->dv, a, saved != nullptr, cs)
+                                         : carve::launch_gdr_fwd_simt(d->dk, d->dv, a, saved != nullptr, cs));
 }
 
 carve_status carve_gdr_bwd(const carve_gdr_dims *d, const int32_t *cu_seqlens, const void *q,
@@ -153,7 +155,8 @@ carve_status carve_gdr_bwd(const carve_gdr_dims *d, const int32_t *cu_seqlens, c
     a.saved = a.prep + up(sizes(d, packed).prep);
     a.ws = static_cast<char *>(workspace);
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    return status(carve::launch_gdr_bwd_simt(d->dk, d->dv, d->io == CARVE_IO_BF16, a, cs));
+    return status(d->io == CARVE_IO_BF16 ? carve::launch_gdr_bwd_tc(d->dk, d->dv, a, cs)
+                                         : carve::launch_gdr_bwd_simt(d->dk, d->dv, a, cs));
 }
 
 carve_status carve_gdr_step(const carve_gdr_dims *d, const void *q, const void *k, const void *v,
