@@ -49,10 +49,71 @@ __device__ __forceinline__ void zero_rows(void *tile, int first, int halves, uin
             reinterpret_cast<uint4 *>(static_cast<char *>(tile) + y * stride)[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// Column of 16 tokens (slice kk of 4) of a split [lane][64 tokens] operand in tensor memory: each half
-// of 32 tokens keeps its hi terms (16 columns) and then its lo terms, over the 32 columns of the
-// accumulator it comes from, so a thread overwrites only what it has read itself.
-__device__ __forceinline__ uint32_t half_col(int kk) { return 32 * (kk / 2) + 8 * (kk % 2); }
+// The sweeps' register warps: four a lane quarter, each with a quarter of the columns (state) or 16
+// of the chunk's tokens.  Half as many threads with twice the columns spilled, and with shared memory
+// taken by the tiles a spill goes to L2.
+constexpr int kRegWarps = 16, kSweepThreads = (kRegWarps + 4) * 32;
+// Registers: 640 threads start with 96 (61440 in all); the register warps take 112 and the others go
+// down to 32 (512 x 112 + 128 x 32 = 61440), or 104 and 64.
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
+
+// A split [lane][64 tokens] operand in tensor memory lies over the accumulator it comes from: 16
+// tokens' hi terms in 8 columns, then their lo terms, so that a thread overwrites only what it has
+// read itself.
+__device__ __forceinline__ uint32_t split_col(int kk, int lo) { return 16 * kk + 8 * lo; }
+// 16 tokens x[] of this lane as such an operand
+__device__ __forceinline__ void put_split16(uint32_t taddr, const float *x) {
+    uint32_t y[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) split_pair(x[2 * i], x[2 * i + 1], y[i], y[8 + i]);
+    tmem_st16(taddr, y);
+}
+// A row's part of the state, COLS columns from x0: operands hi, lo and the accumulator times gl; the hi
+// terms stay in hi[] when the state is kept
+template <int COLS>
+__device__ __forceinline__ void put_state(uint32_t acc, uint32_t hi_at, uint32_t lo_at, const float *S, float gl, uint32_t *hi) {
+#pragma unroll
+    for (int b = 0; b < COLS; b += 16) {
+        uint32_t lo[8], sc[16];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) split_pair(S[b + 2 * i], S[b + 2 * i + 1], hi[b / 2 + i], lo[i]);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sc[i] = __float_as_uint(S[b + i] * gl);
+        tmem_st8(hi_at + b / 2, hi + b / 2);
+        tmem_st8(lo_at + b / 2, lo);
+        tmem_st16(acc + b, sc);
+    }
+    tmem_wait_st();
+    tc_fence_before_sync();
+}
+template <int COLS>
+__device__ __forceinline__ void get_state(uint32_t acc, float *S) {
+    uint32_t *x = reinterpret_cast<uint32_t *>(S);
+#pragma unroll
+    for (int b = 0; b < COLS; b += 16) tmem_ld16(acc + b, x + b);
+    tmem_wait_ld();
+#pragma unroll
+    for (int b = 0; b < COLS; b += 16) tmem_tie16(x + b);
+}
+template <int COLS>
+__device__ __forceinline__ void load_row(float *S, const float *src) {
+#pragma unroll
+    for (int x = 0; x < COLS; x += 4) {
+        const float4 y = src ? *reinterpret_cast<const float4 *>(src + x) : make_float4(0.f, 0.f, 0.f, 0.f);
+        S[x] = y.x;
+        S[x + 1] = y.y;
+        S[x + 2] = y.z;
+        S[x + 3] = y.w;
+    }
+}
+template <int COLS>
+__device__ __forceinline__ void store_row(float *dst, const float *S) {
+#pragma unroll
+    for (int x = 0; x < COLS; x += 4) *reinterpret_cast<float4 *>(dst + x) = make_float4(S[x], S[x + 1], S[x + 2], S[x + 3]);
+}
 
 constexpr uint32_t kUmmaAmn = 1u << 15;   // instruction descriptor: A is MN-contiguous
 

@@ -2,7 +2,7 @@
 //
 // gdr_tc_bsweep: one CTA per (sequence, value head) carries dS backwards through the chunks, the
 // mirror of the forward's sweep (value channels = lanes of the accumulator, A in tensor memory, a
-// thread owns half a state row; only dO^T A takes its A from shared memory, read transposed):
+// thread owns a quarter of a state row; only dO^T A takes its A from shared memory, read transposed):
 //   X = dS1 K^T (hi, lo), dO^T A    -> dU = dO^T A + e^{G_C - G} X, split
 //   dY = dU Tm (three terms)         -> -w e^G dY, split; dV = w dY; dY
 //   dS0 = e^{G_C} dS1 + (e^G dO)^T Q - (w e^G dY)^T K   (hi, lo) -> split for the next chunk
@@ -49,18 +49,18 @@ struct BsweepSmem {
     __nv_bfloat16 k[2][K / 64][kC * 64], q[2][K / 64][kC * 64], dO[2][2][kC * 64];   // dO's second half zero at V = 64
     GdrPrep p[2];
     __nv_bfloat16 S[V * K], y[kC * V], dv[kC * V];   // on their way out
-    uint64_t full[2], free[2], sready, dready, gfull, uready, yfull, yready, sfull, Sout, Sfree, yout, yfree, drain;
+    uint64_t full[2], free[2], sready, gfull, uready, yfull, yready, sfull, Sout, Sfree, yout, yfree, drain;
     uint32_t tmem;
 };
 
 template <int K, int V>
-__global__ void __launch_bounds__(352, 1)
+__global__ void __launch_bounds__(kSweepThreads, 1)
     gdr_tc_bsweep(GdrArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                   const __grid_constant__ CUtensorMap md) {
     extern __shared__ __align__(16) unsigned char raw[];
     typedef BsweepSmem<K, V> Smem;
     Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    constexpr int KH = K / 64, VH = V / 64;
+    constexpr int KH = K / 64, VH = V / 64, KQ = K / 4;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int h = blockIdx.x % a.Hv, n = blockIdx.x / a.Hv, hk = h / (a.Hv / a.Hk);
     long long row0;
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(352, 1)
         for (uint64_t *b : {&sm.full[0], &sm.full[1], &sm.free[0], &sm.free[1], &sm.gfull, &sm.yfull, &sm.sfull, &sm.Sfree,
                             &sm.yfree, &sm.drain})
             mbar_init(b, 1);
-        for (uint64_t *b : {&sm.sready, &sm.dready, &sm.uready, &sm.yready, &sm.Sout, &sm.yout}) mbar_init(b, 256);
+        for (uint64_t *b : {&sm.sready, &sm.uready, &sm.yready, &sm.Sout, &sm.yout}) mbar_init(b, kRegWarps);
         fence_mbar_init();
     }
     if (VH == 1) {
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(352, 1)
             reinterpret_cast<uint4 *>(sm.dO[i / (kC * 8)][1])[i % (kC * 8)] = make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async_smem();
     }
-    if (warp == 9) tmem_alloc(&sm.tmem, 512);
+    if (warp == kRegWarps + 1) tmem_alloc(&sm.tmem, 512);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
@@ -93,7 +93,8 @@ __global__ void __launch_bounds__(352, 1)
         return (bool)__all_sync(0xffffffffu, mbar_wait(&bar, phase & 1, kSwaWait));
     };
 
-    if (warp == 8) {
+    if (warp >= kRegWarps) regs_down<64>();
+    if (warp == kRegWarps) {
         int i = 0;
         for (; i < chunks; ++i) {
             const int s = i & 1, c = chunks - 1 - i;
@@ -111,7 +112,7 @@ __global__ void __launch_bounds__(352, 1)
         }
         if (!ok)
             for (int j = max(0, i - 2); j < i; ++j) wait(sm.full[j & 1], j / 2);
-    } else if (warp == 9) {
+    } else if (warp == kRegWarps + 1) {
         constexpr uint32_t iN64 = umma_idesc_bf16(128, 64), iS = umma_idesc_bf16(128, K) | kUmmaBmn;
         for (int i = 0; i < chunks; ++i) {
             const int s = i & 1, c = chunks - 1 - i;
@@ -142,17 +143,6 @@ __global__ void __launch_bounds__(352, 1)
                 umma_commit(&sm.gfull);
             }
             __syncwarp();
-            if (!(ok = wait(sm.dready, i))) break;
-            tc_fence_after_sync();
-            if (lane == 0) {
-#pragma unroll
-                for (int lo = 0; lo < 2; ++lo)
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        umma_bf16_ta(tm, tm + cD + half_col(kk) + 16 * lo, umma_desc_mn(smem_u32(sm.q[s][0]) + 2048 * kk, kTile64),
-                                     iS, 1);
-            }
-            __syncwarp();
             if (!(ok = wait(sm.uready, i))) break;
             tc_fence_after_sync();
             if (lane == 0) {
@@ -161,9 +151,16 @@ __global__ void __launch_bounds__(352, 1)
                 for (int x = 0; x < 3; ++x)   // dU hi Tm hi, dU lo Tm hi, dU hi Tm lo
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        umma_bf16_ta(tm + cY, tm + cX + half_col(kk) + (x == 1 ? 16 : 0),
+                        umma_bf16_ta(tm + cY, tm + cX + split_col(kk, x == 1),
                                      umma_desc_mn((x == 2 ? tl : th) + 2048 * kk, kTile64), iN64 | kUmmaBmn, x > 0 || kk > 0);
                 umma_commit(&sm.yfull);
+                // in the shadow of the pass over dY
+#pragma unroll
+                for (int lo = 0; lo < 2; ++lo)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_bf16_ta(tm, tm + cD + split_col(kk, lo), umma_desc_mn(smem_u32(sm.q[s][0]) + 2048 * kk, kTile64),
+                                     iS, 1);
             }
             __syncwarp();
             if (!(ok = wait(sm.yready, i))) break;
@@ -173,7 +170,7 @@ __global__ void __launch_bounds__(352, 1)
                 for (int lo = 0; lo < 2; ++lo)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        umma_bf16_ta(tm, tm + cY + half_col(kk) + 16 * lo, umma_desc_mn(smem_u32(sm.k[s][0]) + 2048 * kk, kTile64),
+                        umma_bf16_ta(tm, tm + cY + split_col(kk, lo), umma_desc_mn(smem_u32(sm.k[s][0]) + 2048 * kk, kTile64),
                                      iS, 1);
                 umma_commit(&sm.sfull);
                 umma_commit(&sm.free[s]);
@@ -183,7 +180,7 @@ __global__ void __launch_bounds__(352, 1)
         if (lane == 0) umma_commit(&sm.drain);   // products in flight finish before the tensor memory is freed
         __syncwarp();
         wait(sm.drain, 0);
-    } else if (warp == 10) {
+    } else if (warp == kRegWarps + 2) {
         typedef GdrKeep<K, V> Keep;
         Keep *keep = reinterpret_cast<Keep *>(a.ws) + (size_t)t0 * a.Hv + h;
         for (int i = 0; i < chunks && ok; ++i) {
@@ -207,134 +204,94 @@ __global__ void __launch_bounds__(352, 1)
             if (lane == 0) mbar_arrive(&sm.yfree);
         }
         bulk_wait<0>();
-    } else {
-        const int half = warp / 4, quarter = warp % 4, r = quarter * 32 + lane;
+    } else if (warp < kRegWarps) {
+        regs_up<104>();
+        const int part = warp / 4, quarter = warp % 4, r = quarter * 32 + lane;
         const uint32_t tl = tm + ((uint32_t)quarter << 21);
-        const int x0 = half * (K / 2), c32 = half * 32;   // this thread's columns of dS, its tokens
-        const bool live = r < V;                          // value row (others carry zeros)
+        const int x0 = part * KQ, c16 = part * 16;   // this thread's columns of dS, its tokens
+        const bool live = r < V;                     // value row (others carry zeros)
         const size_t st = (((size_t)n * a.Hv + h) * V + (live ? r : 0)) * K + x0;
-        float S[K / 2];
-#pragma unroll
-        for (int x = 0; x < K / 2; x += 4) {
-            const float4 y = live && a.dS_final ? *reinterpret_cast<const float4 *>(a.dS_final + st + x) : make_float4(0.f, 0.f, 0.f, 0.f);
-            S[x] = y.x;
-            S[x + 1] = y.y;
-            S[x + 2] = y.z;
-            S[x + 3] = y.w;
-        }
-        for (int i = 0; i < chunks && ok; ++i) {
+        float S[KQ];
+        load_row<KQ>(S, live && a.dS_final ? a.dS_final + st : nullptr);
+        for (int i = 0; i < chunks; ++i) {
             const int s = i & 1, c = chunks - 1 - i, m = min(kC, len - c * kC);
             const GdrPrep &p = sm.p[s];
+            uint32_t hi[KQ / 2], x[16];
+            float y[16];
             // dS1 as operands, the accumulator scaled by e^{G_C}
             if (!(ok = wait(sm.full[s], i / 2))) break;
-            {
-                const float gl = p.eG[kC - 1];
-                uint32_t hi[K / 4], lo[K / 4], sc[K / 2];
+            put_state<KQ>(tl + x0, tl + cHi + x0 / 2, tl + cLo + x0 / 2, S, p.eG[kC - 1], hi);
+            mbar_arrive_warp(&sm.sready);
+            if (i > 0 && !(ok = wait(sm.Sfree, i - 1))) break;
+            if (live)
 #pragma unroll
-                for (int x = 0; x < K / 4; ++x) split_pair(S[2 * x], S[2 * x + 1], hi[x], lo[x]);
-#pragma unroll
-                for (int x = 0; x < K / 2; ++x) sc[x] = __float_as_uint(S[x] * gl);
-#pragma unroll
-                for (int x = 0; x < K / 4; x += 16) {
-                    tmem_st16(tl + cHi + x0 / 2 + x, hi + x);
-                    tmem_st16(tl + cLo + x0 / 2 + x, lo + x);
-                }
-#pragma unroll
-                for (int x = 0; x < K / 2; x += 32) tmem_st32(tl + x0 + x, sc + x);
-                tmem_wait_st();
-                tc_fence_before_sync();
-                mbar_arrive(&sm.sready);
-                if (i > 0 && !(ok = wait(sm.Sfree, i - 1))) break;
-                if (live)
-#pragma unroll
-                    for (int x = 0; x < K / 4; x += 4)
-                        *reinterpret_cast<uint4 *>(sm.S + op_off(r, x0 + 2 * x, V)) = make_uint4(hi[x], hi[x + 1], hi[x + 2], hi[x + 3]);
-                fence_proxy_async_smem();
-                mbar_arrive(&sm.Sout);
-            }
-            uint32_t x[32], y[16], z[16];
+                for (int e = 0; e < KQ / 2; e += 4)
+                    *reinterpret_cast<uint4 *>(sm.S + op_off(r, x0 + 2 * e, V)) = make_uint4(hi[e], hi[e + 1], hi[e + 2], hi[e + 3]);
+            fence_proxy_async_smem();
+            mbar_arrive_warp(&sm.Sout);
             // e^G dO, transposed
             const __nv_bfloat16 *dO = sm.dO[s][0];
 #pragma unroll
-            for (int t = 0; t < 32; t += 2) {
-                float g[2];
+            for (int t = 0; t < 16; ++t)
+                y[t] = c16 + t < m && live ? p.eG[c16 + t] * __bfloat162float(dO[op_off(c16 + t, r, kC)]) : 0.f;
+            uint32_t d[16];
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    g[e] = c32 + t + e < m && live ? p.eG[c32 + t + e] * __bfloat162float(dO[op_off(c32 + t + e, r, kC)]) : 0.f;
-                split_pair(g[0], g[1], y[t / 2], z[t / 2]);
-            }
-            tmem_st16(tl + cD + c32, y);
-            tmem_st16(tl + cD + c32 + 16, z);
-            tmem_wait_st();
-            tc_fence_before_sync();
-            mbar_arrive(&sm.dready);
+            for (int t = 0; t < 8; ++t) split_pair(y[2 * t], y[2 * t + 1], d[t], d[8 + t]);
             // dU
             if (!(ok = wait(sm.gfull, i))) break;
             tc_fence_after_sync();
-            uint32_t pa[32];
-            tmem_ld32(tl + cX + c32, x);
-            tmem_ld32(tl + cP + c32, pa);
-            tmem_wait_ld();
-            tmem_tie(x);
-            tmem_tie(pa);
+            {
+                uint32_t pa[16];
+                tmem_ld16(tl + cX + c16, x);
+                tmem_ld16(tl + cP + c16, pa);
+                tmem_wait_ld();
+                tmem_tie16(x);
+                tmem_tie16(pa);
 #pragma unroll
-            for (int t = 0; t < 32; t += 2) {
-                const float u0 = __uint_as_float(pa[t]) + p.eK[c32 + t] * __uint_as_float(x[t]);
-                const float u1 = __uint_as_float(pa[t + 1]) + p.eK[c32 + t + 1] * __uint_as_float(x[t + 1]);
-                split_pair(u0, u1, y[t / 2], z[t / 2]);
+                for (int t = 0; t < 16; ++t) y[t] = fmaf(p.eK[c16 + t], __uint_as_float(x[t]), __uint_as_float(pa[t]));
             }
-            tmem_st16(tl + cX + c32, y);   // over the columns of X that this thread has read
-            tmem_st16(tl + cX + c32 + 16, z);
+            put_split16(tl + cX + c16, y);
+            tmem_st16(tl + cD + c16, d);
             tmem_wait_st();
             tc_fence_before_sync();
-            mbar_arrive(&sm.uready);
+            mbar_arrive_warp(&sm.uready);
             // dY
             if (!(ok = wait(sm.yfull, i))) break;
             tc_fence_after_sync();
-            tmem_ld32(tl + cY + c32, x);
+            tmem_ld16(tl + cY + c16, x);
             tmem_wait_ld();
-            tmem_tie(x);
+            tmem_tie16(x);
+            float dv[16];
 #pragma unroll
-            for (int t = 0; t < 32; t += 2)
-                split_pair(-p.w[c32 + t] * p.eG[c32 + t] * __uint_as_float(x[t]),
-                           -p.w[c32 + t + 1] * p.eG[c32 + t + 1] * __uint_as_float(x[t + 1]), y[t / 2], z[t / 2]);
-            tmem_st16(tl + cY + c32, y);
-            tmem_st16(tl + cY + c32 + 16, z);
+            for (int t = 0; t < 16; ++t) {
+                dv[t] = p.w[c16 + t] * __uint_as_float(x[t]);
+                y[t] = -p.eG[c16 + t] * dv[t];
+            }
+            put_split16(tl + cY + c16, y);
             tmem_wait_st();
             tc_fence_before_sync();
-            float w[32];   // (the stage may be refilled after the arrival)
-#pragma unroll
-            for (int t = 0; t < 32; ++t) w[t] = p.w[c32 + t];
-            mbar_arrive(&sm.yready);
+            mbar_arrive_warp(&sm.yready);
             if (i > 0 && !(ok = wait(sm.yfree, i - 1))) break;
             if (live)
 #pragma unroll
-                for (int t = 0; t < 32; ++t) {
-                    const float dy = __uint_as_float(x[t]);
-                    sm.y[op_off(c32 + t, r, kC)] = __float2bfloat16_rn(dy);
-                    sm.dv[(c32 + t) * V + r] = __float2bfloat16_rn(w[t] * dy);
+                for (int t = 0; t < 16; ++t) {
+                    sm.y[op_off(c16 + t, r, kC)] = __float2bfloat16_rn(__uint_as_float(x[t]));
+                    sm.dv[(c16 + t) * V + r] = __float2bfloat16_rn(dv[t]);
                 }
             fence_proxy_async_smem();
-            mbar_arrive(&sm.yout);
+            mbar_arrive_warp(&sm.yout);
             // dS0
             if (!(ok = wait(sm.sfull, i))) break;
             tc_fence_after_sync();
-#pragma unroll
-            for (int x = 0; x < K / 2; x += 32) tmem_ld32(tl + x0 + x, reinterpret_cast<uint32_t *>(S) + x);
-            tmem_wait_ld();
-#pragma unroll
-            for (int x = 0; x < K / 2; x += 32) tmem_tie(reinterpret_cast<uint32_t *>(S) + x);
+            get_state<KQ>(tl + x0, S);
         }
-        if (ok && a.dS0 && live)
-#pragma unroll
-            for (int x = 0; x < K / 2; x += 4)
-                *reinterpret_cast<float4 *>(a.dS0 + st + x) = make_float4(S[x], S[x + 1], S[x + 2], S[x + 3]);
+        if (ok && a.dS0 && live) store_row<KQ>(a.dS0 + st, S);
     }
     if (!ok && lane == 0) atomicOr(&g_gdr_bwd_timeout, 1);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    if (warp == 9) tmem_dealloc(tm, 512);
+    if (warp == kRegWarps + 1) tmem_dealloc(tm, 512);
 }
 
 template <int K, int V>
@@ -344,7 +301,7 @@ struct GradSmem {
     __nv_bfloat16 qk[K / 64][128 * 64];     // Q, K
     __nv_bfloat16 P[192 * 64];              // zeros, P1, P2
     float vec[2][4][kC];                    // [stage]: e^G, e^{G_C - G}, w, G
-    float dg[2][128], dw[2][kC], kb[2][kC], tot[128], col[8][32], last[4];   // partial sums of a head
+    float dg[4][128], dw[4][kC], kb[4][kC], tot[3][128], col[4][kC], last[8];   // partial sums of a head
     uint64_t qkfull, qkfree, dfull[2], dfree[2], s0full, s0free, s1full, s1free, Dfull, Dfree, xfull, xfree, yfull, yfree,
         pready, pfull, afree, gready, gfree, drain;
     uint32_t tmem;
@@ -361,10 +318,12 @@ __device__ __forceinline__ float dot8(uint4 a, uint4 b, float acc) {
     return acc;
 }
 
-// lane l returns the sum over the warp's lanes of their x[l]
-__device__ __forceinline__ float column_sum(float (&x)[32], int lane) {
+// lane l returns the sum over the warp's lanes of their x[l % 16]
+__device__ __forceinline__ float column_sum(float (&x)[16], int lane) {
 #pragma unroll
-    for (int w = 16; w >= 1; w >>= 1) {
+    for (int i = 0; i < 16; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], 16);
+#pragma unroll
+    for (int w = 8; w >= 1; w >>= 1) {
         const bool up = lane & w;
 #pragma unroll
         for (int i = 0; i < w; ++i) {
@@ -375,29 +334,58 @@ __device__ __forceinline__ float column_sum(float (&x)[32], int lane) {
     return x[0];
 }
 
+// z = f times COLS columns of an accumulator (zero where f is not `here`'s): acc += f2 z, returns <z, row r of
+// [Q; K]>; `read` follows the last load
+template <int COLS, class F>
+__device__ __forceinline__ float product_row(uint32_t taddr, float f, float f2, bool here, const __nv_bfloat16 *qk, int r, int x0,
+                                             float *acc, F read) {
+    float d = 0.f;
+#pragma unroll
+    for (int b = 0; b < COLS; b += 16) {
+        uint32_t x[16];
+        tmem_ld16(taddr + b, x);
+        tmem_wait_ld();
+        tmem_tie16(x);
+        if (b + 16 == COLS) read();
+#pragma unroll
+        for (int i = 0; i < 16; i += 8) {
+            uint4 y = *reinterpret_cast<const uint4 *>(qk + op_off(r, x0 + b + i, 128));
+            if (!here) y = make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t yy[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float z = here ? f * __uint_as_float(x[i + e]) : 0.f;
+                d = fmaf(z, __uint_as_float(e % 2 ? yy[e / 2] & 0xffff0000u : yy[e / 2] << 16), d);
+                acc[b + i + e] = fmaf(f2, z, acc[b + i + e]);
+            }
+        }
+    }
+    return d;
+}
+
 template <int K, int V>
-__global__ void __launch_bounds__(352, 1)
+__global__ void __launch_bounds__(kSweepThreads, 1)
     gdr_tc_grad(GdrArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                 const __grid_constant__ CUtensorMap md) {
     extern __shared__ __align__(16) unsigned char raw[];
     typedef GradSmem<K, V> Smem;
     typedef GdrKeep<K, V> Keep;
     Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    constexpr int KH = K / 64, VH = V / 64;
+    constexpr int KH = K / 64, VH = V / 64, KQ = K / 4;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, share = a.Hv / a.Hk;
     if (threadIdx.x == 0) {
         for (uint64_t *b : {&sm.qkfull, &sm.dfull[0], &sm.dfull[1], &sm.s0full, &sm.s1full, &sm.Dfull, &sm.xfull, &sm.yfull,
                             &sm.pfull, &sm.gfree, &sm.drain})
             mbar_init(b, 1);
-        for (uint64_t *b : {&sm.Dfree, &sm.xfree, &sm.pready, &sm.afree, &sm.gready}) mbar_init(b, 256);
-        for (uint64_t *b : {&sm.qkfree, &sm.dfree[0], &sm.dfree[1]}) mbar_init(b, 257);   // readers and the products
-        for (uint64_t *b : {&sm.s0free, &sm.s1free}) mbar_init(b, 129);
-        mbar_init(&sm.yfree, 128);
+        for (uint64_t *b : {&sm.Dfree, &sm.xfree, &sm.pready, &sm.afree, &sm.gready}) mbar_init(b, kRegWarps);
+        for (uint64_t *b : {&sm.qkfree, &sm.dfree[0], &sm.dfree[1]}) mbar_init(b, kRegWarps + 1);   // readers and the products
+        for (uint64_t *b : {&sm.s0free, &sm.s1free}) mbar_init(b, kRegWarps / 2 + 1);
+        mbar_init(&sm.yfree, kRegWarps / 2);
         fence_mbar_init();
     }
     for (int i = threadIdx.x; i < kC * 8; i += blockDim.x) reinterpret_cast<uint4 *>(sm.P)[i] = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
-    if (warp == 9) tmem_alloc(&sm.tmem, 512);
+    if (warp == kRegWarps + 1) tmem_alloc(&sm.tmem, 512);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
@@ -410,7 +398,8 @@ __global__ void __launch_bounds__(352, 1)
     const long long items = a.seq.n_tiles(kC) * a.Hk;
     int it = 0, j = 0;   // items and heads so far (those of used tiles)
 
-    if (warp == 8) {
+    if (warp >= kRegWarps) regs_down<64>();
+    if (warp == kRegWarps) {
         for (long long w = blockIdx.x; w < items && ok; w += gridDim.x) {
             const int tile = (int)(w / a.Hk), hk = (int)(w % a.Hk);
             int n, c, len;
@@ -465,7 +454,7 @@ __global__ void __launch_bounds__(352, 1)
             wait(sm.s0full, j);
             wait(sm.s1full, j);
         }
-    } else if (warp == 9) {
+    } else if (warp == kRegWarps + 1) {
         constexpr uint32_t iN64 = umma_idesc_bf16(128, 64), iK = umma_idesc_bf16(128, K) | kUmmaBmn;
         const uint32_t P = smem_u32(sm.P), qk = smem_u32(sm.qk[0]);
         for (long long w = blockIdx.x; w < items && ok; w += gridDim.x) {
@@ -526,7 +515,7 @@ __global__ void __launch_bounds__(352, 1)
                         umma_bf16(tm + cY, umma_desc(d + kTile64 + 3 * kTile64 * (kk / 4) + 32 * (kk % 4)),
                                   umma_desc_mn(smem_u32(sm.S1) + 2048 * kk, V * 128), iK, kk > 0);
                     umma_commit(&sm.yfull);
-                    umma_commit(&sm.s1free);
+                umma_commit(&sm.s1free);
                     umma_commit(&sm.dfree[s]);
                 }
                 __syncwarp();
@@ -556,7 +545,7 @@ __global__ void __launch_bounds__(352, 1)
         if (lane == 0) umma_commit(&sm.drain);
         __syncwarp();
         wait(sm.drain, 0);
-    } else if (warp == 10) {
+    } else if (warp == kRegWarps + 2) {
         // gate gradients from the partial sums: lane = tokens lane and lane + 32.  The gradient of log a_t
         // is the sum over every path that crosses the decay of token t, each term as it is (rows minus
         // columns of a cumulative sum would cancel): queries and keys r >= t that read the start state,
@@ -585,40 +574,49 @@ __global__ void __launch_bounds__(352, 1)
                     w[e] = sigmoid_f(ld_io(static_cast<const __nv_bfloat16 *>(a.w_logit) + at));
                 }
                 if (!(ok = wait(sm.gready, j))) break;
-                float G[2], B[2], dw[2], T[2], C[2];   // row sums; sums of key rows; ...; pairs: row totals of s < 32, columns
+                // row sums; sums of key rows; write gate; columns of the pairs; row totals of the first 16, 32, 48 pairs
+                float G[2], B[2], dw[2], C[2], T[3][2], last = 0.f;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int t = lane + 32 * e;
-                    G[e] = sm.dg[0][t] + sm.dg[1][t] + sm.dg[0][t + 64] + sm.dg[1][t + 64];
-                    B[e] = sm.kb[0][t] + sm.kb[1][t];
-                    dw[e] = sm.dw[0][t] + sm.dw[1][t];
-                    T[e] = sm.tot[t] + sm.tot[t + 64];
-                    C[e] = sm.col[4 * e][lane] + sm.col[4 * e + 1][lane] + sm.col[4 * e + 2][lane] + sm.col[4 * e + 3][lane];
+                    G[e] = B[e] = dw[e] = C[e] = 0.f;
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        G[e] += sm.dg[p][t] + sm.dg[p][t + 64];
+                        B[e] += sm.kb[p][t];
+                        dw[e] += sm.dw[p][t];
+                        C[e] += sm.col[p][t];
+                    }
+#pragma unroll
+                    for (int p = 0; p < 3; ++p) T[p][e] = sm.tot[p][t] + sm.tot[p][t + 64];
                 }
-                const float last = sm.last[0] + sm.last[1] + sm.last[2] + sm.last[3];
+#pragma unroll
+                for (int p = 0; p < 8; ++p) last += sm.last[p];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.gfree);
-                // suffix sums of G (over 64) and of T (over its upper half), exclusive prefix of B
+                // suffix sums of G and the T, exclusive prefix of B
 #pragma unroll
                 for (int off = 1; off < 32; off <<= 1) {
-                    const float g0 = __shfl_down_sync(0xffffffffu, G[0], off), g1 = __shfl_down_sync(0xffffffffu, G[1], off);
-                    const float t1 = __shfl_down_sync(0xffffffffu, T[1], off);
-                    const float b0 = __shfl_up_sync(0xffffffffu, B[0], off), b1 = __shfl_up_sync(0xffffffffu, B[1], off);
-                    if (lane + off < 32) {
-                        G[0] += g0;
-                        G[1] += g1;
-                        T[1] += t1;
-                    }
-                    if (lane >= off) {
-                        B[0] += b0;
-                        B[1] += b1;
+                    const bool down = lane + off < 32;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float g1 = __shfl_down_sync(0xffffffffu, G[e], off), b1 = __shfl_up_sync(0xffffffffu, B[e], off);
+                        G[e] += down ? g1 : 0.f;
+                        B[e] += lane >= off ? b1 : 0.f;
+#pragma unroll
+                        for (int p = 0; p < 3; ++p) {
+                            const float t1 = __shfl_down_sync(0xffffffffu, T[p][e], off);
+                            T[p][e] += down ? t1 : 0.f;
+                        }
                     }
                 }
-                const float all1 = __shfl_sync(0xffffffffu, G[1], 0), all0 = __shfl_sync(0xffffffffu, B[0], 31);
+                G[0] += __shfl_sync(0xffffffffu, G[1], 0);
+                const float t0 = __shfl_sync(0xffffffffu, T[0][1], 0), all0 = __shfl_sync(0xffffffffu, B[0], 31);
                 float b0 = __shfl_up_sync(0xffffffffu, B[0], 1), b1 = __shfl_up_sync(0xffffffffu, B[1], 1);
                 b0 = lane ? b0 : 0.f;
                 b1 = (lane ? b1 : 0.f) + all0;
-                const float gr[2] = {G[0] + all1 + b0 + last + C[0], G[1] + b1 + last + C[1] + T[1]};
+                const float gr[2] = {G[0] + b0 + last + C[0] + (lane >= 16 ? T[0][0] + t0 : 0.f),
+                                     G[1] + b1 + last + C[1] + T[0][1] + T[1][1] + (lane >= 16 ? T[2][1] : 0.f)};
                 float dlog = 0.f, damp = 0.f;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -645,50 +643,44 @@ __global__ void __launch_bounds__(352, 1)
                 }
             }
         }
-    } else {
-        const int half = warp / 4, quarter = warp % 4, r = quarter * 32 + lane, t = r % kC;
+    } else if (warp < kRegWarps) {
+        regs_up<104>();
+        const int part = warp / 4, quarter = warp % 4, r = quarter * 32 + lane, t = r % kC;
         const bool key = r >= kC;   // lane of a key (the same for a whole warp)
         const uint32_t tl = tm + ((uint32_t)quarter << 21);
-        const int x0 = half * (K / 2), s0 = half * 32, v0 = half * (V / 2);
-        float acc[K / 2];
+        const int x0 = part * KQ, s0 = part * 16, v0 = part * (V / 4);
+        float acc[KQ];
         for (long long wk = blockIdx.x; wk < items && ok; wk += gridDim.x) {
             const int tile = (int)(wk / a.Hk), hk = (int)(wk % a.Hk);
             int n, c, len;
             long long row;
             if (!a.seq.find(tile, kC, n, c, row, len)) continue;
             row += (long long)c * kC;
-            const int m = min(kC, len - c * kC);
-            const bool here = t < m;
+            const bool here = t < len - c * kC;
 #pragma unroll
-            for (int x = 0; x < K / 2; ++x) acc[x] = 0.f;
+            for (int x = 0; x < KQ; ++x) acc[x] = 0.f;
             for (int g = 0; g < share && ok; ++g, ++j) {
                 const int s = j & 1, h = hk * share + g;
-                uint4 v[V / 16];   // this key's values, half of the channels
-#pragma unroll
-                for (int i = 0; i < V / 16; ++i)
-                    v[i] = key && here ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.v) +
-                                                                              ((size_t)(row + t) * a.Hv + h) * V + v0) + i)
-                                       : make_uint4(0u, 0u, 0u, 0u);
                 if (!(ok = wait(sm.dfull[s], j / 2))) break;
-                const float *eG = sm.vec[s][0], *eK = sm.vec[s][1], *vw = sm.vec[s][2], *G = sm.vec[s][3];
-                const float wt = vw[t];
+                const float *eG = sm.vec[s][0], *eK = sm.vec[s][1], *G = sm.vec[s][3];
+                const float wt = sm.vec[s][2][t];
                 float dw = 0.f, dg, kb = 0.f, run = 0.f;
                 // pairs of the chunk
                 if (!(ok = wait(sm.Dfull, j))) break;
                 tc_fence_after_sync();
                 {
-                    uint32_t D[32], kk[32], p[16];
-                    tmem_ld32(tl + cD + s0, D);
-                    tmem_ld32(tl + cKK + s0, kk);
+                    uint32_t D[16], kk[16], p[8];
+                    tmem_ld16(tl + cD + s0, D);
+                    tmem_ld16(tl + cKK + s0, kk);
                     tmem_wait_ld();
-                    tmem_tie(D);
-                    tmem_tie(kk);
+                    tmem_tie16(D);
+                    tmem_tie16(kk);
                     tc_fence_before_sync();
-                    mbar_arrive(&sm.Dfree);
+                    mbar_arrive_warp(&sm.Dfree);
                     const float Gt = G[t];
-                    float pr[32];
+                    float pr[16];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
+                    for (int e = 0; e < 16; ++e) {
                         const int u = s0 + e;
                         const bool below = here && u < t;
                         float y = below || (here && !key && u == t) ? __expf(Gt - G[u]) * __uint_as_float(D[e]) : 0.f;
@@ -702,123 +694,95 @@ __global__ void __launch_bounds__(352, 1)
                         D[e] = __float_as_uint(y);
                     }
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) p[e] = pack_bf16(__uint_as_float(D[2 * e]), __uint_as_float(D[2 * e + 1]));
+                    for (int e = 0; e < 8; ++e) p[e] = pack_bf16(__uint_as_float(D[2 * e]), __uint_as_float(D[2 * e + 1]));
                     if (j > 0 && !(ok = wait(sm.pfull, j - 1))) break;
 #pragma unroll
-                    for (int e = 0; e < 16; e += 4)
+                    for (int e = 0; e < 8; e += 4)
                         *reinterpret_cast<uint4 *>(sm.P + kC * 64 + op_off(r, s0 + 2 * e, 128)) = make_uint4(p[e], p[e + 1], p[e + 2], p[e + 3]);
                     fence_proxy_async_smem();
-                    mbar_arrive(&sm.pready);
+                    mbar_arrive_warp(&sm.pready);
                     // sums over s before u, for u up to t; then over the warp's tokens
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
+                    for (int e = 0; e < 16; ++e) {
                         const float y = pr[e];
                         pr[e] = s0 + e <= t ? run : 0.f;
                         run += y;
                     }
                     const float cs = column_sum(pr, lane);
                     if (j > 0 && !(ok = wait(sm.gfree, j - 1))) break;
-                    sm.col[warp][lane] = cs;
-                    if (half == 0) sm.tot[r] = run;
+                    if (lane < 16) sm.col[quarter][s0 + lane] = cs;
+                    if (part < 3) sm.tot[part][r] = run;
                 }
+                uint4 v[V / 32];   // this key's values, a quarter of the channels
+#pragma unroll
+                for (int i = 0; i < V / 32; ++i)
+                    v[i] = key && here ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.v) +
+                                                                              ((size_t)(row + t) * a.Hv + h) * V + v0) + i)
+                                       : make_uint4(0u, 0u, 0u, 0u);
                 // start state
                 if (!(ok = wait(sm.xfull, j))) break;
                 tc_fence_after_sync();
                 {
-                    uint32_t x[K / 2];
-#pragma unroll
-                    for (int i = 0; i < K / 2; i += 32) tmem_ld32(tl + cX + x0 + i, x + i);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < K / 2; i += 32) tmem_tie(x + i);
-                    tc_fence_before_sync();
-                    mbar_arrive(&sm.xfree);
-                    const float f = eG[t], f2 = key ? -wt : 1.f;
-                    float d = 0.f;
-#pragma unroll
-                    for (int i = 0; i < K / 2; i += 8) {
-                        const uint4 y = *reinterpret_cast<const uint4 *>(sm.qk[0] + op_off(r, x0 + i, 128));
-                        const uint32_t yy[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float z = here ? f * __uint_as_float(x[i + e]) : 0.f;
-                            const float b = __uint_as_float(e % 2 ? yy[e / 2] & 0xffff0000u : yy[e / 2] << 16);
-                            d = fmaf(z, here ? b : 0.f, d);
-                            acc[i + e] = fmaf(f2, z, acc[i + e]);
-                        }
-                    }
+                    const float f = here ? eG[t] : 0.f, f2 = key ? -wt : 1.f;
+                    const float d = product_row<KQ>(tl + cX + x0, f, f2, here, sm.qk[0], r, x0, acc, [&] {
+                        tc_fence_before_sync();
+                        mbar_arrive_warp(&sm.xfree);
+                    });
                     dg = f2 * d;
                     dw -= d;
                 }
                 if (key) {   // end state; the values
                     if (!(ok = wait(sm.yfull, j))) break;
                     tc_fence_after_sync();
-                    uint32_t x[K / 2];
+                    kb = product_row<KQ>(tl + cY + x0, here ? eK[t] : 0.f, 1.f, here, sm.qk[0], r, x0, acc, [&] {
+                        tc_fence_before_sync();
+                        mbar_arrive_warp(&sm.yfree);
+                    });
 #pragma unroll
-                    for (int i = 0; i < K / 2; i += 32) tmem_ld32(tl + cY + x0 + i, x + i);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < K / 2; i += 32) tmem_tie(x + i);
-                    tc_fence_before_sync();
-                    mbar_arrive(&sm.yfree);
-                    const float f = here ? eK[t] : 0.f;
-#pragma unroll
-                    for (int i = 0; i < K / 2; i += 8) {
-                        const uint4 y = *reinterpret_cast<const uint4 *>(sm.qk[0] + op_off(r, x0 + i, 128));
-                        const uint32_t yy[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float z = f * __uint_as_float(x[i + e]);
-                            const float b = __uint_as_float(e % 2 ? yy[e / 2] & 0xffff0000u : yy[e / 2] << 16);
-                            kb = fmaf(z, here ? b : 0.f, kb);
-                            acc[i + e] += z;
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < V / 16; ++i)
+                    for (int i = 0; i < V / 32; ++i)
                         dw = dot8(*reinterpret_cast<const uint4 *>(sm.d[s][0] + op_off(r, v0 + 8 * i, 192)), v[i], dw);
-                    sm.dw[half][t] = dw;
-                    sm.kb[half][t] = kb;
+                    sm.dw[part][t] = dw;
+                    sm.kb[part][t] = kb;
                 } else {   // <S0, dS1>: both are laid out alike
                     if (!(ok = wait(sm.s0full, j))) break;
                     if (!(ok = wait(sm.s1full, j))) break;
-                    const int at = half * 64 + quarter * 32 + lane;
+                    const int at = part * 64 + quarter * 32 + lane;
                     float y = 0.f;
 #pragma unroll 4
-                    for (int i = at; i < V * K / 8; i += 128)
+                    for (int i = at; i < V * K / 8; i += 256)
                         y = dot8(reinterpret_cast<const uint4 *>(sm.S0)[i], reinterpret_cast<const uint4 *>(sm.S1)[i], y);
-                    mbar_arrive(&sm.s0free);
-                    mbar_arrive(&sm.s1free);
+                    mbar_arrive_warp(&sm.s0free);
+                    mbar_arrive_warp(&sm.s1free);
 #pragma unroll
                     for (int off = 16; off >= 1; off >>= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
-                    if (lane == 0) sm.last[half * 2 + quarter] = y * eG[kC - 1];
+                    if (lane == 0) sm.last[part * 2 + quarter] = y * eG[kC - 1];
                 }
-                sm.dg[half][r] = dg;
-                mbar_arrive(&sm.gready);
-                mbar_arrive(&sm.dfree[s]);
-                if (g == share - 1) mbar_arrive(&sm.qkfree);
+                sm.dg[part][r] = dg;
+                mbar_arrive_warp(&sm.gready);
+                mbar_arrive_warp(&sm.dfree[s]);
+                if (g == share - 1) mbar_arrive_warp(&sm.qkfree);
             }
             if (!ok) break;
             if (!(ok = wait(sm.pfull, j - 1))) break;
             tc_fence_after_sync();
-            uint32_t x[K / 2];
+            uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(key ? a.dk : a.dq) +
+                                                   ((size_t)(row + t) * a.Hk + hk) * K + x0);
 #pragma unroll
-            for (int i = 0; i < K / 2; i += 32) tmem_ld32(tl + cA + x0 + i, x + i);
-            tmem_wait_ld();
+            for (int b = 0; b < KQ; b += 16) {
+                uint32_t x[16], o[8];
+                tmem_ld16(tl + cA + x0 + b, x);
+                tmem_wait_ld();
+                tmem_tie16(x);
+                if (b + 16 == KQ) {
+                    tc_fence_before_sync();
+                    mbar_arrive_warp(&sm.afree);
+                }
 #pragma unroll
-            for (int i = 0; i < K / 2; i += 32) tmem_tie(x + i);
-            tc_fence_before_sync();
-            mbar_arrive(&sm.afree);
-            if (here) {
-                uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(key ? a.dk : a.dq) +
-                                                       ((size_t)(row + t) * a.Hk + hk) * K + x0);
-#pragma unroll
-                for (int i = 0; i < K / 2; i += 8) {
-                    uint32_t o[4];
-#pragma unroll
-                    for (int e = 0; e < 8; e += 2)
-                        o[e / 2] = pack_bf16(acc[i + e] + __uint_as_float(x[i + e]), acc[i + e + 1] + __uint_as_float(x[i + e + 1]));
-                    out[i / 8] = make_uint4(o[0], o[1], o[2], o[3]);
+                for (int e = 0; e < 16; e += 2)
+                    o[e / 2] = pack_bf16(acc[b + e] + __uint_as_float(x[e]), acc[b + e + 1] + __uint_as_float(x[e + 1]));
+                if (here) {
+                    out[b / 8] = make_uint4(o[0], o[1], o[2], o[3]);
+                    out[b / 8 + 1] = make_uint4(o[4], o[5], o[6], o[7]);
                 }
             }
             ++it;
@@ -828,7 +792,7 @@ __global__ void __launch_bounds__(352, 1)
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    if (warp == 9) tmem_dealloc(tm, 512);
+    if (warp == kRegWarps + 1) tmem_dealloc(tm, 512);
 }
 
 template <int K, int V>
@@ -846,9 +810,9 @@ cudaError_t bwd_t(const GdrArgs &a, cudaStream_t st) {
         if (e == cudaSuccess) e = make_operand_tile_map(&md, a.dO, V, a.Hv, rows, kC);
     }
     if (e != cudaSuccess) return e;
-    sweep<<<a.seq.N * a.Hv, 352, sb, st>>>(a, mq, mk, md);
+    sweep<<<a.seq.N * a.Hv, kSweepThreads, sb, st>>>(a, mq, mk, md);
     const long long tiles = a.seq.n_tiles(kC), items = tiles * a.Hk;
-    if (items) grad<<<(unsigned)(items < sm_count() ? items : sm_count()), 352, gb, st>>>(a, mq, mk, md);
+    if (items) grad<<<(unsigned)(items < sm_count() ? items : sm_count()), kSweepThreads, gb, st>>>(a, mq, mk, md);
     if (a.dA_dec || a.dtau)
         launch_gdr_reduce_decay(reinterpret_cast<const float *>(a.ws + (size_t)tiles * a.Hv * sizeof(GdrKeep<K, V>)), tiles, a.Hv,
                                 a.dA_dec, a.dtau, st);

@@ -7,14 +7,15 @@
 // gdr_tc_sweep: one CTA per (sequence, value head) carries the state through the chunks.  The state is
 // a tensor-memory accumulator with the value channels as its 128 lanes, so every product of the
 // recurrence has A in tensor memory (what the last step produced) and B in shared memory (K, Q, Tm or
-// A as copied), and a thread owns half a state row:
+// A as copied), and a thread owns a quarter of a state row:
 //   G = S K^T (hi, lo), Q S^T       -> R = w (v - e^G G), split
 //   U = R Tm^T (three terms)        -> e^{G_C - G} U, split; U
 //   S += (e^{G_C - G} U) K (hi, lo)  -> S split for the next chunk, S scaled by its e^{G_C}
-//   O = e^G Q S^T + U A^T            off the chain
+//   O = e^G Q S^T + U A^T (S, U hi, lo), two accumulators, off the chain
 // The chain of one chunk is three products and three register passes; what bounds the sweep is
 // their latency (B H units on 148 SMs, one chain each), not the tensor core's rate or HBM.
-// Warps 0-7 register passes, 8 copies in (TMA and bulk, two stages), 9 products, 10 copies out.
+// Warps 0-15 register passes, 16 copies in (TMA and bulk, two stages), 17 products, 18 copies out.  What
+// is not on the chain (outputs of the chunk before, copies of S and U) is done while a product runs.
 #include "carve_gdr_tc.cuh"
 
 namespace carve {
@@ -276,19 +277,20 @@ struct SweepSmem {
     GdrPrep p[2];
     __nv_bfloat16 v[2][kC * V];                     // plain rows
     __nv_bfloat16 S[SAVE ? V * K : 8], u[SAVE ? kC * V : 8], o[kC * V];   // on their way out
-    uint64_t full[2], free[2], sready, gfull, qfull, rready, ufull, uready, sfull, ofull, ofree;
-    uint64_t Sout, Sfree, uout, ufree, oout;
+    float eG[2][kC];   // kept for the outputs beyond the stage
+    uint64_t full[2], free[2], sready, gfull, rready, ufull, uready, sfull, ofull, oread, ofree;
+    uint64_t Sout, Sfree, uout, ufree, oout, drain;
     uint32_t tmem;
 };
 
 template <int K, int V, bool SAVE>
-__global__ void __launch_bounds__(352, 1)
+__global__ void __launch_bounds__(kSweepThreads, 1)
     gdr_tc_sweep(GdrArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                  const __grid_constant__ CUtensorMap mv) {
     extern __shared__ __align__(16) unsigned char raw[];
     typedef SweepSmem<K, V, SAVE> Smem;
     Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    constexpr int KH = K / 64;
+    constexpr int KH = K / 64, KQ = K / 4;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int h = blockIdx.x % a.Hv, n = blockIdx.x / a.Hv, hk = h / (a.Hv / a.Hk);
     long long row0;
@@ -297,26 +299,27 @@ __global__ void __launch_bounds__(352, 1)
     const long long t0 = a.seq.tile0(n, kC);
     const int chunks = (len + kC - 1) / kC;
     if (threadIdx.x == 0) {
-        for (uint64_t *b : {&sm.full[0], &sm.full[1], &sm.free[0], &sm.free[1], &sm.gfull, &sm.qfull, &sm.ufull, &sm.sfull,
-                            &sm.ofull, &sm.Sfree, &sm.ufree, &sm.ofree})
+        for (uint64_t *b : {&sm.full[0], &sm.full[1], &sm.free[0], &sm.free[1], &sm.gfull, &sm.ufull, &sm.sfull,
+                            &sm.ofull, &sm.Sfree, &sm.ufree, &sm.ofree, &sm.drain})
             mbar_init(b, 1);
-        for (uint64_t *b : {&sm.sready, &sm.rready, &sm.uready, &sm.Sout, &sm.uout, &sm.oout}) mbar_init(b, 256);
+        for (uint64_t *b : {&sm.sready, &sm.rready, &sm.uready, &sm.oread, &sm.Sout, &sm.uout, &sm.oout}) mbar_init(b, kRegWarps);
         fence_mbar_init();
     }
-    if (warp == 9) tmem_alloc(&sm.tmem, 512);
+    if (warp == kRegWarps + 1) tmem_alloc(&sm.tmem, 512);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tm = sm.tmem;
-    // tensor memory: S 0-127, S hi 128, S lo 192, G (then R hi, lo) 256, Q S (then O) 320, U (then
-    // e^{G_C - G} U hi, lo) 384, U as bf16 448
-    constexpr uint32_t cHi = 128, cLo = 192, cG = 256, cO = 320, cU = 384, cUb = 448;
+    // tensor memory: S 0-127, S hi 128, S lo 192, G (then R hi, lo, then U hi, lo) 256, U (then
+    // e^{G_C - G} U hi, lo) 320, Q S^T 384, U A^T 448
+    constexpr uint32_t cHi = 128, cLo = 192, cG = 256, cU = 320, cQ = 384, cA = 448;
     bool ok = true;
     auto wait = [&](uint64_t &bar, int phase) {   // by a whole warp
         return (bool)__all_sync(0xffffffffu, mbar_wait(&bar, phase & 1, kSwaWait));
     };
 
-    if (warp == 8) {
+    if (warp >= kRegWarps) regs_down<64>();
+    if (warp == kRegWarps) {
         int c = 0;
         for (; c < chunks; ++c) {
             const int s = c & 1;
@@ -334,10 +337,9 @@ __global__ void __launch_bounds__(352, 1)
         }
         if (!ok)
             for (int i = max(0, c - 2); i < c; ++i) wait(sm.full[i & 1], i / 2);
-    } else if (warp == 9) {
+    } else if (warp == kRegWarps + 1) {
         constexpr uint32_t iN64 = umma_idesc_bf16(128, 64), iS = umma_idesc_bf16(128, K) | kUmmaBmn;
-        int c = 0;
-        for (; c < chunks; ++c) {
+        for (int c = 0; c < chunks; ++c) {
             const int s = c & 1;
             if (!(ok = wait(sm.full[s], c / 2))) break;
             if (len - c * kC < kC) {   // key rows behind the end meet U = 0 in the state update
@@ -357,15 +359,6 @@ __global__ void __launch_bounds__(352, 1)
                 umma_commit(&sm.gfull);
             }
             __syncwarp();
-            if (c > 0 && !(ok = wait(sm.ofree, c - 1))) break;
-            tc_fence_after_sync();
-            if (lane == 0) {
-#pragma unroll
-                for (int kk = 0; kk < K / 16; ++kk)
-                    umma_bf16_ta(tm + cO, tm + cHi + 8 * kk, umma_desc(smem_u32(sm.q[s][kk / 4]) + 32 * (kk % 4)), iN64, kk > 0);
-                umma_commit(&sm.qfull);
-            }
-            __syncwarp();
             if (!(ok = wait(sm.rready, c))) break;
             tc_fence_after_sync();
             if (lane == 0) {
@@ -374,9 +367,21 @@ __global__ void __launch_bounds__(352, 1)
                 for (int x = 0; x < 3; ++x)   // R hi Tm hi, R lo Tm hi, R hi Tm lo
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        umma_bf16_ta(tm + cU, tm + cG + half_col(kk) + (x == 1 ? 16 : 0), umma_desc((x == 2 ? tl : th) + 32 * kk), iN64,
+                        umma_bf16_ta(tm + cU, tm + cG + split_col(kk, x == 1), umma_desc((x == 2 ? tl : th) + 32 * kk), iN64,
                                      x > 0 || kk > 0);
                 umma_commit(&sm.ufull);
+            }
+            __syncwarp();
+            // in the shadow of the pass over U
+            if (c > 0 && !(ok = wait(sm.oread, c - 1))) break;
+            tc_fence_after_sync();
+            if (lane == 0) {
+#pragma unroll
+                for (int lo = 0; lo < 2; ++lo)
+#pragma unroll
+                    for (int kk = 0; kk < K / 16; ++kk)
+                        umma_bf16_ta(tm + cQ, tm + (lo ? cLo : cHi) + 8 * kk, umma_desc(smem_u32(sm.q[s][kk / 4]) + 32 * (kk % 4)),
+                                     iN64, lo > 0 || kk > 0);
             }
             __syncwarp();
             if (!(ok = wait(sm.uready, c))) break;
@@ -386,196 +391,157 @@ __global__ void __launch_bounds__(352, 1)
                 for (int lo = 0; lo < 2; ++lo)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        umma_bf16_ta(tm, tm + cU + half_col(kk) + 16 * lo, umma_desc_mn(smem_u32(sm.k[s][0]) + 2048 * kk, kTile64), iS, 1);
+                        umma_bf16_ta(tm, tm + cU + split_col(kk, lo), umma_desc_mn(smem_u32(sm.k[s][0]) + 2048 * kk, kTile64), iS, 1);
                 umma_commit(&sm.sfull);
                 const uint32_t A = smem_u32(sm.p[s].A);
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) umma_bf16_ta(tm + cO, tm + cUb + 8 * kk, umma_desc(A + 32 * kk), iN64, 1);
+                for (int lo = 0; lo < 2; ++lo)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) 
+                        umma_bf16_ta(tm + cA, tm + cG + split_col(kk, lo), umma_desc(A + 32 * kk), iN64, lo > 0 || kk > 0);
                 umma_commit(&sm.ofull);
                 umma_commit(&sm.free[s]);
             }
             __syncwarp();
         }
-        // products in flight finish before the tensor memory is freed
-        if (!ok)
-            for (uint64_t *b : {&sm.gfull, &sm.qfull, &sm.ufull, &sm.sfull, &sm.ofull}) {
-                if (c > 0) wait(*b, c - 1);
-                wait(*b, c);
-            }
-    } else if (warp == 10) {
+        if (lane == 0) umma_commit(&sm.drain);   // products in flight finish before the tensor memory is freed
+        __syncwarp();
+        wait(sm.drain, 0);
+    } else if (warp == kRegWarps + 2) {
         typedef GdrKeep<K, V> Keep;
         Keep *keep = SAVE ? reinterpret_cast<Keep *>(a.saved) + (size_t)t0 * a.Hv + h : nullptr;
-        for (int c = 0; c < chunks && ok; ++c) {
-            if (SAVE) {
+        for (int c = 0; c <= chunks && ok; ++c) {
+            if (c > 0) {   // outputs of the chunk before
+                if (!(ok = wait(sm.oout, c - 1))) break;
+                for (int t = lane; t < min(kC, len - (c - 1) * kC); t += 32)
+                    bulk_s2g(static_cast<__nv_bfloat16 *>(a.o) + ((size_t)(row0 + (long long)(c - 1) * kC + t) * a.Hv + h) * V,
+                             sm.o + t * V, V * 2);
+                bulk_commit();
+            }
+            if (SAVE && c < chunks) {
                 if (!(ok = wait(sm.Sout, c))) break;
                 if (lane == 0) {
                     bulk_s2g(keep[(size_t)c * a.Hv].S, sm.S, sizeof(sm.S));
                     bulk_commit();
                 }
+                __syncwarp();
                 if (!(ok = wait(sm.uout, c))) break;
                 if (lane == 0) {
                     bulk_s2g(keep[(size_t)c * a.Hv].x, sm.u, sizeof(sm.u));
                     bulk_commit();
-                    bulk_wait_read<1>();
-                    mbar_arrive(&sm.Sfree);
                 }
-                __syncwarp();
             }
-            if (!(ok = wait(sm.oout, c))) break;
-            for (int t = lane; t < min(kC, len - c * kC); t += 32)
-                bulk_s2g(static_cast<__nv_bfloat16 *>(a.o) + ((size_t)(row0 + (long long)c * kC + t) * a.Hv + h) * V, sm.o + t * V,
-                         V * 2);
-            bulk_commit();
             bulk_wait_read<0>();
             __syncwarp();
             if (lane == 0) {
-                if (SAVE) mbar_arrive(&sm.ufree);
-                mbar_arrive(&sm.ofree);
+                if (c > 0) mbar_arrive(&sm.ofree);
+                if (SAVE && c < chunks) {
+                    mbar_arrive(&sm.Sfree);
+                    mbar_arrive(&sm.ufree);
+                }
             }
         }
         bulk_wait<0>();
-    } else {
-        const int half = warp / 4, quarter = warp % 4, r = quarter * 32 + lane;
+    } else if (warp < kRegWarps) {
+        regs_up<104>();
+        const int part = warp / 4, quarter = warp % 4, r = quarter * 32 + lane;
         const uint32_t tl = tm + ((uint32_t)quarter << 21);
-        const int x0 = half * (K / 2), c32 = half * 32;   // this thread's columns of S, its tokens
-        const bool live = r < V;                          // value row (others carry zeros)
+        const int x0 = part * KQ, c16 = part * 16;   // this thread's columns of S, its tokens
+        const bool live = r < V;                     // value row (others carry zeros)
         const size_t st = (((size_t)n * a.Hv + h) * V + (live ? r : 0)) * K + x0;
-        float S[K / 2];
-#pragma unroll
-        for (int x = 0; x < K / 2; x += 4) {
-            const float4 y = live && a.S0 ? *reinterpret_cast<const float4 *>(a.S0 + st + x) : make_float4(0.f, 0.f, 0.f, 0.f);
-            S[x] = y.x;
-            S[x + 1] = y.y;
-            S[x + 2] = y.z;
-            S[x + 3] = y.w;
-        }
-        // S (in registers) as the operands of chunk c, scaled accumulator, and its copy out
-        auto put_state = [&](int c) {
-            if (!(ok = wait(sm.full[c & 1], c / 2))) return;
-            const float gl = sm.p[c & 1].eG[kC - 1];
-            uint32_t hi[K / 4], lo[K / 4], sc[K / 2];
-#pragma unroll
-            for (int x = 0; x < K / 4; ++x) split_pair(S[2 * x], S[2 * x + 1], hi[x], lo[x]);
-#pragma unroll
-            for (int x = 0; x < K / 2; ++x) sc[x] = __float_as_uint(S[x] * gl);
-#pragma unroll
-            for (int x = 0; x < K / 4; x += 16) {
-                tmem_st16(tl + cHi + x0 / 2 + x, hi + x);
-                tmem_st16(tl + cLo + x0 / 2 + x, lo + x);
+        float S[KQ];
+        load_row<KQ>(S, live && a.S0 ? a.S0 + st : nullptr);
+        uint32_t x[16];
+        for (int c = 0; c <= chunks; ++c) {
+            const GdrPrep &p = sm.p[c & 1];
+            uint32_t hi[KQ / 2];
+            if (c < chunks) {
+                if (!(ok = wait(sm.full[c & 1], c / 2))) break;
+                put_state<KQ>(tl + x0, tl + cHi + x0 / 2, tl + cLo + x0 / 2, S, p.eG[kC - 1], hi);
+                mbar_arrive_warp(&sm.sready);
             }
-#pragma unroll
-            for (int x = 0; x < K / 2; x += 32) tmem_st32(tl + x0 + x, sc + x);
-            tmem_wait_st();
-            tc_fence_before_sync();
-            mbar_arrive(&sm.sready);
-            if (SAVE) {
-                if (c > 0 && !(ok = wait(sm.Sfree, c - 1))) return;
+            if (c > 0) {   // outputs of the chunk before, while the product runs
+                const float *eG = sm.eG[(c - 1) & 1] + c16;
+                if (!(ok = wait(sm.ofull, c - 1))) break;
+                tc_fence_after_sync();
+                uint32_t z[16];
+                tmem_ld16(tl + cQ + c16, x);
+                tmem_ld16(tl + cA + c16, z);
+                tmem_wait_ld();
+                tmem_tie16(x);
+                tmem_tie16(z);
+                tc_fence_before_sync();
+                mbar_arrive_warp(&sm.oread);
+                if (c > 1 && !(ok = wait(sm.ofree, c - 2))) break;
                 if (live)
 #pragma unroll
-                    for (int x = 0; x < K / 4; x += 4)
-                        *reinterpret_cast<uint4 *>(sm.S + op_off(r, x0 + 2 * x, V)) = make_uint4(hi[x], hi[x + 1], hi[x + 2], hi[x + 3]);
+                    for (int t = 0; t < 16; ++t)
+                        sm.o[(c16 + t) * V + r] = __float2bfloat16_rn(fmaf(eG[t], __uint_as_float(x[t]), __uint_as_float(z[t])));
                 fence_proxy_async_smem();
-                mbar_arrive(&sm.Sout);
+                mbar_arrive_warp(&sm.oout);
             }
-        };
-        if (chunks > 0) put_state(0);
-        for (int c = 0; c < chunks && ok; ++c) {
-            const GdrPrep &p = sm.p[c & 1];
+            if (c == chunks) break;
             const int m = min(kC, len - c * kC);
-            uint32_t x[32], y[16], z[16];
+            float y[16];
+            if (quarter == 0 && lane < 16) sm.eG[c & 1][c16 + lane] = p.eG[c16 + lane];
             // R = w (v - e^G G)
+            const __nv_bfloat16 *v = sm.v[c & 1] + c16 * V + (live ? r : 0);
+#pragma unroll
+            for (int t = 0; t < 16; ++t) y[t] = __bfloat162float(v[t * V]);
             if (!(ok = wait(sm.gfull, c))) break;
             tc_fence_after_sync();
-            tmem_ld32(tl + cG + c32, x);
+            tmem_ld16(tl + cG + c16, x);
             tmem_wait_ld();
-            tmem_tie(x);
-            const __nv_bfloat16 *v = sm.v[c & 1] + c32 * V + (live ? r : 0);
+            tmem_tie16(x);
 #pragma unroll
-            for (int t = 0; t < 32; t += 2) {
-                float R[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    R[e] = c32 + t + e < m && live
-                               ? p.w[c32 + t + e] * (__bfloat162float(v[(t + e) * V]) - p.eG[c32 + t + e] * __uint_as_float(x[t + e]))
-                               : 0.f;
-                split_pair(R[0], R[1], y[t / 2], z[t / 2]);
-            }
-            tmem_st16(tl + cG + c32, y);   // over the columns of G that this thread has read
-            tmem_st16(tl + cG + c32 + 16, z);
+            for (int t = 0; t < 16; ++t)
+                y[t] = c16 + t < m && live ? p.w[c16 + t] * (y[t] - p.eG[c16 + t] * __uint_as_float(x[t])) : 0.f;
+            put_split16(tl + cG + c16, y);
             tmem_wait_st();
             tc_fence_before_sync();
-            mbar_arrive(&sm.rready);
-            // e^G Q S^T
-            if (!(ok = wait(sm.qfull, c))) break;
-            tc_fence_after_sync();
-            tmem_ld32(tl + cO + c32, x);
-            tmem_wait_ld();
-            tmem_tie(x);
+            mbar_arrive_warp(&sm.rready);
+            if (SAVE) {
+                if (c > 0 && !(ok = wait(sm.Sfree, c - 1))) break;
+                if (live)
 #pragma unroll
-            for (int t = 0; t < 32; ++t) x[t] = __float_as_uint(__uint_as_float(x[t]) * p.eG[c32 + t]);
-            tmem_st32(tl + cO + c32, x);
+                    for (int i = 0; i < KQ / 2; i += 4)
+                        *reinterpret_cast<uint4 *>(sm.S + op_off(r, x0 + 2 * i, V)) = make_uint4(hi[i], hi[i + 1], hi[i + 2], hi[i + 3]);
+                fence_proxy_async_smem();
+                mbar_arrive_warp(&sm.Sout);
+            }
             // U
             if (!(ok = wait(sm.ufull, c))) break;
             tc_fence_after_sync();
-            tmem_ld32(tl + cU + c32, x);
+            tmem_ld16(tl + cU + c16, x);
             tmem_wait_ld();
-            tmem_tie(x);
-            uint32_t ub[16];
+            tmem_tie16(x);
 #pragma unroll
-            for (int t = 0; t < 32; t += 2) {
-                const float u0 = __uint_as_float(x[t]), u1 = __uint_as_float(x[t + 1]);
-                ub[t / 2] = pack_bf16(u0, u1);
-                split_pair(u0 * p.eK[c32 + t], u1 * p.eK[c32 + t + 1], y[t / 2], z[t / 2]);
-            }
-            tmem_st16(tl + cU + c32, y);
-            tmem_st16(tl + cU + c32 + 16, z);
-            tmem_st16(tl + cUb + 16 * half, ub);
+            for (int t = 0; t < 16; ++t) y[t] = __uint_as_float(x[t]) * p.eK[c16 + t];
+            put_split16(tl + cU + c16, y);
+            put_split16(tl + cG + c16, reinterpret_cast<const float *>(x));
             tmem_wait_st();
             tc_fence_before_sync();
-            mbar_arrive(&sm.uready);
+            mbar_arrive_warp(&sm.uready);
             if (SAVE) {
                 if (c > 0 && !(ok = wait(sm.ufree, c - 1))) break;
                 if (live)
 #pragma unroll
-                    for (int t = 0; t < 32; ++t)
-                        reinterpret_cast<uint16_t *>(sm.u)[op_off(c32 + t, r, kC)] = (uint16_t)(ub[t / 2] >> (16 * (t & 1)));
+                    for (int t = 0; t < 16; ++t) sm.u[op_off(c16 + t, r, kC)] = __float2bfloat16_rn(__uint_as_float(x[t]));
                 fence_proxy_async_smem();
-                mbar_arrive(&sm.uout);
+                mbar_arrive_warp(&sm.uout);
             }
             // the state after the chunk
             if (!(ok = wait(sm.sfull, c))) break;
             tc_fence_after_sync();
-#pragma unroll
-            for (int i = 0; i < K / 2; i += 32) tmem_ld32(tl + x0 + i, reinterpret_cast<uint32_t *>(S) + i);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < K / 2; i += 32) tmem_tie(reinterpret_cast<uint32_t *>(S) + i);
-            if (c + 1 < chunks) put_state(c + 1);
-            if (!ok) break;
-            // outputs
-            if (!(ok = wait(sm.ofull, c))) break;
-            tc_fence_after_sync();
-            tmem_ld32(tl + cO + c32, x);
-            tmem_wait_ld();
-            tmem_tie(x);
-            tc_fence_before_sync();
-            if (c > 0 && !(ok = wait(sm.ofree, c - 1))) break;
-            if (live)
-#pragma unroll
-                for (int t = 0; t < 32; ++t) sm.o[(c32 + t) * V + r] = __float2bfloat16_rn(__uint_as_float(x[t]));
-            fence_proxy_async_smem();
-            mbar_arrive(&sm.oout);
+            get_state<KQ>(tl + x0, S);
         }
-        if (ok && a.S_final && live)
-#pragma unroll
-            for (int x = 0; x < K / 2; x += 4)
-                *reinterpret_cast<float4 *>(a.S_final + st + x) = make_float4(S[x], S[x + 1], S[x + 2], S[x + 3]);
+        if (ok && a.S_final && live) store_row<KQ>(a.S_final + st, S);
     }
     if (!ok && lane == 0) atomicOr(&g_gdr_timeout, 1);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    if (warp == 9) tmem_dealloc(tm, 512);
+    if (warp == kRegWarps + 1) tmem_dealloc(tm, 512);
 }
 
 template <int K, int V, bool SAVE>
@@ -584,7 +550,7 @@ cudaError_t sweep_t(const GdrArgs &a, const CUtensorMap &mq, const CUtensorMap &
     const int bytes = (int)sizeof(SweepSmem<K, V, SAVE>) + 1024;
     const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), bytes);
     if (e != cudaSuccess) return e;
-    kern<<<a.seq.N * a.Hv, 352, bytes, st>>>(a, mq, mk, mv);
+    kern<<<a.seq.N * a.Hv, kSweepThreads, bytes, st>>>(a, mq, mk, mv);
     return cudaGetLastError();
 }
 
