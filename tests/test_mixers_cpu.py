@@ -184,3 +184,12 @@ def test_window_reference_against_differences():
     f = lambda q, k, v: R.window(q, k, v, 3, 2)[:1]  # noqa: E731
     cot = (r(12, 2, 4),)
     _difference(f, x, cot, R.grads(f, x, cot), 6)
+
+
+def test_declared_arguments_match_the_header(lib):
+    """As many argument types as the C prototype has parameters: one too few would pass half a pointer."""
+    src = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "carve_mixers.h")).read(), flags=re.S)
+    protos = dict(re.findall(r"\b(carve_[a-z_]+)\s*\(([^)]*)\)\s*;", src))
+    assert len(protos) == 11
+    for name, params in protos.items():
+        assert len(getattr(lib, name).argtypes) == len(params.split(",")), name
