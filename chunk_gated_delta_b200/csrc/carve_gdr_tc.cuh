@@ -24,7 +24,7 @@ constexpr uint32_t kTile64 = kC * 128;   // bytes of a 64-row block
 // Per (tile, value head), written by the preparation: Tm hi, Tm lo, A (each [64][64]), then vectors.
 struct GdrPrep {
     __nv_bfloat16 t_hi[kC * 64], t_lo[kC * 64], A[kC * 64];
-    float eG[kC], eK[kC], w[kC], G[kC];   // e^{G_t}, e^{G_C - G_t}, w_t, G_t
+    float eG[kC], eK[kC], w[kC], G[kC];   // e^{G_t}, e^{G_C - G_t}, w_t, G_t log2 e
 };
 static_assert(sizeof(GdrPrep) == 25600, "slots are copied in bulk");
 

@@ -296,14 +296,14 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
 
 template <int K, int V>
 struct GradSmem {
-    __nv_bfloat16 d[2][V / 64][192 * 64];   // [stage]: dO, dY, U
-    __nv_bfloat16 S0[V * K], S1[V * K];     // S0, dS1
-    __nv_bfloat16 qk[K / 64][128 * 64];     // Q, K
-    __nv_bfloat16 P[192 * 64];              // zeros, P1, P2
-    float vec[2][4][kC];                    // [stage]: e^G, e^{G_C - G}, w, G
-    float dg[4][128], dw[4][kC], kb[4][kC], tot[3][128], col[4][kC], last[8];   // partial sums of a head
-    uint64_t qkfull, qkfree, dfull[2], dfree[2], s0full, s0free, s1full, s1free, Dfull, Dfree, xfull, xfree, yfull, yfree,
-        pready, pfull, afree, gready, gfree, drain;
+    __nv_bfloat16 d[V / 64][192 * 64];         // dO, dY, U
+    __nv_bfloat16 S0[V * K], S1[V * K];        // S0, dS1
+    __nv_bfloat16 qk[2][K / 64][128 * 64];     // [stage]: Q, K, then dq, dk on their way out
+    __nv_bfloat16 P[192 * 64];                 // zeros, P1, P2
+    float vec[2][4][kC];                       // [stage]: e^G, e^{G_C - G}, w, G
+    float dg[4][128], dw[kC], kb[4][kC], tot[3][128], col[4][kC], last[8];   // partial sums of a head
+    uint64_t vfull[2], vfree[2], qkfull[2], qkfree[2], dfull, dfree, s0full, s0free, s1full, s1free, Dfull, Dfree, xfull,
+        xfree, yfull, yfree, pready, pfull, afree, gready, gfree, oready, drain;
     uint32_t tmem;
 };
 
@@ -334,11 +334,9 @@ __device__ __forceinline__ float column_sum(float (&x)[16], int lane) {
     return x[0];
 }
 
-// z = f times COLS columns of an accumulator (zero where f is not `here`'s): acc += f2 z, returns <z, row r of
-// [Q; K]>; `read` follows the last load
+// acc += f times COLS columns x of an accumulator; returns <x, row r of [Q; K]>; `read` follows the last load
 template <int COLS, class F>
-__device__ __forceinline__ float product_row(uint32_t taddr, float f, float f2, bool here, const __nv_bfloat16 *qk, int r, int x0,
-                                             float *acc, F read) {
+__device__ __forceinline__ float product_row(uint32_t taddr, float f, const __nv_bfloat16 *qk, int r, int x0, float *acc, F read) {
     float d = 0.f;
 #pragma unroll
     for (int b = 0; b < COLS; b += 16) {
@@ -349,14 +347,13 @@ __device__ __forceinline__ float product_row(uint32_t taddr, float f, float f2, 
         if (b + 16 == COLS) read();
 #pragma unroll
         for (int i = 0; i < 16; i += 8) {
-            uint4 y = *reinterpret_cast<const uint4 *>(qk + op_off(r, x0 + b + i, 128));
-            if (!here) y = make_uint4(0u, 0u, 0u, 0u);
+            const uint4 y = *reinterpret_cast<const uint4 *>(qk + op_off(r, x0 + b + i, 128));
             const uint32_t yy[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float z = here ? f * __uint_as_float(x[i + e]) : 0.f;
+                const float z = __uint_as_float(x[i + e]);
                 d = fmaf(z, __uint_as_float(e % 2 ? yy[e / 2] & 0xffff0000u : yy[e / 2] << 16), d);
-                acc[b + i + e] = fmaf(f2, z, acc[b + i + e]);
+                acc[b + i + e] = fmaf(f, z, acc[b + i + e]);
             }
         }
     }
@@ -366,7 +363,8 @@ __device__ __forceinline__ float product_row(uint32_t taddr, float f, float f2, 
 template <int K, int V>
 __global__ void __launch_bounds__(kSweepThreads, 1)
     gdr_tc_grad(GdrArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                const __grid_constant__ CUtensorMap md) {
+                const __grid_constant__ CUtensorMap md, const __grid_constant__ CUtensorMap mdq,
+                const __grid_constant__ CUtensorMap mdk) {
     extern __shared__ __align__(16) unsigned char raw[];
     typedef GradSmem<K, V> Smem;
     typedef GdrKeep<K, V> Keep;
@@ -374,12 +372,12 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
     constexpr int KH = K / 64, VH = V / 64, KQ = K / 4;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, share = a.Hv / a.Hk;
     if (threadIdx.x == 0) {
-        for (uint64_t *b : {&sm.qkfull, &sm.dfull[0], &sm.dfull[1], &sm.s0full, &sm.s1full, &sm.Dfull, &sm.xfull, &sm.yfull,
-                            &sm.pfull, &sm.gfree, &sm.drain})
+        for (uint64_t *b : {&sm.vfull[0], &sm.vfull[1], &sm.qkfull[0], &sm.qkfull[1], &sm.qkfree[0], &sm.qkfree[1], &sm.dfull,
+                            &sm.dfree, &sm.s0full, &sm.s1full, &sm.Dfull, &sm.xfull, &sm.yfull, &sm.pfull, &sm.gfree, &sm.drain})
             mbar_init(b, 1);
-        for (uint64_t *b : {&sm.Dfree, &sm.xfree, &sm.pready, &sm.afree, &sm.gready}) mbar_init(b, kRegWarps);
-        for (uint64_t *b : {&sm.qkfree, &sm.dfree[0], &sm.dfree[1]}) mbar_init(b, kRegWarps + 1);   // readers and the products
-        for (uint64_t *b : {&sm.s0free, &sm.s1free}) mbar_init(b, kRegWarps / 2 + 1);
+        for (uint64_t *b : {&sm.vfree[0], &sm.vfree[1], &sm.Dfree, &sm.xfree, &sm.pready, &sm.afree, &sm.gready, &sm.oready})
+            mbar_init(b, kRegWarps);
+        for (uint64_t *b : {&sm.s0free, &sm.s1free}) mbar_init(b, kRegWarps / 2 + 1);   // readers and the products
         mbar_init(&sm.yfree, kRegWarps / 2);
         fence_mbar_init();
     }
@@ -395,13 +393,13 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
     auto wait = [&](uint64_t &bar, int phase) {   // by a whole warp
         return (bool)__all_sync(0xffffffffu, mbar_wait(&bar, phase & 1, kSwaWait));
     };
-    const long long items = a.seq.n_tiles(kC) * a.Hk;
+    const int items = (int)a.seq.n_tiles(kC) * a.Hk;   // below 2^28
     int it = 0, j = 0;   // items and heads so far (those of used tiles)
 
     if (warp >= kRegWarps) regs_down<64>();
     if (warp == kRegWarps) {
-        for (long long w = blockIdx.x; w < items && ok; w += gridDim.x) {
-            const int tile = (int)(w / a.Hk), hk = (int)(w % a.Hk);
+        for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
+            const int tile = w / a.Hk, hk = w - tile * a.Hk;
             int n, c, len;
             long long row;
             if (!a.seq.find(tile, kC, n, c, row, len)) continue;
@@ -410,28 +408,34 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                 const int s = j & 1, h = hk * share + g;
                 const size_t slot = (size_t)tile * a.Hv + h;
                 const Keep *fwd = reinterpret_cast<const Keep *>(a.saved) + slot, *bwd = reinterpret_cast<const Keep *>(a.ws) + slot;
-                if (j >= 2 && !(ok = wait(sm.dfree[s], j / 2 - 1))) break;
+                if (j >= 2 && !(ok = wait(sm.vfree[s], j / 2 - 1))) break;
                 if (lane == 0) {
-                    mbar_expect_tx(&sm.dfull[s], 3 * kC * V * 2 + sizeof(sm.vec[0]));
-                    bulk_g2s(sm.vec[s], reinterpret_cast<const GdrPrep *>(a.prep)[slot].eG, sizeof(sm.vec[0]), &sm.dfull[s]);
-                    for (int x = 0; x < VH; ++x) {
-                        tma_load_3d(sm.d[s][x], &md, 64 * x, h, (int)row, &sm.dfull[s]);
-                        bulk_g2s(sm.d[s][x] + kC * 64, bwd->x + x * kC * 64, kTile64, &sm.dfull[s]);
-                        bulk_g2s(sm.d[s][x] + 2 * kC * 64, fwd->x + x * kC * 64, kTile64, &sm.dfull[s]);
-                    }
+                    mbar_expect_tx(&sm.vfull[s], sizeof(sm.vec[0]));
+                    bulk_g2s(sm.vec[s], reinterpret_cast<const GdrPrep *>(a.prep)[slot].eG, sizeof(sm.vec[0]), &sm.vfull[s]);
                 }
                 __syncwarp();
                 if (g == 0) {
-                    if (it > 0 && !(ok = wait(sm.qkfree, it - 1))) break;
+                    const int b = it & 1;
+                    if (it >= 2 && !(ok = wait(sm.qkfree[b], it / 2 - 1))) break;
                     if (lane == 0) {
-                        mbar_expect_tx(&sm.qkfull, 2 * kC * K * 2);
+                        mbar_expect_tx(&sm.qkfull[b], 2 * kC * K * 2);
                         for (int x = 0; x < KH; ++x) {
-                            tma_load_3d(sm.qk[x], &mq, 64 * x, hk, (int)row, &sm.qkfull);
-                            tma_load_3d(sm.qk[x] + kC * 64, &mk, 64 * x, hk, (int)row, &sm.qkfull);
+                            tma_load_3d(sm.qk[b][x], &mq, 64 * x, hk, (int)row, &sm.qkfull[b]);
+                            tma_load_3d(sm.qk[b][x] + kC * 64, &mk, 64 * x, hk, (int)row, &sm.qkfull[b]);
                         }
                     }
                     __syncwarp();
                 }
+                if (j > 0 && !(ok = wait(sm.dfree, j - 1))) break;
+                if (lane == 0) {
+                    mbar_expect_tx(&sm.dfull, 3 * kC * V * 2);
+                    for (int x = 0; x < VH; ++x) {
+                        tma_load_3d(sm.d[x], &md, 64 * x, h, (int)row, &sm.dfull);
+                        bulk_g2s(sm.d[x] + kC * 64, bwd->x + x * kC * 64, kTile64, &sm.dfull);
+                        bulk_g2s(sm.d[x] + 2 * kC * 64, fwd->x + x * kC * 64, kTile64, &sm.dfull);
+                    }
+                }
+                __syncwarp();
                 if (j > 0 && !(ok = wait(sm.s0free, j - 1))) break;
                 if (lane == 0) {
                     mbar_expect_tx(&sm.s0full, sizeof(sm.S0));
@@ -449,26 +453,27 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
         }
         // every copy has landed before the memory is given back (those not issued wait in vain, with a limit)
         if (!ok) {
-            for (int i = max(0, j - 1); i <= j; ++i) wait(sm.dfull[i & 1], i / 2);
-            wait(sm.qkfull, it);
+            for (int i = max(0, j - 1); i <= j; ++i) wait(sm.vfull[i & 1], i / 2);
+            for (int i = max(0, it - 1); i <= it; ++i) wait(sm.qkfull[i & 1], i / 2);
+            wait(sm.dfull, j);
             wait(sm.s0full, j);
             wait(sm.s1full, j);
         }
     } else if (warp == kRegWarps + 1) {
         constexpr uint32_t iN64 = umma_idesc_bf16(128, 64), iK = umma_idesc_bf16(128, K) | kUmmaBmn;
-        const uint32_t P = smem_u32(sm.P), qk = smem_u32(sm.qk[0]);
-        for (long long w = blockIdx.x; w < items && ok; w += gridDim.x) {
-            const int tile = (int)(w / a.Hk);
+        const uint32_t P = smem_u32(sm.P), d = smem_u32(sm.d[0]);
+        for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
+            const int tile = w / a.Hk;
             int n, c, len;
             long long row;
             if (!a.seq.find(tile, kC, n, c, row, len)) continue;
+            const uint32_t qk = smem_u32(sm.qk[it & 1][0]);
             for (int g = 0; g < share && ok; ++g, ++j) {
-                const int s = j & 1;
                 if (g == 0) {
-                    if (!(ok = wait(sm.qkfull, it))) break;
+                    if (!(ok = wait(sm.qkfull[it & 1], it / 2))) break;
                     if (len - c * kC < kC) {   // rows behind the end meet zero factors, so they have to be finite
-                        zero_rows(sm.qk[0], len - c * kC, KH, 2 * kTile64, lane);
-                        zero_rows(sm.qk[0] + kC * 64, len - c * kC, KH, 2 * kTile64, lane);
+                        zero_rows(sm.qk[it & 1][0], len - c * kC, KH, 2 * kTile64, lane);
+                        zero_rows(sm.qk[it & 1][0] + kC * 64, len - c * kC, KH, 2 * kTile64, lane);
                         fence_proxy_async_smem();
                         __syncwarp();
                     }
@@ -483,8 +488,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                     }
                 }
                 __syncwarp();
-                if (!(ok = wait(sm.dfull[s], j / 2))) break;
-                const uint32_t d = smem_u32(sm.d[s][0]);
+                if (!(ok = wait(sm.dfull, j))) break;
                 if (lane == 0) {
 #pragma unroll
                     for (int kk = 0; kk < V / 16; ++kk) {
@@ -516,7 +520,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                                   umma_desc_mn(smem_u32(sm.S1) + 2048 * kk, V * 128), iK, kk > 0);
                     umma_commit(&sm.yfull);
                 umma_commit(&sm.s1free);
-                    umma_commit(&sm.dfree[s]);
+                    umma_commit(&sm.dfree);
                 }
                 __syncwarp();
                 if (!(ok = wait(sm.pready, j))) break;
@@ -536,7 +540,6 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                         umma_bf16(tm + cA, umma_desc_mn(P + 2048 * kk, 2 * kTile64),
                                   umma_desc_mn(qk + kTile64 + 2048 * kk, 2 * kTile64), iK | kUmmaAmn, 1);
                     umma_commit(&sm.pfull);
-                    if (g == share - 1) umma_commit(&sm.qkfree);
                 }
                 __syncwarp();
             }
@@ -551,8 +554,8 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
         // columns of a cumulative sum would cancel): queries and keys r >= t that read the start state,
         // keys s < t that reach the end, S0 itself, and pairs r >= t > s.
         float *part = a.dA_dec || a.dtau ? reinterpret_cast<float *>(a.ws + (size_t)a.seq.n_tiles(kC) * a.Hv * sizeof(Keep)) : nullptr;
-        for (long long wk = blockIdx.x; wk < items && ok; wk += gridDim.x) {
-            const int tile = (int)(wk / a.Hk), hk = (int)(wk % a.Hk);
+        for (int wk = blockIdx.x; wk < items && ok; wk += gridDim.x) {
+            const int tile = wk / a.Hk, hk = wk - tile * a.Hk;
             int n, c, len;
             long long row;
             if (!a.seq.find(tile, kC, n, c, row, len)) {
@@ -574,17 +577,18 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                     w[e] = sigmoid_f(ld_io(static_cast<const __nv_bfloat16 *>(a.w_logit) + at));
                 }
                 if (!(ok = wait(sm.gready, j))) break;
-                // row sums; sums of key rows; write gate; columns of the pairs; row totals of the first 16, 32, 48 pairs
+                // row sums; sums of key rows; dY.U = w dL/dw (from (I + M) U = w R: dL/dw = dY.(R - M U / w) = dY.U / w);
+                // columns of the pairs; row totals of the pairs of tokens 0-15, 16-31, 32-47
                 float G[2], B[2], dw[2], C[2], T[3][2], last = 0.f;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int t = lane + 32 * e;
-                    G[e] = B[e] = dw[e] = C[e] = 0.f;
+                    G[e] = B[e] = C[e] = 0.f;
+                    dw[e] = sm.dw[t];
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {
                         G[e] += sm.dg[p][t] + sm.dg[p][t + 64];
                         B[e] += sm.kb[p][t];
-                        dw[e] += sm.dw[p][t];
                         C[e] += sm.col[p][t];
                     }
 #pragma unroll
@@ -627,7 +631,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                         dlog += dl;
                         damp += -amp * softplus_f(x[e]) * gr[e];
                         st_io(static_cast<__nv_bfloat16 *>(a.dg_logit) + at, dl);
-                        st_io(static_cast<__nv_bfloat16 *>(a.dw_logit) + at, dw[e] * w[e] * (1.f - w[e]));
+                        st_io(static_cast<__nv_bfloat16 *>(a.dw_logit) + at, dw[e] * (1.f - w[e]));
                     }
                 }
                 if (part) {
@@ -643,29 +647,53 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                 }
             }
         }
+    } else if (warp == kRegWarps + 3) {
+        for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
+            const int tile = w / a.Hk, hk = w - tile * a.Hk;
+            int n, c, len;
+            long long row;
+            if (!a.seq.find(tile, kC, n, c, row, len)) continue;
+            row += (long long)c * kC;
+            if (!(ok = wait(sm.oready, it))) break;
+            if (lane == 0) {
+                if (len - c * kC >= kC)
+                    for (int x = 0; x < KH; ++x) {
+                        tma_store_3d(&mdq, sm.qk[it & 1][x], 64 * x, hk, (int)row);
+                        tma_store_3d(&mdk, sm.qk[it & 1][x] + kC * 64, 64 * x, hk, (int)row);
+                    }
+                bulk_commit();
+                bulk_wait_read<0>();
+                mbar_arrive(&sm.qkfree[it & 1]);
+            }
+            __syncwarp();
+            ++it;
+        }
+        bulk_wait<0>();
     } else if (warp < kRegWarps) {
         regs_up<104>();
         const int part = warp / 4, quarter = warp % 4, r = quarter * 32 + lane, t = r % kC;
         const bool key = r >= kC;   // lane of a key (the same for a whole warp)
         const uint32_t tl = tm + ((uint32_t)quarter << 21);
-        const int x0 = part * KQ, s0 = part * 16, v0 = part * (V / 4);
+        const int x0 = part * KQ, s0 = part * 16;
         float acc[KQ];
-        for (long long wk = blockIdx.x; wk < items && ok; wk += gridDim.x) {
-            const int tile = (int)(wk / a.Hk), hk = (int)(wk % a.Hk);
+        for (int wk = blockIdx.x; wk < items && ok; wk += gridDim.x) {
+            const int tile = wk / a.Hk, hk = wk - tile * a.Hk;
             int n, c, len;
             long long row;
             if (!a.seq.find(tile, kC, n, c, row, len)) continue;
             row += (long long)c * kC;
-            const bool here = t < len - c * kC;
+            const int m = min(kC, len - c * kC);
+            const bool here = t < m;
+            const int lim = here ? t + !key - s0 : 0;   // pairs of this token among its 16: s < t, and s = t for queries
+            __nv_bfloat16 *qk = sm.qk[it & 1][0];
 #pragma unroll
             for (int x = 0; x < KQ; ++x) acc[x] = 0.f;
             for (int g = 0; g < share && ok; ++g, ++j) {
-                const int s = j & 1, h = hk * share + g;
-                if (!(ok = wait(sm.dfull[s], j / 2))) break;
-                const float *eG = sm.vec[s][0], *eK = sm.vec[s][1], *G = sm.vec[s][3];
-                const float wt = sm.vec[s][2][t];
-                float dw = 0.f, dg, kb = 0.f, run = 0.f;
-                // pairs of the chunk
+                const int s = j & 1;
+                if (!(ok = wait(sm.vfull[s], j / 2))) break;
+                const float *eG = sm.vec[s][0], *eK = sm.vec[s][1], *G = sm.vec[s][3] + s0;
+                const float Gt = sm.vec[s][3][t], sign = key ? -sm.vec[s][2][t] : 1.f;
+                // pairs of the chunk: y = D (dO U^T) or -w D (dY U^T), times k.k or q.k
                 if (!(ok = wait(sm.Dfull, j))) break;
                 tc_fence_after_sync();
                 {
@@ -677,20 +705,13 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                     tmem_tie16(kk);
                     tc_fence_before_sync();
                     mbar_arrive_warp(&sm.Dfree);
-                    const float Gt = G[t];
-                    float pr[16];
+                    float pr[16], own = 0.f;
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const int u = s0 + e;
-                        const bool below = here && u < t;
-                        float y = below || (here && !key && u == t) ? __expf(Gt - G[u]) * __uint_as_float(D[e]) : 0.f;
-                        const float b = below ? __uint_as_float(kk[e]) : 0.f;
-                        if (key) {
-                            y = -y;
-                            dw = fmaf(y, b, dw);
-                            y *= wt;
-                        }
-                        pr[e] = y * b;
+                        const float x = __uint_as_float(D[e]);
+                        own = t - s0 == e ? x : own;
+                        const float y = e < lim ? sign * ex2(Gt - G[e]) * x : 0.f;
+                        pr[e] = y * __uint_as_float(kk[e]);
                         D[e] = __float_as_uint(y);
                     }
 #pragma unroll
@@ -701,7 +722,8 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                         *reinterpret_cast<uint4 *>(sm.P + kC * 64 + op_off(r, s0 + 2 * e, 128)) = make_uint4(p[e], p[e + 1], p[e + 2], p[e + 3]);
                     fence_proxy_async_smem();
                     mbar_arrive_warp(&sm.pready);
-                    // sums over s before u, for u up to t; then over the warp's tokens
+                    // sums over s before u, for u up to t (what a query's own pair adds is behind its last u)
+                    float run = 0.f;
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const float y = pr[e];
@@ -712,59 +734,48 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                     if (j > 0 && !(ok = wait(sm.gfree, j - 1))) break;
                     if (lane < 16) sm.col[quarter][s0 + lane] = cs;
                     if (part < 3) sm.tot[part][r] = run;
+                    if (key && t / 16 == part) sm.dw[t] = own;
                 }
-                uint4 v[V / 32];   // this key's values, a quarter of the channels
-#pragma unroll
-                for (int i = 0; i < V / 32; ++i)
-                    v[i] = key && here ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.v) +
-                                                                              ((size_t)(row + t) * a.Hv + h) * V + v0) + i)
-                                       : make_uint4(0u, 0u, 0u, 0u);
-                // start state
-                if (!(ok = wait(sm.xfull, j))) break;
-                tc_fence_after_sync();
-                {
-                    const float f = here ? eG[t] : 0.f, f2 = key ? -wt : 1.f;
-                    const float d = product_row<KQ>(tl + cX + x0, f, f2, here, sm.qk[0], r, x0, acc, [&] {
-                        tc_fence_before_sync();
-                        mbar_arrive_warp(&sm.xfree);
-                    });
-                    dg = f2 * d;
-                    dw -= d;
-                }
-                if (key) {   // end state; the values
+                if (key) {   // end state
                     if (!(ok = wait(sm.yfull, j))) break;
                     tc_fence_after_sync();
-                    kb = product_row<KQ>(tl + cY + x0, here ? eK[t] : 0.f, 1.f, here, sm.qk[0], r, x0, acc, [&] {
+                    const float f = eK[t];
+                    const float d = product_row<KQ>(tl + cY + x0, f, qk, r, x0, acc, [&] {
                         tc_fence_before_sync();
                         mbar_arrive_warp(&sm.yfree);
                     });
-#pragma unroll
-                    for (int i = 0; i < V / 32; ++i)
-                        dw = dot8(*reinterpret_cast<const uint4 *>(sm.d[s][0] + op_off(r, v0 + 8 * i, 192)), v[i], dw);
-                    sm.dw[part][t] = dw;
-                    sm.kb[part][t] = kb;
+                    sm.kb[part][t] = here ? f * d : 0.f;
                 } else {   // <S0, dS1>: both are laid out alike
                     if (!(ok = wait(sm.s0full, j))) break;
                     if (!(ok = wait(sm.s1full, j))) break;
-                    const int at = part * 64 + quarter * 32 + lane;
                     float y = 0.f;
-#pragma unroll 4
-                    for (int i = at; i < V * K / 8; i += 256)
-                        y = dot8(reinterpret_cast<const uint4 *>(sm.S0)[i], reinterpret_cast<const uint4 *>(sm.S1)[i], y);
+#pragma unroll
+                    for (int i = 0; i < V * K / 8; i += 256)
+                        y = dot8(reinterpret_cast<const uint4 *>(sm.S0)[i + part * 64 + quarter * 32 + lane],
+                                 reinterpret_cast<const uint4 *>(sm.S1)[i + part * 64 + quarter * 32 + lane], y);
                     mbar_arrive_warp(&sm.s0free);
                     mbar_arrive_warp(&sm.s1free);
 #pragma unroll
                     for (int off = 16; off >= 1; off >>= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
                     if (lane == 0) sm.last[part * 2 + quarter] = y * eG[kC - 1];
                 }
-                sm.dg[part][r] = dg;
+                // start state
+                if (!(ok = wait(sm.xfull, j))) break;
+                tc_fence_after_sync();
+                const float f = sign * eG[t];
+                const float d = product_row<KQ>(tl + cX + x0, f, qk, r, x0, acc, [&] {
+                    tc_fence_before_sync();
+                    mbar_arrive_warp(&sm.xfree);
+                });
+                sm.dg[part][r] = here ? f * d : 0.f;
                 mbar_arrive_warp(&sm.gready);
-                mbar_arrive_warp(&sm.dfree[s]);
-                if (g == share - 1) mbar_arrive_warp(&sm.qkfree);
+                mbar_arrive_warp(&sm.vfree[s]);
             }
             if (!ok) break;
             if (!(ok = wait(sm.pfull, j - 1))) break;
             tc_fence_after_sync();
+            // dq, dk in the place of this thread's part of q, k (rows of a last tile straight to memory: those
+            // behind the end are others')
             uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(key ? a.dk : a.dq) +
                                                    ((size_t)(row + t) * a.Hk + hk) * K + x0);
 #pragma unroll
@@ -780,11 +791,17 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 16; e += 2)
                     o[e / 2] = pack_bf16(acc[b + e] + __uint_as_float(x[e]), acc[b + e + 1] + __uint_as_float(x[e + 1]));
-                if (here) {
-                    out[b / 8] = make_uint4(o[0], o[1], o[2], o[3]);
-                    out[b / 8 + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+#pragma unroll
+                for (int e = 0; e < 8; e += 4) {
+                    const uint4 y = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    if (m == kC)
+                        *reinterpret_cast<uint4 *>(qk + op_off(r, x0 + b + 2 * e, 128)) = y;
+                    else if (here)
+                        out[(b + 2 * e) / 8] = y;
                 }
             }
+            fence_proxy_async_smem();
+            mbar_arrive_warp(&sm.oready);
             ++it;
         }
     }
@@ -798,7 +815,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
 template <int K, int V>
 cudaError_t bwd_t(const GdrArgs &a, cudaStream_t st) {
     const long long rows = a.seq.cu ? a.seq.total : (long long)a.seq.N * a.seq.T;
-    CUtensorMap mq{}, mk{}, md{};
+    CUtensorMap mq{}, mk{}, md{}, mdq{}, mdk{};
     auto sweep = gdr_tc_bsweep<K, V>;
     auto grad = gdr_tc_grad<K, V>;
     const int sb = (int)sizeof(BsweepSmem<K, V>) + 1024, gb = (int)sizeof(GradSmem<K, V>) + 1024;
@@ -808,11 +825,13 @@ cudaError_t bwd_t(const GdrArgs &a, cudaStream_t st) {
         if (e == cudaSuccess) e = make_operand_tile_map(&mq, a.q, K, a.Hk, rows, kC);
         if (e == cudaSuccess) e = make_operand_tile_map(&mk, a.k, K, a.Hk, rows, kC);
         if (e == cudaSuccess) e = make_operand_tile_map(&md, a.dO, V, a.Hv, rows, kC);
+        if (e == cudaSuccess) e = make_operand_tile_map(&mdq, a.dq, K, a.Hk, rows, kC);
+        if (e == cudaSuccess) e = make_operand_tile_map(&mdk, a.dk, K, a.Hk, rows, kC);
     }
     if (e != cudaSuccess) return e;
     sweep<<<a.seq.N * a.Hv, kSweepThreads, sb, st>>>(a, mq, mk, md);
     const long long tiles = a.seq.n_tiles(kC), items = tiles * a.Hk;
-    if (items) grad<<<(unsigned)(items < sm_count() ? items : sm_count()), kSweepThreads, gb, st>>>(a, mq, mk, md);
+    if (items) grad<<<(unsigned)(items < sm_count() ? items : sm_count()), kSweepThreads, gb, st>>>(a, mq, mk, md, mdq, mdk);
     if (a.dA_dec || a.dtau)
         launch_gdr_reduce_decay(reinterpret_cast<const float *>(a.ws + (size_t)tiles * a.Hv * sizeof(GdrKeep<K, V>)), tiles, a.Hv,
                                 a.dA_dec, a.dtau, st);

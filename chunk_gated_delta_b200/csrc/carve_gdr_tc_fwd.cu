@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(128) gdr_tc_prep(GdrArgs a, const __grid_const
             if (tid < m) {
                 const size_t at = (size_t)(row + tid) * a.Hv + h;
                 const float x = ld_io(static_cast<const __nv_bfloat16 *>(a.g_logit) + at) + (a.tau ? a.tau[h] : 0.f);
-                la = -decay_amp(a.A_dec, h) * softplus_f(x);
+                la = -1.4426950408889634f * decay_amp(a.A_dec, h) * softplus_f(x);
                 w = sigmoid_f(ld_io(static_cast<const __nv_bfloat16 *>(a.w_logit) + at));
             }
 #pragma unroll
@@ -216,8 +216,8 @@ __global__ void __launch_bounds__(128) gdr_tc_prep(GdrArgs a, const __grid_const
         if (tid >= 32 && tid < kC) sm.G[tid] += sm.G[31];
         __syncthreads();
         if (tid < kC) {
-            sm.eG[tid] = expf(sm.G[tid]);
-            sm.eK[tid] = expf(sm.G[kC - 1] - sm.G[tid]);
+            sm.eG[tid] = exp2f(sm.G[tid]);
+            sm.eK[tid] = exp2f(sm.G[kC - 1] - sm.G[tid]);
         }
         const float Gt = sm.G[t], wt = sm.w[t];
         if (tid < kC) {
@@ -226,8 +226,8 @@ __global__ void __launch_bounds__(128) gdr_tc_prep(GdrArgs a, const __grid_const
                 uint32_t p[4];
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
-                    const float x0 = s + e <= t && t < m ? __expf(Gt - sm.G[s + e]) * __uint_as_float(g[s + e]) : 0.f;
-                    const float x1 = s + e + 1 <= t && t < m ? __expf(Gt - sm.G[s + e + 1]) * __uint_as_float(g[s + e + 1]) : 0.f;
+                    const float x0 = s + e <= t && t < m ? ex2(Gt - sm.G[s + e]) * __uint_as_float(g[s + e]) : 0.f;
+                    const float x1 = s + e + 1 <= t && t < m ? ex2(Gt - sm.G[s + e + 1]) * __uint_as_float(g[s + e + 1]) : 0.f;
                     p[e / 2] = pack_bf16(x0, x1);
                 }
                 *reinterpret_cast<uint4 *>(sm.A + op_off(t, s, kC)) = make_uint4(p[0], p[1], p[2], p[3]);
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(128) gdr_tc_prep(GdrArgs a, const __grid_const
                 float x[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    x[e] = s + e < t && t < m ? wt * expf(Gt - sm.G[s + e]) * __uint_as_float(g[s + e]) : 0.f;
+                    x[e] = s + e < t && t < m ? wt * ex2(Gt - sm.G[s + e]) * __uint_as_float(g[s + e]) : 0.f;
                 *reinterpret_cast<float4 *>(&sm.M[t][s]) = make_float4(x[0], x[1], x[2], x[3]);
             }
         }
