@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
     constexpr uint32_t cHi = 128, cLo = 192, cX = 256, cP = 320, cY = 384, cD = 448;
     bool ok = true;
     auto wait = [&](uint64_t &bar, int phase) {   // by a whole warp
-        return (bool)__all_sync(0xffffffffu, mbar_wait(&bar, phase & 1, kSwaWait));
+        return (bool)__all_sync(0xffffffffu, mbar_wait_idle(&bar, phase & 1, kIdleWait));
     };
 
     if (warp >= kRegWarps) regs_down<64>();
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
             const int s = i & 1, c = chunks - 1 - i;
             if (i >= 2) ok = wait(sm.free[s], i / 2 - 1);
             if (!ok) break;
-            if (lane == 0) {
+            if (elect_one()) {
                 const int row = (int)(row0 + (long long)c * kC);
                 mbar_expect_tx(&sm.full[s], 2 * kC * K * 2 + kC * V * 2 + sizeof(GdrPrep));
                 for (int x = 0; x < VH; ++x) tma_load_3d(sm.dO[s][x], &md, 64 * x, h, row, &sm.full[s]);
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
             }
-            if (lane == 0) {
+            if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                     umma_bf16(tm + cP, umma_desc_mn(smem_u32(sm.dO[s][0]) + 2048 * kk, kTile64),
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
             __syncwarp();
             if (!(ok = wait(sm.sready, i))) break;
             tc_fence_after_sync();
-            if (lane == 0) {
+            if (elect_one()) {
 #pragma unroll
                 for (int lo = 0; lo < 2; ++lo)
 #pragma unroll
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
             __syncwarp();
             if (!(ok = wait(sm.uready, i))) break;
             tc_fence_after_sync();
-            if (lane == 0) {
+            if (elect_one()) {
                 const uint32_t th = smem_u32(sm.p[s].t_hi), tl = smem_u32(sm.p[s].t_lo);
 #pragma unroll
                 for (int x = 0; x < 3; ++x)   // dU hi Tm hi, dU lo Tm hi, dU hi Tm lo
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
             __syncwarp();
             if (!(ok = wait(sm.yready, i))) break;
             tc_fence_after_sync();
-            if (lane == 0) {
+            if (elect_one()) {
 #pragma unroll
                 for (int lo = 0; lo < 2; ++lo)
 #pragma unroll
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
             }
             __syncwarp();
         }
-        if (lane == 0) umma_commit(&sm.drain);   // products in flight finish before the tensor memory is freed
+        if (elect_one()) umma_commit(&sm.drain);   // products in flight finish before the tensor memory is freed
         __syncwarp();
         wait(sm.drain, 0);
     } else if (warp == kRegWarps + 2) {
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
         for (int i = 0; i < chunks && ok; ++i) {
             const int c = chunks - 1 - i;
             if (!(ok = wait(sm.Sout, i))) break;
-            if (lane == 0) {
+            if (elect_one()) {
                 bulk_s2g(keep[(size_t)c * a.Hv].S, sm.S, sizeof(sm.S));
                 bulk_commit();
                 bulk_wait_read<0>();
@@ -194,14 +194,14 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
             }
             __syncwarp();
             if (!(ok = wait(sm.yout, i))) break;
-            if (lane == 0) bulk_s2g(keep[(size_t)c * a.Hv].x, sm.y, sizeof(sm.y));
+            if (elect_one()) bulk_s2g(keep[(size_t)c * a.Hv].x, sm.y, sizeof(sm.y));
             for (int t = lane; t < min(kC, len - c * kC); t += 32)
                 bulk_s2g(static_cast<__nv_bfloat16 *>(a.dv) + ((size_t)(row0 + (long long)c * kC + t) * a.Hv + h) * V,
                          sm.dv + t * V, V * 2);
             bulk_commit();
             bulk_wait_read<0>();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.yfree);
+            if (elect_one()) mbar_arrive(&sm.yfree);
         }
         bulk_wait<0>();
     } else if (warp < kRegWarps) {
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
     constexpr uint32_t cX = 0, cY = 128, cA = 256, cD = 384, cKK = 448;
     bool ok = true;
     auto wait = [&](uint64_t &bar, int phase) {   // by a whole warp
-        return (bool)__all_sync(0xffffffffu, mbar_wait(&bar, phase & 1, kSwaWait));
+        return (bool)__all_sync(0xffffffffu, mbar_wait_idle(&bar, phase & 1, kIdleWait));
     };
     const int items = (int)a.seq.n_tiles(kC) * a.Hk;   // below 2^28
     int it = 0, j = 0;   // items and heads so far (those of used tiles)
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                 const size_t slot = (size_t)tile * a.Hv + h;
                 const Keep *fwd = reinterpret_cast<const Keep *>(a.saved) + slot, *bwd = reinterpret_cast<const Keep *>(a.ws) + slot;
                 if (j >= 2 && !(ok = wait(sm.vfree[s], j / 2 - 1))) break;
-                if (lane == 0) {
+                if (elect_one()) {
                     mbar_expect_tx(&sm.vfull[s], sizeof(sm.vec[0]));
                     bulk_g2s(sm.vec[s], reinterpret_cast<const GdrPrep *>(a.prep)[slot].eG, sizeof(sm.vec[0]), &sm.vfull[s]);
                 }
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                 if (g == 0) {
                     const int b = it & 1;
                     if (it >= 2 && !(ok = wait(sm.qkfree[b], it / 2 - 1))) break;
-                    if (lane == 0) {
+                    if (elect_one()) {
                         mbar_expect_tx(&sm.qkfull[b], 2 * kC * K * 2);
                         for (int x = 0; x < KH; ++x) {
                             tma_load_3d(sm.qk[b][x], &mq, 64 * x, hk, (int)row, &sm.qkfull[b]);
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                     __syncwarp();
                 }
                 if (j > 0 && !(ok = wait(sm.dfree, j - 1))) break;
-                if (lane == 0) {
+                if (elect_one()) {
                     mbar_expect_tx(&sm.dfull, 3 * kC * V * 2);
                     for (int x = 0; x < VH; ++x) {
                         tma_load_3d(sm.d[x], &md, 64 * x, h, (int)row, &sm.dfull);
@@ -437,13 +437,13 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                 }
                 __syncwarp();
                 if (j > 0 && !(ok = wait(sm.s0free, j - 1))) break;
-                if (lane == 0) {
+                if (elect_one()) {
                     mbar_expect_tx(&sm.s0full, sizeof(sm.S0));
                     bulk_g2s(sm.S0, fwd->S, sizeof(sm.S0), &sm.s0full);
                 }
                 __syncwarp();
                 if (j > 0 && !(ok = wait(sm.s1free, j - 1))) break;
-                if (lane == 0) {
+                if (elect_one()) {
                     mbar_expect_tx(&sm.s1full, sizeof(sm.S1));
                     bulk_g2s(sm.S1, bwd->S, sizeof(sm.S1), &sm.s1full);
                 }
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                 }
                 if (j > 0 && !(ok = wait(sm.Dfree, j - 1))) break;
                 tc_fence_after_sync();
-                if (g == 0 && lane == 0) {
+                if (g == 0 && elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < K / 16; ++kk) {
                         const uint32_t x = qk + 2 * kTile64 * (kk / 4) + 32 * (kk % 4);
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                 }
                 __syncwarp();
                 if (!(ok = wait(sm.dfull, j))) break;
-                if (lane == 0) {
+                if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < V / 16; ++kk) {
                         const uint32_t x = d + 3 * kTile64 * (kk / 4) + 32 * (kk % 4);
@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                 if (!(ok = wait(sm.s0full, j))) break;
                 if (j > 0 && !(ok = wait(sm.xfree, j - 1))) break;
                 tc_fence_after_sync();
-                if (lane == 0) {
+                if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < V / 16; ++kk)
                         umma_bf16(tm + cX, umma_desc(d + 3 * kTile64 * (kk / 4) + 32 * (kk % 4)),
@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                 if (!(ok = wait(sm.s1full, j))) break;
                 if (j > 0 && !(ok = wait(sm.yfree, j - 1))) break;
                 tc_fence_after_sync();
-                if (lane == 0) {
+                if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < V / 16; ++kk)   // [dY; U] dS1, of which the lanes of U count
                         umma_bf16(tm + cY, umma_desc(d + kTile64 + 3 * kTile64 * (kk / 4) + 32 * (kk % 4)),
@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                 if (!(ok = wait(sm.pready, j))) break;
                 if (g == 0 && it > 0 && !(ok = wait(sm.afree, it - 1))) break;
                 tc_fence_after_sync();
-                if (lane == 0) {
+                if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)   // [P1; P2] K
                         umma_bf16(tm + cA, umma_desc(P + kTile64 + 32 * kk), umma_desc_mn(qk + kTile64 + 2048 * kk, 2 * kTile64), iK,
@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
             }
             ++it;
         }
-        if (lane == 0) umma_commit(&sm.drain);
+        if (elect_one()) umma_commit(&sm.drain);
         __syncwarp();
         wait(sm.drain, 0);
     } else if (warp == kRegWarps + 2) {
@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                         dlog += __shfl_xor_sync(0xffffffffu, dlog, off);
                         damp += __shfl_xor_sync(0xffffffffu, damp, off);
                     }
-                    if (lane == 0) {
+                    if (elect_one()) {
                         part[((size_t)tile * a.Hv + h) * 2] = damp;
                         part[((size_t)tile * a.Hv + h) * 2 + 1] = dlog;
                     }
@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
             if (!a.seq.find(tile, kC, n, c, row, len)) continue;
             row += (long long)c * kC;
             if (!(ok = wait(sm.oready, it))) break;
-            if (lane == 0) {
+            if (elect_one()) {
                 if (len - c * kC >= kC)
                     for (int x = 0; x < KH; ++x) {
                         tma_store_3d(&mdq, sm.qk[it & 1][x], 64 * x, hk, (int)row);

@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(128) gdr_tc_prep(GdrArgs a, const __grid_const
     const uint32_t tm = sm.tmem;
     bool ok = true;
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             mbar_expect_tx(&sm.full, 128 * K * 2);
             for (int x = 0; x < K / 64; ++x) {
                 tma_load_3d(sm.qk[x], &mq, 64 * x, hk, (int)row, &sm.full);
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(128) gdr_tc_prep(GdrArgs a, const __grid_const
             }
         }
         ok = __all_sync(0xffffffffu, mbar_wait(&sm.full, 0, kSwaWait));
-        if (ok && lane == 0) {
+        if (ok && elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < K / 16; ++kk)
                 umma_bf16(tm, umma_desc(smem_u32(sm.qk[kk / 4]) + 32 * (kk % 4)),
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
     constexpr uint32_t cHi = 128, cLo = 192, cG = 256, cU = 320, cQ = 384, cA = 448;
     bool ok = true;
     auto wait = [&](uint64_t &bar, int phase) {   // by a whole warp
-        return (bool)__all_sync(0xffffffffu, mbar_wait(&bar, phase & 1, kSwaWait));
+        return (bool)__all_sync(0xffffffffu, mbar_wait_idle(&bar, phase & 1, kIdleWait));
     };
 
     if (warp >= kRegWarps) regs_down<64>();
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
             const int s = c & 1;
             if (c >= 2) ok = wait(sm.free[s], c / 2 - 1);
             if (!ok) break;
-            if (lane == 0) {
+            if (elect_one()) {
                 const int row = (int)(row0 + (long long)c * kC);
                 mbar_expect_tx(&sm.full[s], 2 * kC * K * 2 + kC * V * 2 + sizeof(GdrPrep));
                 for (int x = 0; x < KH; ++x) tma_load_3d(sm.k[s][x], &mk, 64 * x, hk, row, &sm.full[s]);
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
             }
             if (!(ok = wait(sm.sready, c))) break;
             tc_fence_after_sync();
-            if (lane == 0) {
+            if (elect_one()) {
 #pragma unroll
                 for (int lo = 0; lo < 2; ++lo)
 #pragma unroll
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
             __syncwarp();
             if (!(ok = wait(sm.rready, c))) break;
             tc_fence_after_sync();
-            if (lane == 0) {
+            if (elect_one()) {
                 const uint32_t th = smem_u32(sm.p[s].t_hi), tl = smem_u32(sm.p[s].t_lo);
 #pragma unroll
                 for (int x = 0; x < 3; ++x)   // R hi Tm hi, R lo Tm hi, R hi Tm lo
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
             // in the shadow of the pass over U
             if (c > 0 && !(ok = wait(sm.oread, c - 1))) break;
             tc_fence_after_sync();
-            if (lane == 0) {
+            if (elect_one()) {
 #pragma unroll
                 for (int lo = 0; lo < 2; ++lo)
 #pragma unroll
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
             __syncwarp();
             if (!(ok = wait(sm.uready, c))) break;
             tc_fence_after_sync();
-            if (lane == 0) {
+            if (elect_one()) {
 #pragma unroll
                 for (int lo = 0; lo < 2; ++lo)
 #pragma unroll
@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
             }
             __syncwarp();
         }
-        if (lane == 0) umma_commit(&sm.drain);   // products in flight finish before the tensor memory is freed
+        if (elect_one()) umma_commit(&sm.drain);   // products in flight finish before the tensor memory is freed
         __syncwarp();
         wait(sm.drain, 0);
     } else if (warp == kRegWarps + 2) {
@@ -420,20 +420,20 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
             }
             if (SAVE && c < chunks) {
                 if (!(ok = wait(sm.Sout, c))) break;
-                if (lane == 0) {
+                if (elect_one()) {
                     bulk_s2g(keep[(size_t)c * a.Hv].S, sm.S, sizeof(sm.S));
                     bulk_commit();
                 }
                 __syncwarp();
                 if (!(ok = wait(sm.uout, c))) break;
-                if (lane == 0) {
+                if (elect_one()) {
                     bulk_s2g(keep[(size_t)c * a.Hv].x, sm.u, sizeof(sm.u));
                     bulk_commit();
                 }
             }
             bulk_wait_read<0>();
             __syncwarp();
-            if (lane == 0) {
+            if (elect_one()) {
                 if (c > 0) mbar_arrive(&sm.ofree);
                 if (SAVE && c < chunks) {
                     mbar_arrive(&sm.Sfree);

@@ -133,6 +133,7 @@ __device__ __forceinline__ int last_query(int j0, int j1, int len, int window, i
 // Polls of a bounded barrier wait of the tensor-core kernels here (each poll may suspend the thread
 // for a while: of the order of a second, far beyond any copy or product that completes).
 constexpr uint32_t kSwaWait = 1u << 22;
+constexpr uint32_t kIdleWait = 1u << 17;   // of polls that suspend for up to 20 us
 
 // sizes of the delta rule's buffers for one path, in bytes
 struct GdrSizes {

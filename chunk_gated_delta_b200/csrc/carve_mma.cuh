@@ -134,6 +134,15 @@ __device__ __forceinline__ void load_b_kn_swz(uint32_t (&b)[4], const __nv_bfloa
     ldsm_x4_t(b, smem_u32(base + swz128(k, n)));
 }
 
+// True for one lane of a converged warp, the same one each time.  Copies and tensor-core instructions
+// are issued behind this: their operands then stay in uniform registers, where behind `lane == 0` each
+// is moved there lane by lane (16 products N = 64 beside busy warps: 940 cycles against 1780).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p;
+}
+
 // ---- mbarrier + bulk copy (global -> shared through the TMA engine) ------------------------
 __device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(bar)), "r"(count));
@@ -154,6 +163,21 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint32
             "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
             : "=r"(done)
             : "r"(a), "r"(parity));
+        if (done) return true;
+    }
+    return false;
+}
+
+// The same for kernels whose warps wait most of the time: a poll may suspend the warp for 20 us (a
+// hint), so that waiting warps leave the issue slots to the others.
+__device__ __forceinline__ bool mbar_wait_idle(uint64_t *bar, uint32_t parity, uint32_t limit) {
+    const uint32_t a = smem_u32(bar);
+    for (uint32_t it = 0; it < limit; ++it) {
+        uint32_t done;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(done)
+            : "r"(a), "r"(parity), "r"(20000u));
         if (done) return true;
     }
     return false;

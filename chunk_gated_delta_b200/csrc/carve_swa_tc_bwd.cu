@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             const int x = nu & 1;
             if (nu >= 2) ok = wait(sm.rfree[x], nu / 2 - 1);
             if (!ok) break;
-            if (lane == 0) {
+            if (elect_one()) {
                 mbar_expect_tx(&sm.rfull[x], 2 * BR * D * 2);
                 for (int y = 0; y < KH; ++y) {
                     tma_load_3d(sm.r[x][0][y], &mr1, 64 * y, w.head, (int)w.row0 + w.r0, &sm.rfull[x]);
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 const int s = nc % kStages, c0 = w.col0(b), h = w.col_head(a, b);
                 if (nc >= kStages) ok = wait(sm.cfree[s], nc / kStages - 1);
                 if (!ok) break;
-                if (lane == 0) {
+                if (elect_one()) {
                     mbar_expect_tx(&sm.cfull[s], 2 * BC * D * 2);
                     for (int y = 0; y < KH; ++y) {
                         tma_load_3d(sm.c[s][0][y], &mc1, 64 * y, h, (int)w.row0 + c0, &sm.cfull[s]);
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 __syncwarp();
             }
             tc_fence_after_sync();
-            if (lane == 0) {
+            if (elect_one()) {
 #pragma unroll
                 for (int y = 0; y < 2; ++y)
 #pragma unroll
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 if (ok && b == 0 && nu > 0) ok = wait(sm.accfree, nu - 1);
                 if (!ok) break;
                 tc_fence_after_sync();
-                if (lane == 0) {
+                if (elect_one()) {
                     const int s = nc % kStages;
 #pragma unroll
                     for (int kk = 0; kk < BC / 16; ++kk)

@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     };
 
     if (warp == 16) {
-        if (lane == 0) {
+        if (elect_one()) {
             mbar_expect_tx(&sm.qfull, 2 * BM * D * 2);
             for (int t = 0; t < 2; ++t)
                 for (int x = 0; x < KH; ++x)
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         constexpr uint32_t iS = umma_idesc_bf16(BM, BN), iO = umma_idesc_bf16(BM, D) | kUmmaBmn;
         int ns[2] = {0, 0}, np[2] = {0, 0};   // products S and P V issued, per tile
         auto issue_s = [&](int t, int slot) {
-            if (lane == 0) {
+            if (elect_one()) {
                 for (int kk = 0; kk < D / 16; ++kk)
                     umma_bf16(tm + 128 * t, umma_desc(smem_u32(sm.q[t][kk / 4]) + 32 * (kk % 4)),
                               umma_desc(smem_u32(sm.kv[slot][kk / 4]) + 32 * (kk % 4)), iS, kk > 0);
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         if (ok) {
             for (int t = 0; t < 2; ++t)
                 if (w.sees(a, t, w.kt.tile(0) * BN)) issue_s(t, 0);
-            if (lane == 0) umma_commit(&sm.kvfree[0]);
+            if (elect_one()) umma_commit(&sm.kvfree[0]);
         }
         for (int b = 0; b < blocks && ok; ++b) {
             const int vs = (2 * b + 1) % kStages, ks = (2 * b + 2) % kStages;
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     ok = wait(sm.pfull[t], np[t]);
                     if (!ok) break;
                     tc_fence_after_sync();
-                    if (lane == 0) {
+                    if (elect_one()) {
                         for (int kk = 0; kk < BN / 16; ++kk)
                             umma_bf16_ta(tm + 256 + 128 * t, tm + 128 * t + 8 * kk + (kk < 4 ? 0 : 32),
                                          umma_desc_mn(smem_u32(sm.kv[vs][0]) + 2048 * kk, BN * 128), iO, kk > 0 || np[t] > 0);
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 }
                 if (b + 1 < blocks && w.sees(a, t, j1)) issue_s(t, ks);
             }
-            if (lane == 0) {
+            if (elect_one()) {
                 umma_commit(&sm.kvfree[vs]);
                 if (b + 1 < blocks) umma_commit(&sm.kvfree[ks]);
             }
