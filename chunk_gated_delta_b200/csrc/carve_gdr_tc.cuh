@@ -61,15 +61,81 @@ template <int N>
 __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
 
 // A split [lane][64 tokens] operand in tensor memory lies over the accumulator it comes from: 16
-// tokens' hi terms in 8 columns, then their lo terms, so that a thread overwrites only what it has
-// read itself.
+// tokens' hi terms in 8 columns, then their lo terms, so that a warp overwrites only what it has read
+// itself.
 __device__ __forceinline__ uint32_t split_col(int kk, int lo) { return 16 * kk + 8 * lo; }
-// 16 tokens x[] of this lane as such an operand
-__device__ __forceinline__ void put_split16(uint32_t taddr, const float *x) {
-    uint32_t y[16];
+
+// A register warp's 32 value rows x 16 tokens of an accumulator as fragments: x[y][4 j + 2 i + e] is row
+// 16 y + 8 i + lane / 4, token 8 j + 2 (lane % 4) + e.  In this layout a token tile's rows [token][channel]
+// are read and written by ldmatrix / stmatrix.trans (two each) and a factor of the tokens is two
+// 8-byte loads; with a lane a row they took 16 two-byte accesses and 16 loads.
+struct Frag {
+    float x[2][8];
+    __device__ __forceinline__ void load(uint32_t taddr) {   // followed by ready()
+        tmem_ld_frag2(taddr, reinterpret_cast<uint32_t *>(x[0]));
+        tmem_ld_frag2(taddr + (16u << 16), reinterpret_cast<uint32_t *>(x[1]));
+    }
+    __device__ __forceinline__ void ready() { tmem_tie16(reinterpret_cast<uint32_t *>(x[0])); }
+};
+// the thread's four of 16 factors
+struct Factor {
+    float f[4];
+    __device__ __forceinline__ Factor(const float *p, int lane) {
+        const float2 a = *reinterpret_cast<const float2 *>(p + 2 * (lane % 4)), b = *reinterpret_cast<const float2 *>(p + 8 + 2 * (lane % 4));
+        f[0] = a.x;
+        f[1] = a.y;
+        f[2] = b.x;
+        f[3] = b.y;
+    }
+    __device__ __forceinline__ float operator[](int i) const { return f[2 * (i / 4) + i % 2]; }   // of x[.][i]
+};
+// fragments as a split operand over the accumulator at taddr
+__device__ __forceinline__ void put_split(uint32_t taddr, const Frag &a) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) split_pair(x[2 * i], x[2 * i + 1], y[i], y[8 + i]);
-    tmem_st16(taddr, y);
+    for (int y = 0; y < 2; ++y) {
+        uint32_t p[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) split_pair(a.x[y][2 * i], a.x[y][2 * i + 1], p[i], p[4 + i]);
+        tmem_st_frag4(taddr + ((16u * y) << 16), p);
+    }
+}
+// the address of this lane's row of the four 8 x 8 matrices (tokens c16 .. + 15, channels r0 .. + 15) of a
+// [64][channels] tile in operand layout
+__device__ __forceinline__ uint32_t tile_row(const __nv_bfloat16 *tile, int c16, int r0, int lane) {
+    return smem_u32(tile + op_off(c16 + (lane / 16) * 8 + lane % 8, r0 + ((lane / 8) & 1) * 8, kC));
+}
+__device__ __forceinline__ void load_tokens(uint32_t (&v)[2][4], const __nv_bfloat16 *tile, int c16, int r0, int lane) {
+    ldsm_x4_t(v[0], tile_row(tile, c16, r0, lane));
+    ldsm_x4_t(v[1], tile_row(tile, c16, r0 + 16, lane));
+}
+__device__ __forceinline__ float bf16_of(const uint32_t (&v)[4], int i) {   // x[.][i]'s counterpart
+    return __uint_as_float(i % 2 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16);
+}
+__device__ __forceinline__ void store_tokens(__nv_bfloat16 *tile, int c16, int r0, int lane, const Frag &a) {
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+        stsm_x4_t(tile_row(tile, c16, r0 + 16 * y, lane), pack_bf16(a.x[y][0], a.x[y][1]), pack_bf16(a.x[y][2], a.x[y][3]),
+                  pack_bf16(a.x[y][4], a.x[y][5]), pack_bf16(a.x[y][6], a.x[y][7]));
+}
+// a [64][V] tile in operand layout to rows row .. of head h (one warp, its own bulk group): by TMA, or, when only m
+// rows are the sequence's, row by row
+template <int V>
+__device__ __forceinline__ void store_tile(const CUtensorMap *map, void *dst, const __nv_bfloat16 *tile, long long row, int m, int H,
+                                           int h, int lane) {
+    if (m >= kC) {
+        if (elect_one()) {
+            for (int x = 0; x < V / 64; ++x) tma_store_3d(map, tile + x * kC * 64, 64 * x, h, (int)row);
+            bulk_commit();
+            bulk_wait_read<0>();
+        }
+    } else {
+        for (int i = lane; i < m * (V / 8); i += 32) {
+            const int t = i / (V / 8), x = i % (V / 8) * 8;
+            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(dst) + ((size_t)(row + t) * H + h) * V + x) =
+                *reinterpret_cast<const uint4 *>(tile + op_off(t, x, kC));
+        }
+    }
+    __syncwarp();
 }
 // A row's part of the state, COLS columns from x0: operands hi, lo and the accumulator times gl; the hi
 // terms stay in hi[] when the state is kept

@@ -56,7 +56,7 @@ struct BsweepSmem {
 template <int K, int V>
 __global__ void __launch_bounds__(kSweepThreads, 1)
     gdr_tc_bsweep(GdrArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                  const __grid_constant__ CUtensorMap md) {
+                  const __grid_constant__ CUtensorMap md, const __grid_constant__ CUtensorMap mdv) {
     extern __shared__ __align__(16) unsigned char raw[];
     typedef BsweepSmem<K, V> Smem;
     Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
@@ -70,8 +70,9 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
     const int chunks = (len + kC - 1) / kC;
     if (threadIdx.x == 0) {
         for (uint64_t *b : {&sm.full[0], &sm.full[1], &sm.free[0], &sm.free[1], &sm.gfull, &sm.yfull, &sm.sfull, &sm.Sfree,
-                            &sm.yfree, &sm.drain})
+                            &sm.drain})
             mbar_init(b, 1);
+        mbar_init(&sm.yfree, 2);
         for (uint64_t *b : {&sm.sready, &sm.uready, &sm.yready, &sm.Sout, &sm.yout}) mbar_init(b, kRegWarps);
         fence_mbar_init();
     }
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
     } else if (warp == kRegWarps + 2) {
         typedef GdrKeep<K, V> Keep;
         Keep *keep = reinterpret_cast<Keep *>(a.ws) + (size_t)t0 * a.Hv + h;
-        for (int i = 0; i < chunks && ok; ++i) {
+        for (int i = 0; i < chunks; ++i) {
             const int c = chunks - 1 - i;
             if (!(ok = wait(sm.Sout, i))) break;
             if (elect_one()) {
@@ -194,30 +195,38 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
             }
             __syncwarp();
             if (!(ok = wait(sm.yout, i))) break;
-            if (elect_one()) bulk_s2g(keep[(size_t)c * a.Hv].x, sm.y, sizeof(sm.y));
-            for (int t = lane; t < min(kC, len - c * kC); t += 32)
-                bulk_s2g(static_cast<__nv_bfloat16 *>(a.dv) + ((size_t)(row0 + (long long)c * kC + t) * a.Hv + h) * V,
-                         sm.dv + t * V, V * 2);
-            bulk_commit();
-            bulk_wait_read<0>();
+            if (elect_one()) {
+                bulk_s2g(keep[(size_t)c * a.Hv].x, sm.y, sizeof(sm.y));
+                bulk_commit();
+                bulk_wait_read<0>();
+                mbar_arrive(&sm.yfree);
+            }
             __syncwarp();
+        }
+        bulk_wait<0>();
+    } else if (warp == kRegWarps + 3) {
+        for (int i = 0; i < chunks; ++i) {
+            const int c = chunks - 1 - i;
+            if (!(ok = wait(sm.yout, i))) break;
+            store_tile<V>(&mdv, a.dv, sm.dv, row0 + (long long)c * kC, len - c * kC, a.Hv, h, lane);
             if (elect_one()) mbar_arrive(&sm.yfree);
+            __syncwarp();
         }
         bulk_wait<0>();
     } else if (warp < kRegWarps) {
         regs_up<104>();
         const int part = warp / 4, quarter = warp % 4, r = quarter * 32 + lane;
         const uint32_t tl = tm + ((uint32_t)quarter << 21);
-        const int x0 = part * KQ, c16 = part * 16;   // this thread's columns of dS, its tokens
-        const bool live = r < V;                     // value row (others carry zeros)
+        const int x0 = part * KQ, c16 = part * 16;   // this warp's columns of dS, its tokens
+        const bool live = quarter * 32 < V;          // value rows (others carry zeros)
         const size_t st = (((size_t)n * a.Hv + h) * V + (live ? r : 0)) * K + x0;
         float S[KQ];
         load_row<KQ>(S, live && a.dS_final ? a.dS_final + st : nullptr);
+        Frag y;
         for (int i = 0; i < chunks; ++i) {
             const int s = i & 1, c = chunks - 1 - i, m = min(kC, len - c * kC);
             const GdrPrep &p = sm.p[s];
-            uint32_t hi[KQ / 2], x[16];
-            float y[16];
+            uint32_t hi[KQ / 2];
             // dS1 as operands, the accumulator scaled by e^{G_C}
             if (!(ok = wait(sm.full[s], i / 2))) break;
             put_state<KQ>(tl + x0, tl + cHi + x0 / 2, tl + cLo + x0 / 2, S, p.eG[kC - 1], hi);
@@ -229,55 +238,56 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                     *reinterpret_cast<uint4 *>(sm.S + op_off(r, x0 + 2 * e, V)) = make_uint4(hi[e], hi[e + 1], hi[e + 2], hi[e + 3]);
             fence_proxy_async_smem();
             mbar_arrive_warp(&sm.Sout);
-            // e^G dO, transposed
-            const __nv_bfloat16 *dO = sm.dO[s][0];
+            const Factor eG(p.eG + c16, lane), w(p.w + c16, lane);
+            {   // e^G dO, transposed
+                uint32_t d[2][4] = {};
+                if (live) load_tokens(d, sm.dO[s][0], c16, quarter * 32, lane);
 #pragma unroll
-            for (int t = 0; t < 16; ++t)
-                y[t] = c16 + t < m && live ? p.eG[c16 + t] * __bfloat162float(dO[op_off(c16 + t, r, kC)]) : 0.f;
-            uint32_t d[16];
+                for (int e = 0; e < 16; ++e) y.x[e / 8][e % 8] = eG[e % 8] * bf16_of(d[e / 8], e % 8);
+                if (m < kC)   // rows behind the end may hold anything
 #pragma unroll
-            for (int t = 0; t < 8; ++t) split_pair(y[2 * t], y[2 * t + 1], d[t], d[8 + t]);
-            // dU
-            if (!(ok = wait(sm.gfull, i))) break;
-            tc_fence_after_sync();
-            {
-                uint32_t pa[16];
-                tmem_ld16(tl + cX + c16, x);
-                tmem_ld16(tl + cP + c16, pa);
-                tmem_wait_ld();
-                tmem_tie16(x);
-                tmem_tie16(pa);
-#pragma unroll
-                for (int t = 0; t < 16; ++t) y[t] = fmaf(p.eK[c16 + t], __uint_as_float(x[t]), __uint_as_float(pa[t]));
+                    for (int e = 0; e < 16; ++e)
+                        if (c16 + 8 * (e % 8 / 4) + 2 * (lane % 4) + e % 2 >= m) y.x[e / 8][e % 8] = 0.f;
+                put_split(tl + cD + c16, y);
             }
-            put_split16(tl + cX + c16, y);
-            tmem_st16(tl + cD + c16, d);
+            // dU
+            {
+                Frag pa;
+                const Factor eK(p.eK + c16, lane);
+                if (!(ok = wait(sm.gfull, i))) break;
+                tc_fence_after_sync();
+                y.load(tl + cX + c16);
+                pa.load(tl + cP + c16);
+                tmem_wait_ld();
+                y.ready();
+                pa.ready();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) y.x[e / 8][e % 8] = fmaf(eK[e % 8], y.x[e / 8][e % 8], pa.x[e / 8][e % 8]);
+            }
+            put_split(tl + cX + c16, y);
             tmem_wait_st();
             tc_fence_before_sync();
             mbar_arrive_warp(&sm.uready);
             // dY
             if (!(ok = wait(sm.yfull, i))) break;
             tc_fence_after_sync();
-            tmem_ld16(tl + cY + c16, x);
+            y.load(tl + cY + c16);
             tmem_wait_ld();
-            tmem_tie16(x);
-            float dv[16];
+            y.ready();
+            Frag z;
 #pragma unroll
-            for (int t = 0; t < 16; ++t) {
-                dv[t] = p.w[c16 + t] * __uint_as_float(x[t]);
-                y[t] = -p.eG[c16 + t] * dv[t];
-            }
-            put_split16(tl + cY + c16, y);
+            for (int e = 0; e < 16; ++e) z.x[e / 8][e % 8] = -eG[e % 8] * (w[e % 8] * y.x[e / 8][e % 8]);
+            put_split(tl + cY + c16, z);
             tmem_wait_st();
             tc_fence_before_sync();
             mbar_arrive_warp(&sm.yready);
             if (i > 0 && !(ok = wait(sm.yfree, i - 1))) break;
-            if (live)
+            if (live) {
+                store_tokens(sm.y, c16, quarter * 32, lane, y);
 #pragma unroll
-                for (int t = 0; t < 16; ++t) {
-                    sm.y[op_off(c16 + t, r, kC)] = __float2bfloat16_rn(__uint_as_float(x[t]));
-                    sm.dv[(c16 + t) * V + r] = __float2bfloat16_rn(dv[t]);
-                }
+                for (int e = 0; e < 16; ++e) y.x[e / 8][e % 8] *= w[e % 8];
+                store_tokens(sm.dv, c16, quarter * 32, lane, y);
+            }
             fence_proxy_async_smem();
             mbar_arrive_warp(&sm.yout);
             // dS0
@@ -815,7 +825,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
 template <int K, int V>
 cudaError_t bwd_t(const GdrArgs &a, cudaStream_t st) {
     const long long rows = a.seq.cu ? a.seq.total : (long long)a.seq.N * a.seq.T;
-    CUtensorMap mq{}, mk{}, md{}, mdq{}, mdk{};
+    CUtensorMap mq{}, mk{}, md{}, mdq{}, mdk{}, mdv{};
     auto sweep = gdr_tc_bsweep<K, V>;
     auto grad = gdr_tc_grad<K, V>;
     const int sb = (int)sizeof(BsweepSmem<K, V>) + 1024, gb = (int)sizeof(GradSmem<K, V>) + 1024;
@@ -825,11 +835,12 @@ cudaError_t bwd_t(const GdrArgs &a, cudaStream_t st) {
         if (e == cudaSuccess) e = make_operand_tile_map(&mq, a.q, K, a.Hk, rows, kC);
         if (e == cudaSuccess) e = make_operand_tile_map(&mk, a.k, K, a.Hk, rows, kC);
         if (e == cudaSuccess) e = make_operand_tile_map(&md, a.dO, V, a.Hv, rows, kC);
+        if (e == cudaSuccess) e = make_operand_tile_map(&mdv, a.dv, V, a.Hv, rows, kC);
         if (e == cudaSuccess) e = make_operand_tile_map(&mdq, a.dq, K, a.Hk, rows, kC);
         if (e == cudaSuccess) e = make_operand_tile_map(&mdk, a.dk, K, a.Hk, rows, kC);
     }
     if (e != cudaSuccess) return e;
-    sweep<<<a.seq.N * a.Hv, kSweepThreads, sb, st>>>(a, mq, mk, md);
+    sweep<<<a.seq.N * a.Hv, kSweepThreads, sb, st>>>(a, mq, mk, md, mdv);
     const long long tiles = a.seq.n_tiles(kC), items = tiles * a.Hk;
     if (items) grad<<<(unsigned)(items < sm_count() ? items : sm_count()), kSweepThreads, gb, st>>>(a, mq, mk, md, mdq, mdk);
     if (a.dA_dec || a.dtau)

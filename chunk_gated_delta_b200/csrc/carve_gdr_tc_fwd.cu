@@ -14,7 +14,7 @@
 //   O = e^G Q S^T + U A^T (S, U hi, lo), two accumulators, off the chain
 // The chain of one chunk is three products and three register passes; what bounds the sweep is
 // their latency (B H units on 148 SMs, one chain each), not the tensor core's rate or HBM.
-// Warps 0-15 register passes, 16 copies in (TMA and bulk, two stages), 17 products, 18 copies out.  What
+// Warps 0-15 register passes, 16 copies in (TMA and bulk, two stages), 17 products, 18 and 19 copies out.  What
 // is not on the chain (outputs of the chunk before, copies of S and U) is done while a product runs.
 #include "carve_gdr_tc.cuh"
 
@@ -275,8 +275,8 @@ template <int K, int V, bool SAVE>
 struct SweepSmem {
     __nv_bfloat16 k[2][K / 64][kC * 64], q[2][K / 64][kC * 64];
     GdrPrep p[2];
-    __nv_bfloat16 v[2][kC * V];                     // plain rows
-    __nv_bfloat16 S[SAVE ? V * K : 8], u[SAVE ? kC * V : 8], o[kC * V];   // on their way out
+    __nv_bfloat16 v[2][V / 64][kC * 64];
+    __nv_bfloat16 S[SAVE ? V * K : 512], u[SAVE ? kC * V : 512], o[kC * V];   // on their way out
     float eG[2][kC];   // kept for the outputs beyond the stage
     uint64_t full[2], free[2], sready, gfull, rready, ufull, uready, sfull, ofull, oread, ofree;
     uint64_t Sout, Sfree, uout, ufree, oout, drain;
@@ -286,7 +286,7 @@ struct SweepSmem {
 template <int K, int V, bool SAVE>
 __global__ void __launch_bounds__(kSweepThreads, 1)
     gdr_tc_sweep(GdrArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                 const __grid_constant__ CUtensorMap mv) {
+                 const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo) {
     extern __shared__ __align__(16) unsigned char raw[];
     typedef SweepSmem<K, V, SAVE> Smem;
     Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                 for (int x = 0; x < KH; ++x) tma_load_3d(sm.k[s][x], &mk, 64 * x, hk, row, &sm.full[s]);
                 bulk_g2s(&sm.p[s], reinterpret_cast<const GdrPrep *>(a.prep) + (size_t)(t0 + c) * a.Hv + h, sizeof(GdrPrep),
                          &sm.full[s]);
-                tma_load_3d(sm.v[s], &mv, 0, h, row, &sm.full[s]);
+                for (int x = 0; x < V / 64; ++x) tma_load_3d(sm.v[s][x], &mv, 64 * x, h, row, &sm.full[s]);
                 for (int x = 0; x < KH; ++x) tma_load_3d(sm.q[s][x], &mq, 64 * x, hk, row, &sm.full[s]);
             }
         }
@@ -410,48 +410,43 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
     } else if (warp == kRegWarps + 2) {
         typedef GdrKeep<K, V> Keep;
         Keep *keep = SAVE ? reinterpret_cast<Keep *>(a.saved) + (size_t)t0 * a.Hv + h : nullptr;
-        for (int c = 0; c <= chunks && ok; ++c) {
-            if (c > 0) {   // outputs of the chunk before
-                if (!(ok = wait(sm.oout, c - 1))) break;
-                for (int t = lane; t < min(kC, len - (c - 1) * kC); t += 32)
-                    bulk_s2g(static_cast<__nv_bfloat16 *>(a.o) + ((size_t)(row0 + (long long)(c - 1) * kC + t) * a.Hv + h) * V,
-                             sm.o + t * V, V * 2);
-                bulk_commit();
-            }
-            if (SAVE && c < chunks) {
-                if (!(ok = wait(sm.Sout, c))) break;
-                if (elect_one()) {
-                    bulk_s2g(keep[(size_t)c * a.Hv].S, sm.S, sizeof(sm.S));
-                    bulk_commit();
-                }
-                __syncwarp();
-                if (!(ok = wait(sm.uout, c))) break;
-                if (elect_one()) {
-                    bulk_s2g(keep[(size_t)c * a.Hv].x, sm.u, sizeof(sm.u));
-                    bulk_commit();
-                }
-            }
-            bulk_wait_read<0>();
-            __syncwarp();
+        for (int c = 0; SAVE && c < chunks; ++c) {
+            if (!(ok = wait(sm.Sout, c))) break;
             if (elect_one()) {
-                if (c > 0) mbar_arrive(&sm.ofree);
-                if (SAVE && c < chunks) {
-                    mbar_arrive(&sm.Sfree);
-                    mbar_arrive(&sm.ufree);
-                }
+                bulk_s2g(keep[(size_t)c * a.Hv].S, sm.S, sizeof(sm.S));
+                bulk_commit();
+                bulk_wait_read<0>();
+                mbar_arrive(&sm.Sfree);
             }
+            __syncwarp();
+            if (!(ok = wait(sm.uout, c))) break;
+            if (elect_one()) {
+                bulk_s2g(keep[(size_t)c * a.Hv].x, sm.u, sizeof(sm.u));
+                bulk_commit();
+                bulk_wait_read<0>();
+                mbar_arrive(&sm.ufree);
+            }
+            __syncwarp();
+        }
+        bulk_wait<0>();
+    } else if (warp == kRegWarps + 3) {
+        for (int c = 0; c < chunks; ++c) {
+            if (!(ok = wait(sm.oout, c))) break;
+            store_tile<V>(&mo, a.o, sm.o, row0 + (long long)c * kC, len - c * kC, a.Hv, h, lane);
+            if (elect_one()) mbar_arrive(&sm.ofree);
+            __syncwarp();
         }
         bulk_wait<0>();
     } else if (warp < kRegWarps) {
         regs_up<104>();
         const int part = warp / 4, quarter = warp % 4, r = quarter * 32 + lane;
         const uint32_t tl = tm + ((uint32_t)quarter << 21);
-        const int x0 = part * KQ, c16 = part * 16;   // this thread's columns of S, its tokens
-        const bool live = r < V;                     // value row (others carry zeros)
+        const int x0 = part * KQ, c16 = part * 16;   // this warp's columns of S, its tokens
+        const bool live = quarter * 32 < V;          // value rows (others carry zeros)
         const size_t st = (((size_t)n * a.Hv + h) * V + (live ? r : 0)) * K + x0;
         float S[KQ];
         load_row<KQ>(S, live && a.S0 ? a.S0 + st : nullptr);
-        uint32_t x[16];
+        Frag y;
         for (int c = 0; c <= chunks; ++c) {
             const GdrPrep &p = sm.p[c & 1];
             uint32_t hi[KQ / 2];
@@ -461,42 +456,48 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                 mbar_arrive_warp(&sm.sready);
             }
             if (c > 0) {   // outputs of the chunk before, while the product runs
-                const float *eG = sm.eG[(c - 1) & 1] + c16;
+                const Factor eG(sm.eG[(c - 1) & 1] + c16, lane);
                 if (!(ok = wait(sm.ofull, c - 1))) break;
                 tc_fence_after_sync();
-                uint32_t z[16];
-                tmem_ld16(tl + cQ + c16, x);
-                tmem_ld16(tl + cA + c16, z);
+                Frag z;
+                y.load(tl + cQ + c16);
+                z.load(tl + cA + c16);
                 tmem_wait_ld();
-                tmem_tie16(x);
-                tmem_tie16(z);
+                y.ready();
+                z.ready();
                 tc_fence_before_sync();
                 mbar_arrive_warp(&sm.oread);
-                if (c > 1 && !(ok = wait(sm.ofree, c - 2))) break;
-                if (live)
 #pragma unroll
-                    for (int t = 0; t < 16; ++t)
-                        sm.o[(c16 + t) * V + r] = __float2bfloat16_rn(fmaf(eG[t], __uint_as_float(x[t]), __uint_as_float(z[t])));
+                for (int e = 0; e < 16; ++e) y.x[e / 8][e % 8] = fmaf(eG[e % 8], y.x[e / 8][e % 8], z.x[e / 8][e % 8]);
+                if (c > 1 && !(ok = wait(sm.ofree, c - 2))) break;
+                if (live) store_tokens(sm.o, c16, quarter * 32, lane, y);
                 fence_proxy_async_smem();
                 mbar_arrive_warp(&sm.oout);
             }
             if (c == chunks) break;
             const int m = min(kC, len - c * kC);
-            float y[16];
             if (quarter == 0 && lane < 16) sm.eG[c & 1][c16 + lane] = p.eG[c16 + lane];
             // R = w (v - e^G G)
-            const __nv_bfloat16 *v = sm.v[c & 1] + c16 * V + (live ? r : 0);
+            {
+                uint32_t v[2][4] = {};
+                if (live) load_tokens(v, sm.v[c & 1][0], c16, quarter * 32, lane);
+                const Factor eG(p.eG + c16, lane), w(p.w + c16, lane);
+                if (!(ok = wait(sm.gfull, c))) break;
+                tc_fence_after_sync();
+                y.load(tl + cG + c16);
+                tmem_wait_ld();
+                y.ready();
 #pragma unroll
-            for (int t = 0; t < 16; ++t) y[t] = __bfloat162float(v[t * V]);
-            if (!(ok = wait(sm.gfull, c))) break;
-            tc_fence_after_sync();
-            tmem_ld16(tl + cG + c16, x);
-            tmem_wait_ld();
-            tmem_tie16(x);
+                for (int e = 0; e < 16; ++e) {
+                    float &x = y.x[e / 8][e % 8];
+                    x = w[e % 8] * fmaf(-eG[e % 8], x, bf16_of(v[e / 8], e % 8));
+                }
+                if (m < kC)   // value rows behind the end may hold anything
 #pragma unroll
-            for (int t = 0; t < 16; ++t)
-                y[t] = c16 + t < m && live ? p.w[c16 + t] * (y[t] - p.eG[c16 + t] * __uint_as_float(x[t])) : 0.f;
-            put_split16(tl + cG + c16, y);
+                    for (int e = 0; e < 16; ++e)
+                        if (c16 + 8 * (e % 8 / 4) + 2 * (lane % 4) + e % 2 >= m) y.x[e / 8][e % 8] = 0.f;
+            }
+            put_split(tl + cG + c16, y);
             tmem_wait_st();
             tc_fence_before_sync();
             mbar_arrive_warp(&sm.rready);
@@ -510,23 +511,25 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                 mbar_arrive_warp(&sm.Sout);
             }
             // U
+            const Factor eK(p.eK + c16, lane);
             if (!(ok = wait(sm.ufull, c))) break;
             tc_fence_after_sync();
-            tmem_ld16(tl + cU + c16, x);
+            y.load(tl + cU + c16);
             tmem_wait_ld();
-            tmem_tie16(x);
+            y.ready();
+            {
+                Frag z;
 #pragma unroll
-            for (int t = 0; t < 16; ++t) y[t] = __uint_as_float(x[t]) * p.eK[c16 + t];
-            put_split16(tl + cU + c16, y);
-            put_split16(tl + cG + c16, reinterpret_cast<const float *>(x));
+                for (int e = 0; e < 16; ++e) z.x[e / 8][e % 8] = eK[e % 8] * y.x[e / 8][e % 8];
+                put_split(tl + cU + c16, z);
+            }
+            put_split(tl + cG + c16, y);
             tmem_wait_st();
             tc_fence_before_sync();
             mbar_arrive_warp(&sm.uready);
             if (SAVE) {
                 if (c > 0 && !(ok = wait(sm.ufree, c - 1))) break;
-                if (live)
-#pragma unroll
-                    for (int t = 0; t < 16; ++t) sm.u[op_off(c16 + t, r, kC)] = __float2bfloat16_rn(__uint_as_float(x[t]));
+                if (live) store_tokens(sm.u, c16, quarter * 32, lane, y);
                 fence_proxy_async_smem();
                 mbar_arrive_warp(&sm.uout);
             }
@@ -545,30 +548,32 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
 }
 
 template <int K, int V, bool SAVE>
-cudaError_t sweep_t(const GdrArgs &a, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t st) {
+cudaError_t sweep_t(const GdrArgs &a, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const CUtensorMap &mo,
+                    cudaStream_t st) {
     auto kern = gdr_tc_sweep<K, V, SAVE>;
     const int bytes = (int)sizeof(SweepSmem<K, V, SAVE>) + 1024;
     const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), bytes);
     if (e != cudaSuccess) return e;
-    kern<<<a.seq.N * a.Hv, kSweepThreads, bytes, st>>>(a, mq, mk, mv);
+    kern<<<a.seq.N * a.Hv, kSweepThreads, bytes, st>>>(a, mq, mk, mv, mo);
     return cudaGetLastError();
 }
 
 template <int K, int V>
 cudaError_t fwd_t(const GdrArgs &a, bool save, cudaStream_t st) {
     const long long rows = a.seq.cu ? a.seq.total : (long long)a.seq.N * a.seq.T;
-    CUtensorMap mq{}, mk{}, mv{};
+    CUtensorMap mq{}, mk{}, mv{}, mo{};
     if (rows > 0) {   // without rows no tile is copied; the sweep hands the states on
         cudaError_t e = make_operand_tile_map(&mq, a.q, K, a.Hk, rows, kC);
         if (e == cudaSuccess) e = make_operand_tile_map(&mk, a.k, K, a.Hk, rows, kC);
-        if (e == cudaSuccess) e = make_token_tile_map(&mv, a.v, 2, V, a.Hv, rows, kC);
+        if (e == cudaSuccess) e = make_operand_tile_map(&mv, a.v, V, a.Hv, rows, kC);
+        if (e == cudaSuccess) e = make_operand_tile_map(&mo, a.o, V, a.Hv, rows, kC);
         auto prep = gdr_tc_prep<K>;
         const int bytes = (int)sizeof(PrepSmem<K>) + 1024;
         if (e == cudaSuccess) e = set_smem_once(reinterpret_cast<const void *>(prep), bytes);
         if (e != cudaSuccess) return e;
         prep<<<(unsigned)(a.seq.n_tiles(kC) * a.Hk), 128, bytes, st>>>(a, mq, mk);
     }
-    return save ? sweep_t<K, V, true>(a, mq, mk, mv, st) : sweep_t<K, V, false>(a, mq, mk, mv, st);
+    return save ? sweep_t<K, V, true>(a, mq, mk, mv, mo, st) : sweep_t<K, V, false>(a, mq, mk, mv, mo, st);
 }
 
 }  // namespace
