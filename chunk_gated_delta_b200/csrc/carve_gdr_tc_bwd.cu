@@ -115,8 +115,14 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
             for (int j = max(0, i - 2); j < i; ++j) wait(sm.full[j & 1], j / 2);
     } else if (warp == kRegWarps + 1) {
         constexpr uint32_t iN64 = umma_idesc_bf16(128, 64), iS = umma_idesc_bf16(128, K) | kUmmaBmn;
+        const uint64_t dk0 = umma_desc(smem_u32(sm.k)), dkt0 = umma_desc_mn(smem_u32(sm.k), kTile64),
+                       dqt0 = umma_desc_mn(smem_u32(sm.q), kTile64), dt0 = umma_desc_mn(smem_u32(sm.p), kTile64),
+                       do0 = umma_desc_mn(smem_u32(sm.dO), kTile64);
         for (int i = 0; i < chunks; ++i) {
             const int s = i & 1, c = chunks - 1 - i;
+            const uint64_t dk = desc_at(dk0, s * KH * kTile64), dkt = desc_at(dkt0, s * KH * kTile64),
+                           dqt = desc_at(dqt0, s * KH * kTile64), dt = desc_at(dt0, s * sizeof(GdrPrep)),
+                           dd = desc_at(do0, s * 2 * kTile64);
             if (!(ok = wait(sm.full[s], i / 2))) break;
             if (len - c * kC < kC) {   // rows behind the end meet zero factors, so they have to be finite
                 zero_rows(sm.k[s], len - c * kC, KH, kTile64, lane);
@@ -128,8 +134,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
             if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    umma_bf16(tm + cP, umma_desc_mn(smem_u32(sm.dO[s][0]) + 2048 * kk, kTile64),
-                              umma_desc_mn(smem_u32(sm.p[s].A) + 2048 * kk, kTile64), iN64 | kUmmaAmn | kUmmaBmn, kk > 0);
+                    umma_bf16(tm + cP, desc_at(dd, 2048 * kk), desc_at(dt, 2 * kTile64 + 2048 * kk), iN64 | kUmmaAmn | kUmmaBmn, kk > 0);
             }
             __syncwarp();
             if (!(ok = wait(sm.sready, i))) break;
@@ -139,7 +144,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                 for (int lo = 0; lo < 2; ++lo)
 #pragma unroll
                     for (int kk = 0; kk < K / 16; ++kk)
-                        umma_bf16_ta(tm + cX, tm + (lo ? cLo : cHi) + 8 * kk, umma_desc(smem_u32(sm.k[s][kk / 4]) + 32 * (kk % 4)),
+                        umma_bf16_ta(tm + cX, tm + (lo ? cLo : cHi) + 8 * kk, desc_at(dk, kTile64 * (kk / 4) + 32 * (kk % 4)),
                                      iN64, lo > 0 || kk > 0);
                 umma_commit(&sm.gfull);
             }
@@ -147,20 +152,19 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
             if (!(ok = wait(sm.uready, i))) break;
             tc_fence_after_sync();
             if (elect_one()) {
-                const uint32_t th = smem_u32(sm.p[s].t_hi), tl = smem_u32(sm.p[s].t_lo);
 #pragma unroll
                 for (int x = 0; x < 3; ++x)   // dU hi Tm hi, dU lo Tm hi, dU hi Tm lo
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         umma_bf16_ta(tm + cY, tm + cX + split_col(kk, x == 1),
-                                     umma_desc_mn((x == 2 ? tl : th) + 2048 * kk, kTile64), iN64 | kUmmaBmn, x > 0 || kk > 0);
+                                     desc_at(dt, (x == 2 ? kTile64 : 0) + 2048 * kk), iN64 | kUmmaBmn, x > 0 || kk > 0);
                 umma_commit(&sm.yfull);
                 // in the shadow of the pass over dY
 #pragma unroll
                 for (int lo = 0; lo < 2; ++lo)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        umma_bf16_ta(tm, tm + cD + split_col(kk, lo), umma_desc_mn(smem_u32(sm.q[s][0]) + 2048 * kk, kTile64),
+                        umma_bf16_ta(tm, tm + cD + split_col(kk, lo), desc_at(dqt, 2048 * kk),
                                      iS, 1);
             }
             __syncwarp();
@@ -171,7 +175,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                 for (int lo = 0; lo < 2; ++lo)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        umma_bf16_ta(tm, tm + cY + split_col(kk, lo), umma_desc_mn(smem_u32(sm.k[s][0]) + 2048 * kk, kTile64),
+                        umma_bf16_ta(tm, tm + cY + split_col(kk, lo), desc_at(dkt, 2048 * kk),
                                      iS, 1);
                 umma_commit(&sm.sfull);
                 umma_commit(&sm.free[s]);
@@ -310,22 +314,31 @@ struct GradSmem {
     __nv_bfloat16 S0[V * K], S1[V * K];        // S0, dS1
     __nv_bfloat16 qk[2][K / 64][128 * 64];     // [stage]: Q, K, then dq, dk on their way out
     __nv_bfloat16 P[192 * 64];                 // zeros, P1, P2
-    float vec[2][4][kC];                       // [stage]: e^G, e^{G_C - G}, w, G
+    float vec[2][5][kC];                       // [stage]: e^G, e^{G_C - G}, w, G, e^{G_r - G}
     float dg[4][128], dw[kC], kb[4][kC], tot[3][128], col[4][kC], last[8];   // partial sums of a head
     uint64_t vfull[2], vfree[2], qkfull[2], qkfree[2], dfull, dfree, s0full, s0free, s1full, s1free, Dfull, Dfree, xfull,
         xfree, yfull, yfree, pready, pfull, afree, gready, gfree, oready, drain;
     uint32_t tmem;
 };
 
-// sum of the products of eight bf16 pairs
-__device__ __forceinline__ float dot8(uint4 a, uint4 b, float acc) {
-    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+// <rows v0 .. v0 + 15 of S0, the same of S1> of [V][K] tiles in operand layout, by this warp: the diagonal of
+// S0 S1^T from m16n8k16 products (the sum of 64 products a lane took four times as many instructions)
+template <int K, int V>
+__device__ __forceinline__ float inner16(const __nv_bfloat16 *S0, const __nv_bfloat16 *S1, int v0, int lane) {
+    float d[2][4] = {};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        acc = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), acc);
-        acc = fmaf(__uint_as_float(x[i] & 0xffff0000u), __uint_as_float(y[i] & 0xffff0000u), acc);
+    for (int k = 0; k < K; k += 16) {
+        uint32_t a[4], b[4];
+        load_a_um(a, S0, V, v0, k, lane);
+        ldsm_x4(b, smem_u32(S1 + umma_off(v0 + (lane & 7) + ((lane >> 4) << 3), k + ((lane >> 3) & 1) * 8, V)));
+        mma_bf16(d[0], a, b[0], b[1]);
+        mma_bf16(d[1], a, b[2], b[3]);
     }
-    return acc;
+    const int g = lane / 4;   // this thread's rows g, g + 8 meet their columns in lane 4 g + g / 2
+    float x = lane % 4 == g / 2 ? (g & 1 ? d[0][1] + d[1][3] : d[0][0] + d[1][2]) : 0.f;
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    return x;
 }
 
 // lane l returns the sum over the warp's lanes of their x[l % 16]
@@ -391,7 +404,11 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
         mbar_init(&sm.yfree, kRegWarps / 2);
         fence_mbar_init();
     }
-    for (int i = threadIdx.x; i < kC * 8; i += blockDim.x) reinterpret_cast<uint4 *>(sm.P)[i] = make_uint4(0u, 0u, 0u, 0u);
+    // the zero block, and what stays zero: blocks of 16 above the diagonal
+    for (int i = threadIdx.x; i < (int)sizeof(sm.P) / 16; i += blockDim.x) reinterpret_cast<uint4 *>(sm.P)[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = threadIdx.x; i < 4 * kC; i += blockDim.x) sm.col[i / kC][i % kC] = 0.f;
+    for (int i = threadIdx.x; i < 3 * 128; i += blockDim.x) sm.tot[i / 128][i % 128] = 0.f;
+    for (int i = threadIdx.x; i < 8; i += blockDim.x) sm.last[i] = 0.f;
     fence_proxy_async_smem();
     if (warp == kRegWarps + 1) tmem_alloc(&sm.tmem, 512);
     tc_fence_before_sync();
@@ -408,20 +425,22 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
 
     if (warp >= kRegWarps) regs_down<64>();
     if (warp == kRegWarps) {
+#pragma unroll 1
         for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
             const int tile = w / a.Hk, hk = w - tile * a.Hk;
             int n, c, len;
             long long row;
             if (!a.seq.find(tile, kC, n, c, row, len)) continue;
             row += (long long)c * kC;
+#pragma unroll 1
             for (int g = 0; g < share && ok; ++g, ++j) {
                 const int s = j & 1, h = hk * share + g;
                 const size_t slot = (size_t)tile * a.Hv + h;
                 const Keep *fwd = reinterpret_cast<const Keep *>(a.saved) + slot, *bwd = reinterpret_cast<const Keep *>(a.ws) + slot;
                 if (j >= 2 && !(ok = wait(sm.vfree[s], j / 2 - 1))) break;
                 if (elect_one()) {
-                    mbar_expect_tx(&sm.vfull[s], sizeof(sm.vec[0]));
-                    bulk_g2s(sm.vec[s], reinterpret_cast<const GdrPrep *>(a.prep)[slot].eG, sizeof(sm.vec[0]), &sm.vfull[s]);
+                    mbar_expect_tx(&sm.vfull[s], kVecBytes);
+                    bulk_g2s(sm.vec[s], reinterpret_cast<const GdrPrep *>(a.prep)[slot].eG, kVecBytes, &sm.vfull[s]);
                 }
                 __syncwarp();
                 if (g == 0) {
@@ -471,13 +490,17 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
         }
     } else if (warp == kRegWarps + 1) {
         constexpr uint32_t iN64 = umma_idesc_bf16(128, 64), iK = umma_idesc_bf16(128, K) | kUmmaBmn;
-        const uint32_t P = smem_u32(sm.P), d = smem_u32(sm.d[0]);
+        const uint32_t P = smem_u32(sm.P);
+        const uint64_t dd = umma_desc(smem_u32(sm.d)), dS0 = umma_desc_mn(smem_u32(sm.S0), V * 128), dS1 = umma_desc_mn(smem_u32(sm.S1), V * 128);
+        const uint64_t dP = umma_desc(P + kTile64), dP1 = umma_desc_mn(P, kTile64), dP2 = umma_desc_mn(P, 2 * kTile64);
+#pragma unroll 1
         for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
             const int tile = w / a.Hk;
             int n, c, len;
             long long row;
             if (!a.seq.find(tile, kC, n, c, row, len)) continue;
-            const uint32_t qk = smem_u32(sm.qk[it & 1][0]);
+            const uint64_t dqk = umma_desc(smem_u32(sm.qk[it & 1])), dqkt = umma_desc_mn(smem_u32(sm.qk[it & 1]), 2 * kTile64);
+#pragma unroll 1
             for (int g = 0; g < share && ok; ++g, ++j) {
                 if (g == 0) {
                     if (!(ok = wait(sm.qkfull[it & 1], it / 2))) break;
@@ -493,8 +516,8 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                 if (g == 0 && elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < K / 16; ++kk) {
-                        const uint32_t x = qk + 2 * kTile64 * (kk / 4) + 32 * (kk % 4);
-                        umma_bf16(tm + cKK, umma_desc(x), umma_desc(x + kTile64), iN64, kk > 0);
+                        const uint32_t x = 2 * kTile64 * (kk / 4) + 32 * (kk % 4);
+                        umma_bf16(tm + cKK, desc_at(dqk, x), desc_at(dqk, x + kTile64), iN64, kk > 0);
                     }
                 }
                 __syncwarp();
@@ -502,8 +525,8 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < V / 16; ++kk) {
-                        const uint32_t x = d + 3 * kTile64 * (kk / 4) + 32 * (kk % 4);
-                        umma_bf16(tm + cD, umma_desc(x), umma_desc(x + 2 * kTile64), iN64, kk > 0);
+                        const uint32_t x = 3 * kTile64 * (kk / 4) + 32 * (kk % 4);
+                        umma_bf16(tm + cD, desc_at(dd, x), desc_at(dd, x + 2 * kTile64), iN64, kk > 0);
                     }
                     umma_commit(&sm.Dfull);
                 }
@@ -514,8 +537,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < V / 16; ++kk)
-                        umma_bf16(tm + cX, umma_desc(d + 3 * kTile64 * (kk / 4) + 32 * (kk % 4)),
-                                  umma_desc_mn(smem_u32(sm.S0) + 2048 * kk, V * 128), iK, kk > 0);
+                        umma_bf16(tm + cX, desc_at(dd, 3 * kTile64 * (kk / 4) + 32 * (kk % 4)), desc_at(dS0, 2048 * kk), iK, kk > 0);
                     umma_commit(&sm.xfull);
                     umma_commit(&sm.s0free);
                 }
@@ -526,8 +548,8 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < V / 16; ++kk)   // [dY; U] dS1, of which the lanes of U count
-                        umma_bf16(tm + cY, umma_desc(d + kTile64 + 3 * kTile64 * (kk / 4) + 32 * (kk % 4)),
-                                  umma_desc_mn(smem_u32(sm.S1) + 2048 * kk, V * 128), iK, kk > 0);
+                        umma_bf16(tm + cY, desc_at(dd, kTile64 + 3 * kTile64 * (kk / 4) + 32 * (kk % 4)), desc_at(dS1, 2048 * kk), iK,
+                                  kk > 0);
                     umma_commit(&sm.yfull);
                 umma_commit(&sm.s1free);
                     umma_commit(&sm.dfree);
@@ -539,16 +561,13 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)   // [P1; P2] K
-                        umma_bf16(tm + cA, umma_desc(P + kTile64 + 32 * kk), umma_desc_mn(qk + kTile64 + 2048 * kk, 2 * kTile64), iK,
-                                  g > 0 || kk > 0);
+                        umma_bf16(tm + cA, desc_at(dP, 32 * kk), desc_at(dqkt, kTile64 + 2048 * kk), iK, g > 0 || kk > 0);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)   // [0; P1^T] Q
-                        umma_bf16(tm + cA, umma_desc_mn(P + 2048 * kk, kTile64), umma_desc_mn(qk + 2048 * kk, 2 * kTile64),
-                                  iK | kUmmaAmn, 1);
+                        umma_bf16(tm + cA, desc_at(dP1, 2048 * kk), desc_at(dqkt, 2048 * kk), iK | kUmmaAmn, 1);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)   // [0; P2^T] K
-                        umma_bf16(tm + cA, umma_desc_mn(P + 2048 * kk, 2 * kTile64),
-                                  umma_desc_mn(qk + kTile64 + 2048 * kk, 2 * kTile64), iK | kUmmaAmn, 1);
+                        umma_bf16(tm + cA, desc_at(dP2, 2048 * kk), desc_at(dqkt, kTile64 + 2048 * kk), iK | kUmmaAmn, 1);
                     umma_commit(&sm.pfull);
                 }
                 __syncwarp();
@@ -564,6 +583,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
         // columns of a cumulative sum would cancel): queries and keys r >= t that read the start state,
         // keys s < t that reach the end, S0 itself, and pairs r >= t > s.
         float *part = a.dA_dec || a.dtau ? reinterpret_cast<float *>(a.ws + (size_t)a.seq.n_tiles(kC) * a.Hv * sizeof(Keep)) : nullptr;
+#pragma unroll 1
         for (int wk = blockIdx.x; wk < items && ok; wk += gridDim.x) {
             const int tile = wk / a.Hk, hk = wk - tile * a.Hk;
             int n, c, len;
@@ -575,17 +595,10 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
             }
             row += (long long)c * kC;
             const int m = min(kC, len - c * kC);
+#pragma unroll 1
             for (int g = 0; g < share && ok; ++g, ++j) {
                 const int h = hk * share + g;
                 const float amp = decay_amp(a.A_dec, h), bias = a.tau ? a.tau[h] : 0.f;
-                float x[2], w[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int t = lane + 32 * e;
-                    const size_t at = (size_t)(row + (t < m ? t : 0)) * a.Hv + h;
-                    x[e] = ld_io(static_cast<const __nv_bfloat16 *>(a.g_logit) + at) + bias;
-                    w[e] = sigmoid_f(ld_io(static_cast<const __nv_bfloat16 *>(a.w_logit) + at));
-                }
                 if (!(ok = wait(sm.gready, j))) break;
                 // row sums; sums of key rows; dY.U = w dL/dw (from (I + M) U = w R: dL/dw = dY.(R - M U / w) = dY.U / w);
                 // columns of the pairs; row totals of the pairs of tokens 0-15, 16-31, 32-47
@@ -609,7 +622,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.gfree);
                 // suffix sums of G and the T, exclusive prefix of B
-#pragma unroll
+#pragma unroll 1
                 for (int off = 1; off < 32; off <<= 1) {
                     const bool down = lane + off < 32;
 #pragma unroll
@@ -629,21 +642,21 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                 float b0 = __shfl_up_sync(0xffffffffu, B[0], 1), b1 = __shfl_up_sync(0xffffffffu, B[1], 1);
                 b0 = lane ? b0 : 0.f;
                 b1 = (lane ? b1 : 0.f) + all0;
-                const float gr[2] = {G[0] + b0 + last + C[0] + (lane >= 16 ? T[0][0] + t0 : 0.f),
-                                     G[1] + b1 + last + C[1] + T[0][1] + T[1][1] + (lane >= 16 ? T[2][1] : 0.f)};
+                const float gr0 = G[0] + b0 + last + C[0] + (lane >= 16 ? T[0][0] + t0 : 0.f);
+                const float gr1 = G[1] + b1 + last + C[1] + T[0][1] + T[1][1] + (lane >= 16 ? T[2][1] : 0.f);
                 float dlog = 0.f, damp = 0.f;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int t = lane + 32 * e;
-                    if (t < m) {
-                        const size_t at = (size_t)(row + t) * a.Hv + h;
-                        const float dl = -amp * sigmoid_f(x[e]) * gr[e];
-                        dlog += dl;
-                        damp += -amp * softplus_f(x[e]) * gr[e];
-                        st_io(static_cast<__nv_bfloat16 *>(a.dg_logit) + at, dl);
-                        st_io(static_cast<__nv_bfloat16 *>(a.dw_logit) + at, dw[e] * (1.f - w[e]));
-                    }
+#pragma unroll 1
+                for (int t = lane; t < m; t += 32) {
+                    const size_t at = (size_t)(row + t) * a.Hv + h;
+                    const float x = ld_io(static_cast<const __nv_bfloat16 *>(a.g_logit) + at) + bias;
+                    const float w = sigmoid_f(ld_io(static_cast<const __nv_bfloat16 *>(a.w_logit) + at));
+                    const float gr = -amp * (t < 32 ? gr0 : gr1), dl = sigmoid_f(x) * gr;
+                    dlog += dl;
+                    damp += softplus_f(x) * gr;
+                    st_io(static_cast<__nv_bfloat16 *>(a.dg_logit) + at, dl);
+                    st_io(static_cast<__nv_bfloat16 *>(a.dw_logit) + at, (t < 32 ? dw[0] : dw[1]) * (1.f - w));
                 }
+                __syncwarp();
                 if (part) {
 #pragma unroll
                     for (int off = 16; off >= 1; off >>= 1) {
@@ -658,6 +671,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
             }
         }
     } else if (warp == kRegWarps + 3) {
+#pragma unroll 1
         for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
             const int tile = w / a.Hk, hk = w - tile * a.Hk;
             int n, c, len;
@@ -685,7 +699,10 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
         const bool key = r >= kC;   // lane of a key (the same for a whole warp)
         const uint32_t tl = tm + ((uint32_t)quarter << 21);
         const int x0 = part * KQ, s0 = part * 16;
+        // this warp's 32 tokens x 16 pairs: above the diagonal, across it, below it
+        const int pairs = s0 > (t | 31) ? 0 : s0 + 15 < (t & 32) ? 2 : 1;
         float acc[KQ];
+#pragma unroll 1
         for (int wk = blockIdx.x; wk < items && ok; wk += gridDim.x) {
             const int tile = wk / a.Hk, hk = wk - tile * a.Hk;
             int n, c, len;
@@ -698,6 +715,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
             __nv_bfloat16 *qk = sm.qk[it & 1][0];
 #pragma unroll
             for (int x = 0; x < KQ; ++x) acc[x] = 0.f;
+#pragma unroll 1
             for (int g = 0; g < share && ok; ++g, ++j) {
                 const int s = j & 1;
                 if (!(ok = wait(sm.vfull[s], j / 2))) break;
@@ -706,8 +724,8 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                 // pairs of the chunk: y = D (dO U^T) or -w D (dY U^T), times k.k or q.k
                 if (!(ok = wait(sm.Dfull, j))) break;
                 tc_fence_after_sync();
-                {
-                    uint32_t D[16], kk[16], p[8];
+                if (pairs) {
+                    uint32_t D[16], kk[16];
                     tmem_ld16(tl + cD + s0, D);
                     tmem_ld16(tl + cKK + s0, kk);
                     tmem_wait_ld();
@@ -715,29 +733,44 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                     tmem_tie16(kk);
                     tc_fence_before_sync();
                     mbar_arrive_warp(&sm.Dfree);
-                    float pr[16], own = 0.f;
+                    float pr[16], own = 0.f, run = 0.f;
+                    if (pairs == 2) {   // all of them below the diagonal: one factor a row, one a column
+                        const float f = here ? sign * ex2(Gt - G[15]) : 0.f;
+                        const float *eB = sm.vec[s][4] + s0;
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float x = __uint_as_float(D[e]);
-                        own = t - s0 == e ? x : own;
-                        const float y = e < lim ? sign * ex2(Gt - G[e]) * x : 0.f;
-                        pr[e] = y * __uint_as_float(kk[e]);
-                        D[e] = __float_as_uint(y);
+                        for (int e = 0; e < 16; e += 4) {
+                            const float4 b = *reinterpret_cast<const float4 *>(eB + e);
+                            const float c[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float y = here ? f * c[i] * __uint_as_float(D[e + i]) : 0.f;
+                                pr[e + i] = y * __uint_as_float(kk[e + i]);
+                                D[e + i] = __float_as_uint(y);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float x = __uint_as_float(D[e]);
+                            own = t - s0 == e ? x : own;
+                            const float y = e < lim ? sign * ex2(Gt - G[e]) * x : 0.f;
+                            pr[e] = y * __uint_as_float(kk[e]);
+                            D[e] = __float_as_uint(y);
+                        }
                     }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) p[e] = pack_bf16(__uint_as_float(D[2 * e]), __uint_as_float(D[2 * e + 1]));
+                    for (int e = 0; e < 8; ++e) kk[e] = pack_bf16(__uint_as_float(D[2 * e]), __uint_as_float(D[2 * e + 1]));
                     if (j > 0 && !(ok = wait(sm.pfull, j - 1))) break;
 #pragma unroll
                     for (int e = 0; e < 8; e += 4)
-                        *reinterpret_cast<uint4 *>(sm.P + kC * 64 + op_off(r, s0 + 2 * e, 128)) = make_uint4(p[e], p[e + 1], p[e + 2], p[e + 3]);
+                        *reinterpret_cast<uint4 *>(sm.P + kC * 64 + op_off(r, s0 + 2 * e, 128)) = make_uint4(kk[e], kk[e + 1], kk[e + 2], kk[e + 3]);
                     fence_proxy_async_smem();
                     mbar_arrive_warp(&sm.pready);
                     // sums over s before u, for u up to t (what a query's own pair adds is behind its last u)
-                    float run = 0.f;
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const float y = pr[e];
-                        pr[e] = s0 + e <= t ? run : 0.f;
+                        pr[e] = pairs == 2 || s0 + e <= t ? run : 0.f;
                         run += y;
                     }
                     const float cs = column_sum(pr, lane);
@@ -745,6 +778,10 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                     if (lane < 16) sm.col[quarter][s0 + lane] = cs;
                     if (part < 3) sm.tot[part][r] = run;
                     if (key && t / 16 == part) sm.dw[t] = own;
+                } else {
+                    mbar_arrive_warp(&sm.Dfree);
+                    mbar_arrive_warp(&sm.pready);
+                    if (j > 0 && !(ok = wait(sm.gfree, j - 1))) break;
                 }
                 if (key) {   // end state
                     if (!(ok = wait(sm.yfull, j))) break;
@@ -758,16 +795,12 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                 } else {   // <S0, dS1>: both are laid out alike
                     if (!(ok = wait(sm.s0full, j))) break;
                     if (!(ok = wait(sm.s1full, j))) break;
+                    const int v0 = (part * 2 + quarter) * 16;
                     float y = 0.f;
-#pragma unroll
-                    for (int i = 0; i < V * K / 8; i += 256)
-                        y = dot8(reinterpret_cast<const uint4 *>(sm.S0)[i + part * 64 + quarter * 32 + lane],
-                                 reinterpret_cast<const uint4 *>(sm.S1)[i + part * 64 + quarter * 32 + lane], y);
+                    if (v0 < V) y = inner16<K, V>(sm.S0, sm.S1, v0, lane);
                     mbar_arrive_warp(&sm.s0free);
                     mbar_arrive_warp(&sm.s1free);
-#pragma unroll
-                    for (int off = 16; off >= 1; off >>= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
-                    if (lane == 0) sm.last[part * 2 + quarter] = y * eG[kC - 1];
+                    if (lane == 0 && v0 < V) sm.last[part * 2 + quarter] = y * eG[kC - 1];
                 }
                 // start state
                 if (!(ok = wait(sm.xfull, j))) break;

@@ -59,7 +59,7 @@ struct PrepSmem {
         };
     };
     __nv_bfloat16 A[kC * 64];
-    float eG[kC], eK[kC], w[kC], G[kC];
+    float eG[kC], eK[kC], w[kC], G[kC], eB[kC];
     uint64_t full, done;
     uint32_t tmem;
 };
@@ -218,6 +218,7 @@ __global__ void __launch_bounds__(128) gdr_tc_prep(GdrArgs a, const __grid_const
         if (tid < kC) {
             sm.eG[tid] = exp2f(sm.G[tid]);
             sm.eK[tid] = exp2f(sm.G[kC - 1] - sm.G[tid]);
+            sm.eB[tid] = exp2f(sm.G[tid | 15] - sm.G[tid]);
         }
         const float Gt = sm.G[t], wt = sm.w[t];
         if (tid < kC) {
@@ -262,7 +263,7 @@ __global__ void __launch_bounds__(128) gdr_tc_prep(GdrArgs a, const __grid_const
             GdrPrep *out = reinterpret_cast<GdrPrep *>(a.prep) + (size_t)tile * a.Hv + h;
             bulk_s2g(out->t_hi, sm.t, sizeof(sm.t));
             bulk_s2g(out->A, sm.A, sizeof(sm.A));
-            bulk_s2g(out->eG, sm.eG, 4 * sizeof(sm.eG));
+            bulk_s2g(out->eG, sm.eG, kVecBytes);
             bulk_commit();
         }
     }
@@ -339,8 +340,12 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
             for (int i = max(0, c - 2); i < c; ++i) wait(sm.full[i & 1], i / 2);
     } else if (warp == kRegWarps + 1) {
         constexpr uint32_t iN64 = umma_idesc_bf16(128, 64), iS = umma_idesc_bf16(128, K) | kUmmaBmn;
+        const uint64_t dk0 = umma_desc(smem_u32(sm.k)), dq0 = umma_desc(smem_u32(sm.q)), dt0 = umma_desc(smem_u32(sm.p)),
+                       ds0 = umma_desc_mn(smem_u32(sm.k), kTile64);
         for (int c = 0; c < chunks; ++c) {
             const int s = c & 1;
+            const uint64_t dk = desc_at(dk0, s * KH * kTile64), dq = desc_at(dq0, s * KH * kTile64),
+                           dt = desc_at(dt0, s * sizeof(GdrPrep)), ds = desc_at(ds0, s * KH * kTile64);
             if (!(ok = wait(sm.full[s], c / 2))) break;
             if (len - c * kC < kC) {   // key rows behind the end meet U = 0 in the state update
                 zero_rows(sm.k[s], len - c * kC, KH, kTile64, lane);
@@ -354,7 +359,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                 for (int lo = 0; lo < 2; ++lo)
 #pragma unroll
                     for (int kk = 0; kk < K / 16; ++kk)
-                        umma_bf16_ta(tm + cG, tm + (lo ? cLo : cHi) + 8 * kk, umma_desc(smem_u32(sm.k[s][kk / 4]) + 32 * (kk % 4)),
+                        umma_bf16_ta(tm + cG, tm + (lo ? cLo : cHi) + 8 * kk, desc_at(dk, kTile64 * (kk / 4) + 32 * (kk % 4)),
                                      iN64, lo > 0 || kk > 0);
                 umma_commit(&sm.gfull);
             }
@@ -362,12 +367,11 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
             if (!(ok = wait(sm.rready, c))) break;
             tc_fence_after_sync();
             if (elect_one()) {
-                const uint32_t th = smem_u32(sm.p[s].t_hi), tl = smem_u32(sm.p[s].t_lo);
 #pragma unroll
                 for (int x = 0; x < 3; ++x)   // R hi Tm hi, R lo Tm hi, R hi Tm lo
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        umma_bf16_ta(tm + cU, tm + cG + split_col(kk, x == 1), umma_desc((x == 2 ? tl : th) + 32 * kk), iN64,
+                        umma_bf16_ta(tm + cU, tm + cG + split_col(kk, x == 1), desc_at(dt, (x == 2 ? kTile64 : 0) + 32 * kk), iN64,
                                      x > 0 || kk > 0);
                 umma_commit(&sm.ufull);
             }
@@ -380,7 +384,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                 for (int lo = 0; lo < 2; ++lo)
 #pragma unroll
                     for (int kk = 0; kk < K / 16; ++kk)
-                        umma_bf16_ta(tm + cQ, tm + (lo ? cLo : cHi) + 8 * kk, umma_desc(smem_u32(sm.q[s][kk / 4]) + 32 * (kk % 4)),
+                        umma_bf16_ta(tm + cQ, tm + (lo ? cLo : cHi) + 8 * kk, desc_at(dq, kTile64 * (kk / 4) + 32 * (kk % 4)),
                                      iN64, lo > 0 || kk > 0);
             }
             __syncwarp();
@@ -391,14 +395,13 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                 for (int lo = 0; lo < 2; ++lo)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        umma_bf16_ta(tm, tm + cU + split_col(kk, lo), umma_desc_mn(smem_u32(sm.k[s][0]) + 2048 * kk, kTile64), iS, 1);
+                        umma_bf16_ta(tm, tm + cU + split_col(kk, lo), desc_at(ds, 2048 * kk), iS, 1);
                 umma_commit(&sm.sfull);
-                const uint32_t A = smem_u32(sm.p[s].A);
 #pragma unroll
                 for (int lo = 0; lo < 2; ++lo)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) 
-                        umma_bf16_ta(tm + cA, tm + cG + split_col(kk, lo), umma_desc(A + 32 * kk), iN64, lo > 0 || kk > 0);
+                        umma_bf16_ta(tm + cA, tm + cG + split_col(kk, lo), desc_at(dt, 2 * kTile64 + 32 * kk), iN64, lo > 0 || kk > 0);
                 umma_commit(&sm.ofull);
                 umma_commit(&sm.free[s]);
             }

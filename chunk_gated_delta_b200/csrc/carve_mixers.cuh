@@ -48,6 +48,7 @@ struct Seqs {
             c = tile - n * per;
         } else {
             int lo = 0, hi = N - 1;
+#pragma unroll 1
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
                 if (cu[mid] / C + mid <= tile)

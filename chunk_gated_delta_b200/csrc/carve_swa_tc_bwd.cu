@@ -180,6 +180,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         constexpr uint32_t iS = umma_idesc_bf16(BR, BC), iA = umma_idesc_bf16(BR, D) | kUmmaBmn;
         // S, dP of column tile number c (of all) with rows in buffer x: waits for the tile, zeroes its
         // rows behind the sequence's end (they meet P = dS = 0 in the sums)
+        const uint64_t dr = umma_desc(smem_u32(sm.r)), dc = umma_desc(smem_u32(sm.c)), dct = umma_desc_mn(smem_u32(sm.c), BC * 128);
         auto issue_s = [&](int c, int x, int there) {
             const int s = c % kStages;
             ok = wait(sm.cfull[s], c / kStages);
@@ -193,12 +194,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             }
             tc_fence_after_sync();
             if (elect_one()) {
+                const uint64_t rows = desc_at(dr, x * sizeof(sm.r[0])), cols = desc_at(dc, s * sizeof(sm.c[0]));
 #pragma unroll
                 for (int y = 0; y < 2; ++y)
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk)
-                        umma_bf16(tm + 128 * y + 64 * (c & 1), umma_desc(smem_u32(sm.r[x][y][kk / 4]) + 32 * (kk % 4)),
-                                  umma_desc(smem_u32(sm.c[s][y][kk / 4]) + 32 * (kk % 4)), iS, kk > 0);
+                        umma_bf16(tm + 128 * y + 64 * (c & 1), desc_at(rows, BR * 128 * (KH * y + kk / 4) + 32 * (kk % 4)),
+                                  desc_at(cols, BC * 128 * (KH * y + kk / 4) + 32 * (kk % 4)), iS, kk > 0);
                 umma_commit(&sm.sfull[c & 1]);
             }
             __syncwarp();
@@ -219,15 +221,16 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 tc_fence_after_sync();
                 if (elect_one()) {
                     const int s = nc % kStages;
+                    const uint64_t cols = desc_at(dct, s * sizeof(sm.c[0]));
 #pragma unroll
                     for (int kk = 0; kk < BC / 16; ++kk)
                         umma_bf16_ta(tm + 256, tm + 128 + 64 * (nc & 1) + 8 * kk,
-                                     umma_desc_mn(smem_u32(sm.c[s][0][0]) + 2048 * kk, BC * 128), iA, b > 0 || kk > 0);
+                                     desc_at(cols, 2048 * kk), iA, b > 0 || kk > 0);
                     if (KEYS) {
 #pragma unroll
                         for (int kk = 0; kk < BC / 16; ++kk)
                             umma_bf16_ta(tm + 384, tm + 64 * (nc & 1) + 8 * kk,
-                                         umma_desc_mn(smem_u32(sm.c[s][1][0]) + 2048 * kk, BC * 128), iA, b > 0 || kk > 0);
+                                         desc_at(cols, BC * 128 * KH + 2048 * kk), iA, b > 0 || kk > 0);
                     }
                     umma_commit(&sm.cfree[s]);
                     if (b == w.n - 1) {

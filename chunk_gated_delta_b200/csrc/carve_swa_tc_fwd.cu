@@ -131,11 +131,14 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     } else if (warp == 17) {
         constexpr uint32_t iS = umma_idesc_bf16(BM, BN), iO = umma_idesc_bf16(BM, D) | kUmmaBmn;
         int ns[2] = {0, 0}, np[2] = {0, 0};   // products S and P V issued, per tile
+        const uint64_t dq = umma_desc(smem_u32(sm.q)), dk = umma_desc(smem_u32(sm.kv)), dv = umma_desc_mn(smem_u32(sm.kv), BN * 128);
         auto issue_s = [&](int t, int slot) {
             if (elect_one()) {
+                const uint64_t q = desc_at(dq, t * sizeof(sm.q[0])), k = desc_at(dk, slot * sizeof(sm.kv[0]));
+#pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    umma_bf16(tm + 128 * t, umma_desc(smem_u32(sm.q[t][kk / 4]) + 32 * (kk % 4)),
-                              umma_desc(smem_u32(sm.kv[slot][kk / 4]) + 32 * (kk % 4)), iS, kk > 0);
+                    umma_bf16(tm + 128 * t, desc_at(q, BM * 128 * (kk / 4) + 32 * (kk % 4)), desc_at(k, BN * 128 * (kk / 4) + 32 * (kk % 4)),
+                              iS, kk > 0);
                 umma_commit(&sm.sfull[t]);
             }
             __syncwarp();
@@ -167,9 +170,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     if (!ok) break;
                     tc_fence_after_sync();
                     if (elect_one()) {
+                        const uint64_t v = desc_at(dv, vs * sizeof(sm.kv[0]));
+#pragma unroll
                         for (int kk = 0; kk < BN / 16; ++kk)
                             umma_bf16_ta(tm + 256 + 128 * t, tm + 128 * t + 8 * kk + (kk < 4 ? 0 : 32),
-                                         umma_desc_mn(smem_u32(sm.kv[vs][0]) + 2048 * kk, BN * 128), iO, kk > 0 || np[t] > 0);
+                                         desc_at(v, 2048 * kk), iO, kk > 0 || np[t] > 0);
                         umma_commit(&sm.ofull[t]);
                     }
                     __syncwarp();

@@ -45,6 +45,10 @@ __device__ __forceinline__ uint64_t umma_desc_mn(uint32_t saddr, uint32_t next64
     return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)((next64 & 0x3FFFFu) >> 4) << 16) |
            ((uint64_t)(1024u >> 4) << 32) | ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
 }
+// the descriptor of a slice `bytes` further on (the start address stays below its 14 bits: one addition)
+__device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t bytes) {
+    return (desc & 0xffffffff00000000ull) | ((uint32_t)desc + (bytes >> 4));
+}
 constexpr uint32_t kUmmaBmn = 1u << 16;   // instruction descriptor: B is MN-contiguous
 
 // D (TMEM) = A B^T (+ D when `accumulate`), issued by one thread.
