@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
     constexpr uint32_t cHi = 128, cLo = 192, cX = 256, cP = 320, cY = 384, cD = 448;
     bool ok = true;
     auto wait = [&](uint64_t &bar, int phase) {   // by a whole warp
-        return (bool)__all_sync(0xffffffffu, mbar_wait_idle(&bar, phase & 1, kIdleWait));
+        return mbar_wait_warp(&bar, phase & 1, kIdleWait);
     };
 
     if (warp >= kRegWarps) regs_down<64>();
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
     constexpr uint32_t cX = 0, cY = 128, cA = 256, cD = 384, cKK = 448;
     bool ok = true;
     auto wait = [&](uint64_t &bar, int phase) {   // by a whole warp
-        return (bool)__all_sync(0xffffffffu, mbar_wait_idle(&bar, phase & 1, kIdleWait));
+        return mbar_wait_warp(&bar, phase & 1, kIdleWait);
     };
     const int items = (int)a.seq.n_tiles(kC) * a.Hk;   // below 2^28
     int it = 0, j = 0;   // items and heads so far (those of used tiles)

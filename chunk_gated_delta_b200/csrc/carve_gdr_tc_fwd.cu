@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
     constexpr uint32_t cHi = 128, cLo = 192, cG = 256, cU = 320, cQ = 384, cA = 448;
     bool ok = true;
     auto wait = [&](uint64_t &bar, int phase) {   // by a whole warp
-        return (bool)__all_sync(0xffffffffu, mbar_wait_idle(&bar, phase & 1, kIdleWait));
+        return mbar_wait_warp(&bar, phase & 1, kIdleWait);
     };
 
     if (warp >= kRegWarps) regs_down<64>();

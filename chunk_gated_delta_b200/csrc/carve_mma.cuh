@@ -168,19 +168,21 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint32
     return false;
 }
 
-// The same for kernels whose warps wait most of the time: a poll may suspend the warp for 20 us (a
-// hint), so that waiting warps leave the issue slots to the others.
-__device__ __forceinline__ bool mbar_wait_idle(uint64_t *bar, uint32_t parity, uint32_t limit) {
+// The same by a converged warp whose polls may suspend it for 20 us each (a hint): for kernels whose
+// warps wait most of the time.  Returns false in all lanes if the limit ran out.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, uint32_t limit) {
     const uint32_t a = smem_u32(bar);
-    for (uint32_t it = 0; it < limit; ++it) {
-        uint32_t done;
+    uint32_t done;
+#pragma unroll 1
+    do {
         asm volatile(
             "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
             : "=r"(done)
-            : "r"(a), "r"(parity), "r"(20000u));
-        if (done) return true;
-    }
-    return false;
+            : "r"(a), "r"(parity), "r"(20000u)
+            : "memory");
+        done = __all_sync(0xffffffffu, done);
+    } while (!done && --limit);
+    return done;
 }
 
 // 1-D bulk copy of `bytes` (multiple of 16, both addresses 16-byte aligned) into shared
