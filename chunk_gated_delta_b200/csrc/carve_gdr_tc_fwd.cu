@@ -64,72 +64,93 @@ struct PrepSmem {
     uint32_t tmem;
 };
 
-// X = (I + M)^-1 for a strictly lower-triangular M (64 x 64), X zero on entry; M is overwritten.
-// 16 x 16 diagonal blocks by substitution, then off-diagonal blocks by T21 = -T22 (M21 T11), first of
-// size 16, then of size 32.  128 threads.
+// acc (16 x 16, m16n8 fragments) = A B over KD terms of fp32 matrices in shared memory (row stride LM), by
+// one warp: each factor in two tf32 terms, three products, about 2^-21 relative
+template <int KD>
+__device__ __forceinline__ void mm16(float (&acc)[2][4], const float *A, const float *B, int lane) {
+    const int g = lane / 4, c = lane % 4;
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+    auto mma = [](float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+        asm volatile(
+            "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+    };
+    auto split = [](float x, uint32_t &hi, uint32_t &lo) {
+        hi = __float_as_uint(x) & 0xffffe000u;
+        lo = __float_as_uint(x - __uint_as_float(hi));
+    };
+#pragma unroll
+    for (int k = 0; k < KD; k += 8) {
+        uint32_t ah[4], al[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) split(A[(g + 8 * (i % 2)) * LM + k + c + 4 * (i / 2)], ah[i], al[i]);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            uint32_t bh[2], bl[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) split(B[(k + c + 4 * i) * LM + 8 * n + g], bh[i], bl[i]);
+            mma(acc[n], al, bh);
+            mma(acc[n], ah, bl);
+            mma(acc[n], ah, bh);
+        }
+    }
+}
+// C (16 x 16 at row stride LM) = f acc
+__device__ __forceinline__ void put16(float *C, const float (&acc)[2][4], float f, int lane) {
+    const int g = lane / 4, c = 2 * (lane % 4);
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<float2 *>(C + (g + 8 * i) * LM + 8 * n + c) = make_float2(f * acc[n][2 * i], f * acc[n][2 * i + 1]);
+}
+
+// The lower blocks of X = (I + M)^-1 for a strictly lower-triangular M (64 x 64; its blocks of 16 above the
+// diagonal are not read); M is overwritten.  16 x 16 diagonal blocks by substitution in fp32, then
+// off-diagonal blocks by T21 = -T22 (M21 T11), first of size 16 (a warp each), then of size 32.  128 threads.
 __device__ __forceinline__ void invert64(float (*M)[LM], float (*X)[LM]) {
-    const int tid = threadIdx.x;
-    if (tid < kC) {
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    if (tid < kC) {   // column c of a block
         const int o = tid / 16 * 16, c = tid % 16;
-        float acc[16];
+        float x[16];
 #pragma unroll
-        for (int t = 0; t < 16; ++t) acc[t] = 0.f;
+        for (int t = 0; t < 16; ++t) {
+            float y = t == c ? 1.f : 0.f;
 #pragma unroll
-        for (int s = 0; s < 16; ++s) {
-            const float x = (s == c ? 1.f : 0.f) - acc[s];
-            X[o + s][o + c] = x;
+            for (int s = 0; s < t; s += 4) {
+                const float4 m = *reinterpret_cast<const float4 *>(&M[o + t][o + s]);
+                const float mm[4] = {m.x, m.y, m.z, m.w};
 #pragma unroll
-            for (int t = s + 1; t < 16; ++t) acc[t] += M[o + t][o + s] * x;
+                for (int e = 0; e < 4; ++e)
+                    if (s + e < t) y = fmaf(-mm[e], x[s + e], y);
+            }
+            x[t] = y;
+            X[o + t][o + c] = y;
         }
     }
     __syncthreads();
-    {
-        const int o = tid / 64 * 32, i = tid % 64 / 4, j = tid % 4 * 4;
-        float y[4] = {};
-#pragma unroll
-        for (int s = 0; s < 16; ++s) {
-            const float m = M[o + 16 + i][o + s];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] += m * X[o + s][o + j + e];
-        }
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < 4; ++e) M[o + 16 + i][o + j + e] = y[e];
-        __syncthreads();
-        float z[4] = {};
-#pragma unroll
-        for (int s = 0; s < 16; ++s) {
-            const float x = X[o + 16 + i][o + 16 + s];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) z[e] -= x * M[o + 16 + s][o + j + e];
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) X[o + 16 + i][o + j + e] = z[e];
+    float acc[2][4];
+    if (warp < 2) {
+        const int o = 32 * warp;
+        mm16<16>(acc, &M[o + 16][o], &X[o][o], lane);
+        __syncwarp();
+        put16(&M[o + 16][o], acc, 1.f, lane);
+        __syncwarp();
+        mm16<16>(acc, &X[o + 16][o + 16], &M[o + 16][o], lane);
+        put16(&X[o + 16][o], acc, -1.f, lane);
     }
     __syncthreads();
-    {
-        const int i = tid / 4, j = tid % 4 * 8;
-        float y[8] = {};
-#pragma unroll 8
-        for (int s = 0; s < 32; ++s) {
-            const float m = M[32 + i][s];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] += m * X[s][j + e];
-        }
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < 8; ++e) M[32 + i][j + e] = y[e];
-        __syncthreads();
-        float z[8] = {};
-#pragma unroll 8
-        for (int s = 0; s < 32; ++s) {
-            const float x = X[32 + i][32 + s];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) z[e] -= x * M[32 + s][j + e];
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) X[32 + i][j + e] = z[e];
-    }
+    const int r = warp / 2 * 16, c = warp % 2 * 16;
+    mm16<32>(acc, &M[32 + r][0], &X[0][c], lane);
+    __syncthreads();
+    put16(&M[32 + r][c], acc, 1.f, lane);
+    __syncthreads();
+    mm16<32>(acc, &X[32 + r][32], &M[32][c], lane);
+    put16(&X[32 + r][c], acc, -1.f, lane);
     __syncthreads();
 }
 
@@ -185,14 +206,13 @@ __global__ void __launch_bounds__(128) gdr_tc_prep(GdrArgs a, const __grid_const
         return;
     }
     tc_fence_after_sync();
-    // row tid of [Q; K] K^T: q_t.k_s for tid = t < 64, k_t.k_s for tid = 64 + t
-    uint32_t g[64];
-    tmem_ld32(tm + ((uint32_t)warp << 21), g);
-    tmem_ld32(tm + ((uint32_t)warp << 21) + 32, g + 32);
-    tmem_wait_ld();
-    tmem_tie(g);
-    tmem_tie(g + 32);
+    // row tid of [Q; K] K^T: q_t.k_s for tid = t < 64, k_t.k_s for tid = 64 + t; A in the lower half of
+    // sm.A, M (w D k.k below the diagonal) in sm.M; blocks of 16 above the diagonal stay zero
     const int t = tid % kC;
+    const bool key = tid >= kC, here = t < m;
+    for (int i = tid; i < kC * 8; i += 128) reinterpret_cast<uint4 *>(sm.A)[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = tid; i < kC * LM / 4; i += 128) reinterpret_cast<float4 *>(sm.X)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
     for (int h = hk * share; h < (hk + 1) * share; ++h) {
         if (tid == 0) bulk_wait_read<0>();   // the last head's copies out have left the buffers
         __syncthreads();
@@ -220,28 +240,32 @@ __global__ void __launch_bounds__(128) gdr_tc_prep(GdrArgs a, const __grid_const
             sm.eK[tid] = exp2f(sm.G[kC - 1] - sm.G[tid]);
             sm.eB[tid] = exp2f(sm.G[tid | 15] - sm.G[tid]);
         }
-        const float Gt = sm.G[t], wt = sm.w[t];
-        if (tid < kC) {
+        __syncthreads();
+        const float Gt = sm.G[t], f0 = key ? sm.w[t] : 1.f;
+#pragma unroll 1
+        for (int s0 = 0; s0 <= (t | 31); s0 += 16) {
+            uint32_t g[16];
+            tmem_ld16(tm + ((uint32_t)warp << 21) + s0, g);
+            tmem_wait_ld();
+            tmem_tie16(g);
+            float y[16];
+            if (s0 + 15 < (t & 32)) {   // all below the diagonal: one factor a row, one a column
+                const float f = f0 * ex2(Gt - sm.G[s0 + 15]);
 #pragma unroll
-            for (int s = 0; s < kC; s += 8) {
-                uint32_t p[4];
+                for (int e = 0; e < 16; ++e) y[e] = here ? f * sm.eB[s0 + e] * __uint_as_float(g[e]) : 0.f;
+            } else {
+                const int lim = here ? t + !key - s0 : 0;   // s < t, and s = t for queries
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    const float x0 = s + e <= t && t < m ? ex2(Gt - sm.G[s + e]) * __uint_as_float(g[s + e]) : 0.f;
-                    const float x1 = s + e + 1 <= t && t < m ? ex2(Gt - sm.G[s + e + 1]) * __uint_as_float(g[s + e + 1]) : 0.f;
-                    p[e / 2] = pack_bf16(x0, x1);
-                }
-                *reinterpret_cast<uint4 *>(sm.A + op_off(t, s, kC)) = make_uint4(p[0], p[1], p[2], p[3]);
-                *reinterpret_cast<float4 *>(&sm.X[t][s]) = *reinterpret_cast<float4 *>(&sm.X[t][s + 4]) = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int e = 0; e < 16; ++e) y[e] = e < lim ? f0 * ex2(Gt - sm.G[s0 + e]) * __uint_as_float(g[e]) : 0.f;
             }
-        } else {
+            if (!key) {
 #pragma unroll
-            for (int s = 0; s < kC; s += 4) {
-                float x[4];
+                for (int e = 0; e < 16; e += 8)
+                    *reinterpret_cast<uint4 *>(sm.A + op_off(t, s0 + e, kC)) =
+                        make_uint4(pack_bf16(y[e], y[e + 1]), pack_bf16(y[e + 2], y[e + 3]), pack_bf16(y[e + 4], y[e + 5]), pack_bf16(y[e + 6], y[e + 7]));
+            } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    x[e] = s + e < t && t < m ? wt * ex2(Gt - sm.G[s + e]) * __uint_as_float(g[s + e]) : 0.f;
-                *reinterpret_cast<float4 *>(&sm.M[t][s]) = make_float4(x[0], x[1], x[2], x[3]);
+                for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4 *>(&sm.M[t][s0 + e]) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
             }
         }
         __syncthreads();
