@@ -12,12 +12,13 @@
 //   KEYS      k    v    q    dO     over the query heads of the key head
 //   else      q    dO   k    v
 //   S = R1 C1^T, dP = R2 C2^T   accumulators in tensor memory, two buffers
-//   P, dS                       thread = row, 64 columns; back to tensor memory as bf16 over S, dP
+//   P, dS                       two threads a row, 32 columns each; back to tensor memory as bf16 over S, dP
 //   acc1 += dS C1 (dk or dq),  acc2 += P C2 (dv)   A from tensor memory, C's rows contracted
-// Roles: warps 0-3 and 4-7 form P, dS of the even and odd column tiles, warp 8 copies, warp 9 issues
+// Roles: warps 0-7 and 8-15 form P, dS of the even and odd column tiles, warp 16 copies, warp 17 issues
 // the products: S, dP of the tile after next go out while the other buffer is being worked on.
-// Persistent: a CTA walks its units with one set of running phases; R is double-buffered, so the next
-// unit's copies and first products overlap the last one's epilogue.
+// Persistent: a CTA walks its units with one set of running phases; R is given back with the unit's last
+// S and dP, so the next unit's rows load beside this one's last sums and epilogue.  Four column stages:
+// three tiles are held by what is being computed.
 #include "carve_mixers.cuh"
 #include "carve_umma.cuh"
 
@@ -37,19 +38,19 @@ int swa_bwd_take_timeout() {
 
 namespace {
 
-constexpr int BR = 128, BC = 64, kStages = 3, kThreadsTc = 320;
+constexpr int BR = 128, BC = 64, kStages = 4, kWorkers = 16, kThreadsTc = (kWorkers + 2) * 32;
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>
 struct BwdSmem {
-    __nv_bfloat16 r[2][2][D / 64][BR * 64];        // [buffer][R1, R2]
+    __nv_bfloat16 r[2][D / 64][BR * 64];           // R1, R2
     __nv_bfloat16 c[kStages][2][D / 64][BC * 64];  // [stage][C1, C2]
-    float2 ld[kStages][BC];                        // (lse log2 e, delta) of the columns (KEYS)
-    uint64_t rfull[2], rfree[2], cfull[kStages], cfree[kStages], sfull[2], dfull[2], accfull, accfree;
+    float2 ld[kStages][BC + 2];                    // (-lse log2 e, -delta) of the columns (KEYS), from an even index on
+    uint64_t rfull, rfree, cfull[kStages], cfree[kStages], sfull[2], dfull[2], accfull, accfree;
     uint32_t tmem;
 };
 
-// (lse log2 e, delta) of every row and query head, [Hq][rows]: 16 lanes a (row, head), 16 bytes each
+// (-lse log2 e, -delta) of every row and query head, [Hq][rows]: 16 lanes a (row, head), 16 bytes each
 template <int D>
 __global__ void __launch_bounds__(256) swa_rows(SwaArgs a, long long rows) {
     constexpr int L = D / 8;
@@ -68,7 +69,7 @@ __global__ void __launch_bounds__(256) swa_rows(SwaArgs a, long long rows) {
 #pragma unroll
     for (int off = L / 2; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
     if (x == 0 && i < rows * a.Hq)
-        reinterpret_cast<float2 *>(a.delta)[(i % a.Hq) * rows + i / a.Hq] = make_float2(a.lse[i] * kLog2e, s);
+        reinterpret_cast<float2 *>(a.delta)[(i % a.Hq) * rows + i / a.Hq] = make_float2(-a.lse[i] * kLog2e, -s);
 }
 
 // A unit: 128 rows of one sequence and head, and its column tiles.
@@ -95,7 +96,7 @@ struct Unit {
         }
         return true;
     }
-    __device__ __forceinline__ int col0(int b) const { return (KEYS ? c0 + b % per : kt.tile(b)) * BC; }
+    __device__ __forceinline__ int col0(int b) const { return (KEYS ? c0 + b - b / per * per : kt.tile(b)) * BC; }
     __device__ __forceinline__ int col_head(const SwaArgs &a, int b) const {
         const int share = a.Hq / a.Hkv;
         return KEYS ? head * share + b / per : head / share;
@@ -113,109 +114,112 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.rfull[i], 1);
-            mbar_init(&sm.rfree[i], 1);
             mbar_init(&sm.sfull[i], 1);
-            mbar_init(&sm.dfull[i], 128);
+            mbar_init(&sm.dfull[i], kWorkers / 2);
         }
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&sm.cfull[i], KEYS ? 33 : 1);
+            mbar_init(&sm.cfull[i], 1);
             mbar_init(&sm.cfree[i], 1);
         }
+        mbar_init(&sm.rfull, 1);
+        mbar_init(&sm.rfree, 1);
         mbar_init(&sm.accfull, 1);
-        mbar_init(&sm.accfree, 256);
+        mbar_init(&sm.accfree, kWorkers);
         fence_mbar_init();
     }
-    if (warp == 9) tmem_alloc(&sm.tmem, 512);
+    if (warp == kWorkers + 1) tmem_alloc(&sm.tmem, 512);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tm = sm.tmem;   // S buffers at 0, 64; dP at 128, 192; acc1 at 256, acc2 at 384
     bool ok = true;
     auto wait = [&](uint64_t &bar, int phase) {   // by a whole warp
-        return (bool)__all_sync(0xffffffffu, mbar_wait(&bar, phase & 1, kSwaWait));
+        return mbar_wait_warp(&bar, phase & 1, kIdleWait);
     };
     Unit<KEYS> w;
+    // index of a column's entry in the table [Hq][rows]
+    auto col_index = [&](const Unit<KEYS> &u, int h, int c0) { return (long long)h * rows + u.row0 + c0; };
     int nu = 0, nc = 0;   // units and column tiles so far
 
-    if (warp == 8) {
+    if (warp == kWorkers) {
         for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
             if (!w.set(a, u)) continue;
-            const int x = nu & 1;
-            if (nu >= 2) ok = wait(sm.rfree[x], nu / 2 - 1);
-            if (!ok) break;
-            if (elect_one()) {
-                mbar_expect_tx(&sm.rfull[x], 2 * BR * D * 2);
-                for (int y = 0; y < KH; ++y) {
-                    tma_load_3d(sm.r[x][0][y], &mr1, 64 * y, w.head, (int)w.row0 + w.r0, &sm.rfull[x]);
-                    tma_load_3d(sm.r[x][1][y], &mr2, 64 * y, w.head, (int)w.row0 + w.r0, &sm.rfull[x]);
-                }
-            }
-            ++nu;
             for (int b = 0; b < w.n; ++b) {
+                if (b == 0) {
+                    if (nu > 0) ok = wait(sm.rfree, nu - 1);
+                    if (!ok) break;
+                    if (elect_one()) {
+                        mbar_expect_tx(&sm.rfull, 2 * BR * D * 2);
+                        for (int y = 0; y < KH; ++y) {
+                            tma_load_3d(sm.r[0][y], &mr1, 64 * y, w.head, (int)w.row0 + w.r0, &sm.rfull);
+                            tma_load_3d(sm.r[1][y], &mr2, 64 * y, w.head, (int)w.row0 + w.r0, &sm.rfull);
+                        }
+                    }
+                    ++nu;
+                }
                 const int s = nc % kStages, c0 = w.col0(b), h = w.col_head(a, b);
                 if (nc >= kStages) ok = wait(sm.cfree[s], nc / kStages - 1);
                 if (!ok) break;
                 if (elect_one()) {
-                    mbar_expect_tx(&sm.cfull[s], 2 * BC * D * 2);
+                    mbar_expect_tx(&sm.cfull[s], 2 * BC * D * 2 + (KEYS ? sizeof(sm.ld[0]) : 0));
                     for (int y = 0; y < KH; ++y) {
                         tma_load_3d(sm.c[s][0][y], &mc1, 64 * y, h, (int)w.row0 + c0, &sm.cfull[s]);
                         tma_load_3d(sm.c[s][1][y], &mc2, 64 * y, h, (int)w.row0 + c0, &sm.cfull[s]);
                     }
-                }
-                if (KEYS) {
-                    const float2 *src = reinterpret_cast<const float2 *>(a.delta) + (size_t)h * rows + w.row0;
-#pragma unroll
-                    for (int i = lane; i < BC; i += 32) sm.ld[s][i] = c0 + i < w.len ? src[c0 + i] : make_float2(0.f, 0.f);
-                    mbar_arrive(&sm.cfull[s]);
+                    // rows behind the sequence are masked; those behind the table lie in the workspace's tail
+                    if (KEYS) bulk_g2s(sm.ld[s], reinterpret_cast<const float2 *>(a.delta) + (col_index(w, h, c0) & ~1ll), sizeof(sm.ld[0]), &sm.cfull[s]);
                 }
                 ++nc;
             }
         }
         if (!ok) {   // the copies in flight land before the CTA leaves
-            for (int i = max(0, nu - 2); i < nu; ++i) wait(sm.rfull[i & 1], i / 2);
+            if (nu) wait(sm.rfull, nu - 1);
             for (int i = max(0, nc - kStages); i < nc; ++i) wait(sm.cfull[i % kStages], i / kStages);
         }
-    } else if (warp == 9) {
+    } else if (warp == kWorkers + 1) {
         constexpr uint32_t iS = umma_idesc_bf16(BR, BC), iA = umma_idesc_bf16(BR, D) | kUmmaBmn;
-        // S, dP of column tile number c (of all) with rows in buffer x: waits for the tile, zeroes its
-        // rows behind the sequence's end (they meet P = dS = 0 in the sums)
+        // column tile number c (of all) has landed; its rows behind the sequence's end (they meet
+        // P = dS = 0 in the sums) become zero
         const uint64_t dr = umma_desc(smem_u32(sm.r)), dc = umma_desc(smem_u32(sm.c)), dct = umma_desc_mn(smem_u32(sm.c), BC * 128);
-        auto issue_s = [&](int c, int x, int there) {
+        auto take = [&](int c, int there) {
             const int s = c % kStages;
             ok = wait(sm.cfull[s], c / kStages);
-            if (!ok) return;
-            if (there < BC) {
+            if (ok && there < BC) {
                 for (int y = 0; y < 2 * KH; ++y)
                     for (int i = there * 8 + lane; i < BC * 8; i += 32)
                         reinterpret_cast<uint4 *>(sm.c[s][y / KH][y % KH])[i] = make_uint4(0u, 0u, 0u, 0u);
                 fence_proxy_async_smem();
                 __syncwarp();
             }
-            tc_fence_after_sync();
-            if (elect_one()) {
-                const uint64_t rows = desc_at(dr, x * sizeof(sm.r[0])), cols = desc_at(dc, s * sizeof(sm.c[0]));
+        };
+        // S, dP of the tile (by the elected lane)
+        auto issue_s = [&](int c, bool last) {
+            const uint64_t cols = desc_at(dc, c % kStages * (uint32_t)sizeof(sm.c[0]));
 #pragma unroll
-                for (int y = 0; y < 2; ++y)
+            for (int y = 0; y < 2; ++y)
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk)
-                        umma_bf16(tm + 128 * y + 64 * (c & 1), desc_at(rows, BR * 128 * (KH * y + kk / 4) + 32 * (kk % 4)),
-                                  desc_at(cols, BC * 128 * (KH * y + kk / 4) + 32 * (kk % 4)), iS, kk > 0);
-                umma_commit(&sm.sfull[c & 1]);
-            }
-            __syncwarp();
+                for (int kk = 0; kk < D / 16; ++kk)
+                    umma_bf16(tm + 128 * y + 64 * (c & 1), desc_at(dr, BR * 128 * (KH * y + kk / 4) + 32 * (kk % 4)),
+                              desc_at(cols, BC * 128 * (KH * y + kk / 4) + 32 * (kk % 4)), iS, kk > 0);
+            umma_commit(&sm.sfull[c & 1]);
+            if (last) umma_commit(&sm.rfree);   // the next unit's rows load beside this one's last sums
         };
         int done = 0;   // column tiles whose S, dP were issued
         for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
             if (!w.set(a, u)) continue;
-            const int x = nu & 1;
-            ok = wait(sm.rfull[x], nu / 2);
+            ok = wait(sm.rfull, nu);
             for (int b = 0; b < min(2, w.n) && ok; ++b) {
-                issue_s(nc + b, x, w.len - w.col0(b));
-                if (ok) ++done;
+                take(nc + b, w.len - w.col0(b));
+                if (!ok) break;
+                tc_fence_after_sync();
+                if (elect_one()) issue_s(nc + b, b == w.n - 1);
+                __syncwarp();
+                ++done;
             }
             for (int b = 0; b < w.n && ok; ++b, ++nc) {
-                ok = wait(sm.dfull[nc & 1], nc / 2);
+                // before the tile's P, dS are there: the sums and the next products then go out together
+                if (b + 2 < w.n) take(nc + 2, w.len - w.col0(b + 2));
+                if (ok) ok = wait(sm.dfull[nc & 1], nc / 2);
                 if (ok && b == 0 && nu > 0) ok = wait(sm.accfree, nu - 1);
                 if (!ok) break;
                 tc_fence_after_sync();
@@ -224,25 +228,20 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     const uint64_t cols = desc_at(dct, s * sizeof(sm.c[0]));
 #pragma unroll
                     for (int kk = 0; kk < BC / 16; ++kk)
-                        umma_bf16_ta(tm + 256, tm + 128 + 64 * (nc & 1) + 8 * kk,
-                                     desc_at(cols, 2048 * kk), iA, b > 0 || kk > 0);
+                        umma_bf16_ta(tm + 256, tm + 128 + 64 * (nc & 1) + 8 * kk + (kk < 2 ? 0 : 16), desc_at(cols, 2048 * kk), iA,
+                                     b > 0 || kk > 0);
                     if (KEYS) {
 #pragma unroll
                         for (int kk = 0; kk < BC / 16; ++kk)
-                            umma_bf16_ta(tm + 384, tm + 64 * (nc & 1) + 8 * kk,
+                            umma_bf16_ta(tm + 384, tm + 64 * (nc & 1) + 8 * kk + (kk < 2 ? 0 : 16),
                                          desc_at(cols, BC * 128 * KH + 2048 * kk), iA, b > 0 || kk > 0);
                     }
                     umma_commit(&sm.cfree[s]);
-                    if (b == w.n - 1) {
-                        umma_commit(&sm.rfree[x]);
-                        umma_commit(&sm.accfull);
-                    }
+                    if (b == w.n - 1) umma_commit(&sm.accfull);
+                    if (b + 2 < w.n) issue_s(nc + 2, b + 2 == w.n - 1);
                 }
                 __syncwarp();
-                if (b + 2 < w.n) {
-                    issue_s(nc + 2, x, w.len - w.col0(b + 2));
-                    if (ok) ++done;
-                }
+                if (b + 2 < w.n) ++done;
             }
             ++nu;
         }
@@ -251,9 +250,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             for (int i = max(0, nc - kStages); i < nc; ++i) wait(sm.cfree[i % kStages], i / kStages);
         }
     } else {
-        const int g = warp / 4, quarter = warp % 4, t = quarter * 32 + lane;
+        const int g = warp / 8, half = (warp / 4) % 2, quarter = warp % 4, t = quarter * 32 + lane;
         const uint32_t lanes = (uint32_t)quarter << 21;
-        const uint32_t tS = tm + 64 * g + lanes, tP = tm + 128 + 64 * g + lanes;
+        const uint32_t tS = tm + 64 * g + 32 * half + lanes, tP = tm + 128 + 64 * g + 32 * half + lanes;
         const float sc = a.scale * kLog2e;
         for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
             if (!w.set(a, u)) continue;
@@ -269,73 +268,76 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 // masked only where the diagonal, the window's far edge or the end crosses the tile
                 const int i0 = KEYS ? c0 : w.r0, i1 = KEYS ? c0 + BC : w.r0 + BR, j0 = KEYS ? w.r0 : c0, j1 = KEYS ? w.r0 + BR : c0 + BC;
                 const bool edge = !(j1 - 1 <= i0 && (i1 - 1 - j0 < a.window || j1 <= a.sinks) && i1 <= w.len);
-                const float2 *ld = sm.ld[nc % kStages];
+                const int y = c0 + 32 * half;
+                uint32_t seen = 0xffffffffu;
+                if (edge) {   // bit x: column y + x
+                    if (KEYS) {   // queries from this key on, below its window's end (a sink: any), below len
+                        const int from = row - y;
+                        const long long end = row < a.sinks ? (long long)w.len : min((long long)w.len, (long long)row + a.window);
+                        const long long n = end - y;
+                        seen = from <= 0 ? 0xffffffffu : from > 31 ? 0u : 0xffffffffu << from;
+                        seen &= n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << (int)n) - 1u;
+                    } else {      // keys up to this query, from its window's start on or sinks
+                        const int top = row - y, before = a.sinks - y;
+                        const long long from = (long long)row - a.window + 1 - y;
+                        const uint32_t near = from <= 0 ? 0xffffffffu : from > 31 ? 0u : 0xffffffffu << (int)from;
+                        const uint32_t sink = before >= 32 ? 0xffffffffu : before <= 0 ? 0u : (1u << before) - 1u;
+                        seen = (top >= 31 ? 0xffffffffu : top < 0 ? 0u : (2u << top) - 1u) & (near | sink);
+                    }
+                }
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t s[32], d[32];
-                    tmem_ld32(tS + 32 * half, s);
-                    tmem_ld32(tP + 32 * half, d);
+                for (int b16 = 0; b16 < 32; b16 += 16) {
+                    uint32_t s[16], d[16], pk[8], dk[8];
+                    tmem_ld16(tS + b16, s);
+                    tmem_ld16(tP + b16, d);
                     tmem_wait_ld();
-                    tmem_tie(s);
-                    tmem_tie(d);
-                    uint32_t seen = 0xffffffffu;
-                    if (edge) {   // bit x: column c0 + 32 half + x
-                        const int y = c0 + 32 * half;
-                        if (KEYS) {   // queries from this key on, below its window's end (a sink: any), below len
-                            const int from = row - y;
-                            const long long end = row < a.sinks ? (long long)w.len : min((long long)w.len, (long long)row + a.window);
-                            const long long n = end - y;
-                            seen = from <= 0 ? 0xffffffffu : from > 31 ? 0u : 0xffffffffu << from;
-                            seen &= n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << (int)n) - 1u;
-                        } else {      // keys up to this query, from its window's start on or sinks
-                            const int top = row - y, before = a.sinks - y;
-                            const long long from = (long long)row - a.window + 1 - y;
-                            const uint32_t near = from <= 0 ? 0xffffffffu : from > 31 ? 0u : 0xffffffffu << (int)from;
-                            const uint32_t sink = before >= 32 ? 0xffffffffu : before <= 0 ? 0u : (1u << before) - 1u;
-                            seen = (top >= 31 ? 0xffffffffu : top < 0 ? 0u : (2u << top) - 1u) & (near | sink);
-                        }
-                    }
-                    uint32_t pk[16], dk[16];
+                    tmem_tie16(s);
+                    tmem_tie16(d);
+                    const float2 *ld = sm.ld[nc % kStages] + 32 * half + b16 + (KEYS ? col_index(w, w.col_head(a, b), c0) & 1 : 0);
 #pragma unroll
-                    for (int x = 0; x < 32; x += 2) {
-                        float p[2], e[2];
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            const float2 c = KEYS ? ld[32 * half + x + y] : mine;
-                            p[y] = ex2(fmaf(__uint_as_float(s[x + y]), sc, -c.x));
-                            e[y] = p[y] * (__uint_as_float(d[x + y]) - c.y);
-                            if (edge && !((seen >> (x + y)) & 1u)) p[y] = e[y] = 0.f;
+                    for (int x = 0; x < 16; x += 2) {
+                        const float2 c = KEYS ? ld[x] : mine, c1 = KEYS ? ld[x + 1] : mine;
+                        const float2 z = fma2(make_float2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), make_float2(sc, sc), make_float2(c.x, c1.x));
+                        const float2 f = add2(make_float2(__uint_as_float(d[x]), __uint_as_float(d[x + 1])), make_float2(c.y, c1.y));
+                        float p0 = ex2(z.x), p1 = ex2(z.y);
+                        const float2 g2 = mul2(make_float2(p0, p1), f);
+                        float e0 = g2.x, e1 = g2.y;
+                        if (edge) {
+                            if (!((seen >> (b16 + x)) & 1u)) p0 = e0 = 0.f;
+                            if (!((seen >> (b16 + x + 1)) & 1u)) p1 = e1 = 0.f;
                         }
-                        pk[x / 2] = pack_bf16(p[0], p[1]);
-                        dk[x / 2] = pack_bf16(e[0], e[1]);
+                        pk[x / 2] = pack_bf16(p0, p1);
+                        dk[x / 2] = pack_bf16(e0, e1);
                     }
-                    if (KEYS) tmem_st16(tS + 16 * half, pk);
-                    tmem_st16(tP + 16 * half, dk);
+                    // over columns that this thread has read
+                    if (KEYS) tmem_st8(tS + b16 / 2, pk);
+                    tmem_st8(tP + b16 / 2, dk);
                 }
                 tmem_wait_st();
                 tc_fence_before_sync();
-                mbar_arrive(&sm.dfull[g]);
+                mbar_arrive_warp(&sm.dfull[g]);
             }
             if (!ok) break;
             ok = wait(sm.accfull, nu);
             if (!ok) break;
             ++nu;
             tc_fence_after_sync();
-            // KEYS: warps 0-3 write dv, 4-7 dk; else both write half the channels of dq
-            constexpr int W = KEYS ? D : D / 2;
-            const uint32_t src = tm + lanes + (KEYS ? (g == 0 ? 384 : 256) : 256 + W * g);
+            // KEYS: group 0 writes dv, 1 dk, a thread half the channels; else a quarter of dq's
+            constexpr int W = KEYS ? D / 2 : D / 4;
+            const int x0 = W * (KEYS ? half : 2 * g + half);
+            const uint32_t src = tm + lanes + x0 + (KEYS && g == 0 ? 384 : 256);
             const float f = KEYS && g == 0 ? 1.f : a.scale;
-            const size_t at = ((size_t)(w.row0 + row) * (KEYS ? a.Hkv : a.Hq) + w.head) * D;
-            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(KEYS ? (g == 0 ? a.dv : a.dk) : a.dq) + at + (KEYS ? 0 : W * g);
+            const size_t at = ((size_t)(w.row0 + row) * (KEYS ? a.Hkv : a.Hq) + w.head) * D + x0;
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(KEYS ? (g == 0 ? a.dv : a.dk) : a.dq) + at;
 #pragma unroll
-            for (int x = 0; x < W; x += 32) {
-                uint32_t o[32];
-                tmem_ld32(src + x, o);
+            for (int x = 0; x < W; x += 16) {
+                uint32_t o[16];
+                tmem_ld16(src + x, o);
                 tmem_wait_ld();
-                tmem_tie(o);
+                tmem_tie16(o);
                 if (row < w.r1) {
 #pragma unroll
-                    for (int y = 0; y < 32; y += 8) {
+                    for (int y = 0; y < 16; y += 8) {
                         uint4 v;
                         v.x = pack_bf16(__uint_as_float(o[y]) * f, __uint_as_float(o[y + 1]) * f);
                         v.y = pack_bf16(__uint_as_float(o[y + 2]) * f, __uint_as_float(o[y + 3]) * f);
@@ -346,14 +348,14 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 }
             }
             tc_fence_before_sync();
-            mbar_arrive(&sm.accfree);
+            mbar_arrive_warp(&sm.accfree);
         }
     }
     if (!ok && lane == 0) atomicOr(&g_swa_bwd_timeout, 1);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    if (warp == 9) tmem_dealloc(tm, 512);
+    if (warp == kWorkers + 1) tmem_dealloc(tm, 512);
 }
 
 template <int D, bool KEYS>

@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     const uint32_t tm = sm.tmem;   // S of tile t at column 128 t, O at 256 + 128 t
     bool ok = true;
     auto wait = [&](uint64_t &bar, int phase) {   // by a whole warp
-        return (bool)__all_sync(0xffffffffu, mbar_wait(&bar, phase & 1, kSwaWait));
+        return mbar_wait_warp(&bar, phase & 1, kIdleWait);
     };
 
     if (warp == 16) {
