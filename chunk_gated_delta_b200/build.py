@@ -1,4 +1,5 @@
-"""Builds libcarve.so (the C-ABI library of include/carve.h and carve_mixers.h) in-tree for sm_100a with nvcc.
+"""Builds libcarve.so (the C-ABI library of include/carve.h and carve_mixers.h) in-tree for sm_100a with nvcc, and
+_carve_bind.so (the host side of the mixers' Python calls, against PyTorch's headers) with g++.
 
 Each .cu file is compiled to an object in its own process (in parallel), then the objects are
 linked into the shared library; an object is rebuilt only when its source, a header or this
@@ -6,15 +7,19 @@ file is newer than it."""
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libcarve.so")
 OBJ = os.path.join(PKG, "_build")
+BIND = os.path.join(PKG, "_carve_bind.so")
+BIND_SRC = os.path.join(PKG, "csrc", "carve_bind.cpp")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2"]
 
@@ -43,6 +48,30 @@ def stale() -> bool:
     return any(os.path.getmtime(p) > t for p in deps())
 
 
+def bind_stale() -> bool:
+    if not os.path.exists(BIND):
+        return True
+    t = os.path.getmtime(BIND)
+    return any(os.path.getmtime(p) > t for p in [BIND_SRC, os.path.abspath(__file__)] +
+               glob.glob(os.path.join(ROOT, "include", "*.h")))
+
+
+def _bind(verbose):
+    """Compiles and links the binding beside libcarve.so, which it finds in its own folder."""
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    inc = os.path.join(torch, "include")
+    cuda = os.path.dirname(os.path.dirname(os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")))
+    tmp = BIND + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-w", "-I", inc, "-I",
+           os.path.join(inc, "torch", "csrc", "api", "include"), "-I", os.path.join(cuda, "include"), "-I",
+           sysconfig.get_paths()["include"], "-o", tmp, BIND_SRC, LIB, "-Wl,-rpath,$ORIGIN", "-L", os.path.join(torch, "lib"),
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BIND)
+
+
 def _compile(src, nvcc, force, verbose):
     obj = _obj(src)
     newest = max(os.path.getmtime(p) for p in [src] + headers())
@@ -60,6 +89,8 @@ def _compile(src, nvcc, force, verbose):
 
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not stale():
+        if bind_stale():
+            _bind(verbose)
         return LIB
     nvcc = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
     os.makedirs(OBJ, exist_ok=True)
@@ -69,6 +100,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     tmp = LIB + f".tmp{os.getpid()}"
     subprocess.run([nvcc, "-shared", *ARCH, "-o", tmp, *objs], check=True)
     os.replace(tmp, LIB)
+    if force or bind_stale():
+        _bind(verbose)
     return LIB
 
 
