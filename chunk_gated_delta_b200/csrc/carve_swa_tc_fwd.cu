@@ -3,18 +3,20 @@
 //
 // A CTA holds two query tiles of 128 rows that read the same keys: two query heads of one key
 // head when the heads pair up (the keys of one 128-row window), else 256 rows of one head.  For
-// each 128-key block that a tile sees:
-//   S = Q K^T                    tcgen05.mma, accumulator in tensor memory (128 columns)
-//   P = 2^{S scale log2 e - m}   two threads a row, 64 scores each in registers; they exchange
+// each 64-key block that a tile sees:
+//   S = Q K^T                    tcgen05.mma, accumulator in tensor memory (64 columns, two buffers)
+//   P = 2^{S scale log2 e - m}   two threads a row, 32 scores each in registers; they exchange
 //                                their maxima through shared memory; P goes back as bf16 over S
 //   O += P V                     A = P from tensor memory, O stays in tensor memory
-// The two tiles alternate, so the tensor core works on one while the other's rows are in
-// softmax.  m is the maximum that was current when O was last rescaled: O is rescaled (a round
-// trip through registers) only when some row's maximum has grown by more than 2^8 since, which
-// keeps P below 2^8 and sums in fp32 exact to rounding; the last division removes the reference.
-// Roles: warps 0-7 and 8-15 softmax of tile 0 and 1 (the second four of each take columns 64 ..
-// 127: four warps a scheduler hide each other's latency, one half as many took 1.7 times as
-// long), warp 16 copies (TMA, ring of four 128-row key or value tiles), warp 17 issues the products.
+// The next block's S is there while this one is in softmax.  (With 128-key blocks tensor memory has room
+// for one S a tile: softmax, P V and the next S of a tile then wait for one another, 3850 cycles for 128
+// keys of both tiles where their products take 2048.)  m is the maximum that was current when O was last
+// rescaled: O is rescaled (a round trip through registers) only when some row's maximum has grown
+// by more than 2^8 since, which keeps P below 2^8 and sums in fp32 exact to rounding; the last
+// division removes the reference.
+// Roles: warps 0-7 and 8-15 softmax of tile 0 and 1 (the second four of each take the upper half of the
+// columns), warp 16 copies (TMA, ring of eight 64-row key or value tiles), warps 17 and 18 issue
+// the products of a tile each.
 //
 // Blocks that a tile does not see are skipped; only blocks that a window edge or the diagonal
 // crosses are masked, by selection.  Value rows behind the sequence's end are zeroed in shared
@@ -38,15 +40,23 @@ int swa_fwd_take_timeout() {
 
 namespace {
 
-constexpr int BM = 128, BN = 128, kStages = 4, kThreadsTc = 576;
+// rows `first` .. 63 of a block of 64 rows x 64 KH channels in operand layout become zero (one warp)
+__device__ __forceinline__ void zero_block_rows(void *tile, int first, int halves, int lane) {
+    for (int y = 0; y < halves; ++y)
+        for (int i = max(first, 0) * 8 + lane; i < 64 * 8; i += 32)
+            reinterpret_cast<uint4 *>(tile)[y * 64 * 8 + i] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+constexpr int BM = 128, BN = 64, kStages = 8, kThreadsTc = 608;
 constexpr float kLazy = 8.f;   // growth of a row's maximum, in powers of two, that O may lag behind
 
 template <int D>
 struct FwdSmem {
     __nv_bfloat16 q[2][D / 64][BM * 64];
     __nv_bfloat16 kv[kStages][D / 64][BN * 64];
-    float part[2][2][BM];   // a row's maximum, at the end its sum, by tile and column half
-    uint64_t qfull, kvfull[kStages], kvfree[kStages], sfull[2], pfull[2], ofull[2], xbar[2][4];
+    float part[2][2][2][BM];   // a row's maximum, at the end its sum, by turn, tile and column half
+    uint64_t qfull, kvfull[kStages], kvfree[kStages], sfull[2][2], pfull[2][2], ofull[2][2];   // [tile][parity of its block]:
+                                                                                          // two blocks may be under way
     uint32_t tmem;
 };
 
@@ -85,13 +95,15 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         mbar_init(&sm.qfull, 1);
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&sm.kvfull[i], 1);
-            mbar_init(&sm.kvfree[i], 1);
+            mbar_init(&sm.kvfree[i], 2);
         }
         for (int t = 0; t < 2; ++t) {
-            mbar_init(&sm.sfull[t], 1);
-            mbar_init(&sm.pfull[t], 256);
-            for (int i = 0; i < 4; ++i) mbar_init(&sm.xbar[t][i], 2);
-            mbar_init(&sm.ofull[t], 1);
+            mbar_init(&sm.sfull[t][0], 1);
+            mbar_init(&sm.sfull[t][1], 1);
+            mbar_init(&sm.pfull[t][0], 8);
+            mbar_init(&sm.pfull[t][1], 8);
+            mbar_init(&sm.ofull[t][0], 1);
+            mbar_init(&sm.ofull[t][1], 1);
         }
         fence_mbar_init();
     }
@@ -99,7 +111,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    const uint32_t tm = sm.tmem;   // S of tile t at column 128 t, O at 256 + 128 t
+    const uint32_t tm = sm.tmem;   // S of tile t at column 128 t, two buffers of 64, O at 256 + 128 t
     bool ok = true;
     auto wait = [&](uint64_t &bar, int phase) {   // by a whole warp
         return mbar_wait_warp(&bar, phase & 1, kIdleWait);
@@ -112,15 +124,20 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 for (int x = 0; x < KH; ++x)
                     tma_load_3d(sm.q[t][x], &mq, 64 * x, w.h[t], (int)(w.row0 + w.i0[t]), &sm.qfull);
             int filled = 0;
+            auto fill = [&](const CUtensorMap *map, int b) {
+                const int s = filled % kStages;
+                if (filled >= kStages) ok = mbar_wait(&sm.kvfree[s], (filled / kStages - 1) & 1, kSwaWait);
+                if (!ok) return;
+                mbar_expect_tx(&sm.kvfull[s], kTile);
+                for (int x = 0; x < KH; ++x) tma_load_3d(sm.kv[s][x], map, 64 * x, w.hk, (int)w.row0 + w.kt.tile(b) * BN, &sm.kvfull[s]);
+                ++filled;
+            };
+            // in the order in which they are used: K0, K1, V0, K2, V1, ...
+            fill(&mk, 0);
+            if (blocks > 1 && ok) fill(&mk, 1);
             for (int b = 0; b < blocks && ok; ++b) {
-                const int row = (int)w.row0 + w.kt.tile(b) * BN;
-                for (int kv = 0; kv < 2 && ok; ++kv, ++filled) {
-                    const int s = filled % kStages;
-                    if (filled >= kStages) ok = mbar_wait(&sm.kvfree[s], (filled / kStages - 1) & 1, kSwaWait);
-                    if (!ok) break;
-                    mbar_expect_tx(&sm.kvfull[s], kTile);
-                    for (int x = 0; x < KH; ++x) tma_load_3d(sm.kv[s][x], kv ? &mv : &mk, 64 * x, w.hk, row, &sm.kvfull[s]);
-                }
+                fill(&mv, b);
+                if (b + 2 < blocks && ok) fill(&mk, b + 2);
             }
             if (!ok) {   // the copies in flight land before the CTA leaves
                 mbar_wait(&sm.qfull, 0, kSwaWait);
@@ -128,133 +145,133 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     mbar_wait(&sm.kvfull[i % kStages], (i / kStages) & 1, kSwaWait);
             }
         }
-    } else if (warp == 17) {
+    } else if (warp >= 17) {
+        // a warp for each tile: what one does between its products runs beside the other's
         constexpr uint32_t iS = umma_idesc_bf16(BM, BN), iO = umma_idesc_bf16(BM, D) | kUmmaBmn;
-        int ns[2] = {0, 0}, np[2] = {0, 0};   // products S and P V issued, per tile
-        const uint64_t dq = umma_desc(smem_u32(sm.q)), dk = umma_desc(smem_u32(sm.kv)), dv = umma_desc_mn(smem_u32(sm.kv), BN * 128);
-        auto issue_s = [&](int t, int slot) {
-            if (elect_one()) {
-                const uint64_t q = desc_at(dq, t * sizeof(sm.q[0])), k = desc_at(dk, slot * sizeof(sm.kv[0]));
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    umma_bf16(tm + 128 * t, desc_at(q, BM * 128 * (kk / 4) + 32 * (kk % 4)), desc_at(k, BN * 128 * (kk / 4) + 32 * (kk % 4)),
-                              iS, kk > 0);
-                umma_commit(&sm.sfull[t]);
-            }
+        const int t = warp - 17;
+        const uint32_t tS = tm + 128 * t, tO = tm + 256 + 128 * t;
+        const uint64_t dq = umma_desc(smem_u32(sm.q[t])), dk0 = umma_desc(smem_u32(sm.kv)), dv0 = umma_desc_mn(smem_u32(sm.kv), BN * 128);
+        int ns = 0, np = 0;             // products S and P V issued
+        int slot = 0, turn = 0;         // the ring, in the order of its copies
+        auto next = [&] {
+            if (elect_one()) umma_commit(&sm.kvfree[slot]);
             __syncwarp();
-            ++ns[t];
+            slot = (slot + 1) % kStages;
+            turn += slot == 0;
         };
-        ok = wait(sm.qfull, 0) && wait(sm.kvfull[0], 0);
-        tc_fence_after_sync();
-        if (ok) {
-            for (int t = 0; t < 2; ++t)
-                if (w.sees(a, t, w.kt.tile(0) * BN)) issue_s(t, 0);
-            if (elect_one()) umma_commit(&sm.kvfree[0]);
-        }
-        for (int b = 0; b < blocks && ok; ++b) {
-            const int vs = (2 * b + 1) % kStages, ks = (2 * b + 2) % kStages;
-            const int j0 = w.kt.tile(b) * BN, j1 = b + 1 < blocks ? w.kt.tile(b + 1) * BN : 0;
-            ok = wait(sm.kvfull[vs], (2 * b + 1) / kStages);
-            if (ok && w.len - j0 < BN) {   // value rows behind the end: zero
-                const int first = w.len - j0;
-                for (int x = 0; x < KH; ++x)
-                    for (int i = first * 8 + lane; i < BN * 8; i += 32)
-                        reinterpret_cast<uint4 *>(sm.kv[vs][x])[i] = make_uint4(0u, 0u, 0u, 0u);
-                fence_proxy_async_smem();
-                __syncwarp();
-            }
-            if (ok && b + 1 < blocks) ok = wait(sm.kvfull[ks], (2 * b + 2) / kStages);
-            for (int t = 0; t < 2 && ok; ++t) {
-                if (w.sees(a, t, j0)) {
-                    ok = wait(sm.pfull[t], np[t]);
-                    if (!ok) break;
-                    tc_fence_after_sync();
-                    if (elect_one()) {
-                        const uint64_t v = desc_at(dv, vs * sizeof(sm.kv[0]));
+        auto issue_s = [&](bool sees) {   // S of a key block
+            ok = wait(sm.kvfull[slot], turn);
+            if (!ok) return;
+            if (sees) {
+                tc_fence_after_sync();
+                if (elect_one()) {
+                    const uint64_t k = desc_at(dk0, slot * sizeof(sm.kv[0]));
 #pragma unroll
-                        for (int kk = 0; kk < BN / 16; ++kk)
-                            umma_bf16_ta(tm + 256 + 128 * t, tm + 128 * t + 8 * kk + (kk < 4 ? 0 : 32),
-                                         desc_at(v, 2048 * kk), iO, kk > 0 || np[t] > 0);
-                        umma_commit(&sm.ofull[t]);
-                    }
-                    __syncwarp();
-                    ++np[t];
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        umma_bf16(tS + 64 * (ns & 1), desc_at(dq, BM * 128 * (kk / 4) + 32 * (kk % 4)),
+                                  desc_at(k, BN * 128 * (kk / 4) + 32 * (kk % 4)), iS, kk > 0);
+                    umma_commit(&sm.sfull[t][ns & 1]);
                 }
-                if (b + 1 < blocks && w.sees(a, t, j1)) issue_s(t, ks);
+                __syncwarp();
+                ++ns;
             }
-            if (elect_one()) {
-                umma_commit(&sm.kvfree[vs]);
-                if (b + 1 < blocks) umma_commit(&sm.kvfree[ks]);
+            next();
+        };
+        auto sees = [&](int b) { return b < blocks && w.sees(a, t, w.kt.tile(b) * BN); };
+        bool s0 = sees(0), s1 = sees(1);   // of blocks b and b + 1
+        ok = wait(sm.qfull, 0);
+        if (ok) issue_s(s0);
+        if (ok && blocks > 1) issue_s(s1);
+        for (int b = 0; b < blocks && ok; ++b) {
+            const bool s2 = sees(b + 2);
+            ok = wait(sm.kvfull[slot], turn);
+            if (!ok) break;
+            if (s0) {
+                const int there = w.len - w.kt.tile(b) * BN;
+                if (there < BN) {   // value rows behind the end: zero (by both warps, each before its product)
+                    zero_block_rows(sm.kv[slot][0], there, KH, lane);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                ok = wait(sm.pfull[t][np & 1], np / 2);
+                if (!ok) break;
+                tc_fence_after_sync();
+                if (elect_one()) {
+                    const uint64_t v = desc_at(dv0, slot * sizeof(sm.kv[0]));
+#pragma unroll
+                    for (int kk = 0; kk < BN / 16; ++kk)
+                        umma_bf16_ta(tO, tS + 64 * (np & 1) + 8 * kk + (kk < 2 ? 0 : 16), desc_at(v, 2048 * kk), iO, kk > 0 || np > 0);
+                    umma_commit(&sm.ofull[t][np & 1]);
+                }
+                __syncwarp();
+                ++np;
             }
+            next();
+            // the buffer of block b, whose P has been issued for, takes block b + 2
+            if (b + 2 < blocks) issue_s(s2);
+            s0 = s1;
+            s1 = s2;
         }
         // products in flight finish before the tensor memory is freed: the softmax warps wait for
-        // the last of each tile, and on the way out after a timeout this warp does
-        if (!ok)
-            for (int t = 0; t < 2; ++t) {
-                if (ns[t]) wait(sm.sfull[t], ns[t] - 1);
-                if (np[t]) wait(sm.ofull[t], np[t] - 1);
-            }
+        // the last P V, and on the way out after a timeout this warp does
+        if (!ok) {
+            for (int i = max(0, ns - 2); i < ns; ++i) wait(sm.sfull[t][i & 1], i / 2);
+            for (int i = max(0, np - 2); i < np; ++i) wait(sm.ofull[t][i & 1], i / 2);
+        }
     } else {
         const int t = warp / 8, half = (warp / 4) % 2, quarter = warp % 4, r = quarter * 32 + lane, i = w.i0[t] + r;
         const uint32_t lanes = (uint32_t)quarter << 21;   // lane quarter in bits 16+
-        // this thread's 64 scores (and over the first 32 of them its 64 values of P), its half of O
-        const uint32_t tS = tm + 128 * t + 64 * half + lanes, tO = tm + 256 + 128 * t + (D / 2) * half + lanes;
+        // this thread's 32 scores (and over the first 16 of them its 32 values of P), its half of O
+        const uint32_t tS0 = tm + 128 * t + 32 * half + lanes, tO = tm + 256 + 128 * t + (D / 2) * half + lanes;
         const bool plain = a.scale > 0.f;   // else the scores are scaled first (its sign, or zero)
         const float sc = (plain ? a.scale : 1.f) * 1.4426950408889634f;
         float m = -INFINITY, l = 0.f;   // reference maximum (of unscaled scores) and this half's sum
-        int nb = 0, nx = 0;
-        auto other = [&](float x) {     // exchange with the thread of the row's other half
-            sm.part[t][half][r] = x;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.xbar[t][quarter]);
-            ok = wait(sm.xbar[t][quarter], nx++);
-            return sm.part[t][1 - half][r];
+        int nb = 0;
+        // exchange with the thread of the row's other half: a barrier of the two warps that both reach once a
+        // block whatever else fails (after a wait that ran out the loop goes on without waiting)
+        int nx = 0;
+        auto other = [&](float x) {
+            sm.part[nx & 1][t][half][r] = x;
+            asm volatile("bar.sync %0, 64;\n" ::"r"(1 + 4 * t + quarter) : "memory");
+            return sm.part[nx++ & 1][t][1 - half][r];
         };
-        for (int b = 0; b < blocks && ok; ++b) {
+        for (int b = 0; b < blocks; ++b) {
             const int j0 = w.kt.tile(b) * BN;
             if (!w.sees(a, t, j0)) continue;
-            ok = wait(sm.sfull[t], nb);
-            if (!ok) break;
+            ok = ok && wait(sm.sfull[t][nb & 1], nb / 2);
             tc_fence_after_sync();
-            uint32_t s[64];
+            const uint32_t tS = tS0 + 64 * (nb & 1);
+            uint32_t s[32];
             tmem_ld32(tS, s);
-            tmem_ld32(tS + 32, s + 32);
             tmem_wait_ld();
             tmem_tie(s);
-            tmem_tie(s + 32);
             if (!plain) {
 #pragma unroll
-                for (int x = 0; x < 64; ++x) s[x] = __float_as_uint(__uint_as_float(s[x]) * a.scale);
+                for (int x = 0; x < 32; ++x) s[x] = __float_as_uint(__uint_as_float(s[x]) * a.scale);
             }
             // masked only where the diagonal or the window's far edge crosses the block
             if (!(j0 + BN - 1 <= w.i0[t] && (w.i0[t] + BM - 1 - j0 < a.window || j0 + BN <= a.sinks))) {
-                const int c0 = j0 + 64 * half, hi = i - c0;                      // seen: columns 0 .. hi that are
-                const int lo = (int)max((long long)i - a.window + 1 - c0, 0LL);  // from lo on, or before sk
-                const int sk = a.sinks - c0;
+                const int c0 = j0 + 32 * half, top = i - c0;                       // seen: columns 0 .. top that are
+                const int from = (int)max((long long)i - a.window + 1 - c0, 0LL);  // from this one on, or sinks
+                const int before = a.sinks - c0;
+                const uint32_t past = top >= 31 ? 0xffffffffu : top < 0 ? 0u : (2u << top) - 1u;
+                const uint32_t near = from > 31 ? 0u : 0xffffffffu << from;
+                const uint32_t sink = before >= 32 ? 0xffffffffu : before <= 0 ? 0u : (1u << before) - 1u;
+                const uint32_t seen = past & (near | sink);
 #pragma unroll
-                for (int y = 0; y < 64; y += 32) {
-                    const int top = hi - y, from = lo - y, before = sk - y;
-                    const uint32_t past = top >= 31 ? 0xffffffffu : top < 0 ? 0u : (2u << top) - 1u;
-                    const uint32_t near = from <= 0 ? 0xffffffffu : from > 31 ? 0u : 0xffffffffu << from;
-                    const uint32_t sink = before >= 32 ? 0xffffffffu : before <= 0 ? 0u : (1u << before) - 1u;
-                    const uint32_t seen = past & (near | sink);
-#pragma unroll
-                    for (int x = 0; x < 32; ++x)
-                        if (!((seen >> x) & 1u)) s[y + x] = 0xff800000u;   // -inf
-                }
+                for (int x = 0; x < 32; ++x)
+                    if (!((seen >> x) & 1u)) s[x] = 0xff800000u;   // -inf
             }
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int x = 0; x < 64; ++x) mx[x & 3] = fmaxf(mx[x & 3], __uint_as_float(s[x]));
+            for (int x = 0; x < 32; x += 2) mx[x / 2 & 3] = max3(mx[x / 2 & 3], __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
             float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             mb = fmaxf(mb, other(mb));
-            if (!ok) break;
             const bool grown = (mb - m) * sc > kLazy;   // of this row alone: a row's result depends on no other
             if (__any_sync(0xffffffffu, grown)) {       // rare after the first block
                 const float m1 = grown ? mb : m, f = grown ? ex2((m - m1) * sc) : 1.f;
                 if (nb > 0) {
-                    ok = wait(sm.ofull[t], nb - 1);
-                    if (!ok) break;
+                    ok = ok && wait(sm.ofull[t][(nb - 1) & 1], (nb - 1) / 2);
                     tc_fence_after_sync();
 #pragma unroll 1
                     for (int x = 0; x < D / 2; x += 16) {
@@ -271,24 +288,24 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 m = m1;
             }
             const float base = m == -INFINITY ? 0.f : m * sc;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int x = 0; x < 64; x += 2) {
-                const float p0 = ex2(fmaf(__uint_as_float(s[x]), sc, -base)), p1 = ex2(fmaf(__uint_as_float(s[x + 1]), sc, -base));
-                sum[x & 2] += p0;
-                sum[(x & 2) + 1] += p1;
-                s[x / 2] = pack_bf16(p0, p1);
+            for (int x = 0; x < 32; x += 2) {
+                const float2 z = fma2(make_float2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), make_float2(sc, sc), make_float2(-base, -base));
+                const float2 p = make_float2(ex2(z.x), ex2(z.y));
+                sum[x / 2 & 1] = add2(sum[x / 2 & 1], p);
+                s[x / 2] = pack_bf16(p.x, p.y);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tmem_st32(tS, s);
+            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            tmem_st16(tS, s);
             tmem_wait_st();
             tc_fence_before_sync();
-            mbar_arrive(&sm.pfull[t]);
+            mbar_arrive_warp(&sm.pfull[t][nb & 1]);
             ++nb;
         }
-        if (ok && nb > 0) {
+        if (nb > 0) {
             l += other(l);
-            ok = ok && wait(sm.ofull[t], nb - 1);
+            ok = ok && wait(sm.ofull[t][(nb - 1) & 1], (nb - 1) / 2);
             tc_fence_after_sync();
             const float inv = 1.f / l;
             const size_t at = (size_t)(w.row0 + i) * a.Hq + w.h[t];
