@@ -14,8 +14,8 @@
 //   S = R1 C1^T, dP = R2 C2^T   accumulators in tensor memory, two buffers
 //   P, dS                       two threads a row, 32 columns each; back to tensor memory as bf16 over S, dP
 //   acc1 += dS C1 (dk or dq),  acc2 += P C2 (dv)   A from tensor memory, C's rows contracted
-// Roles: warps 0-7 and 8-15 form P, dS of the even and odd column tiles, warp 16 copies, warp 17 issues
-// the products: S, dP of the tile after next go out while the other buffer is being worked on.
+// Roles: warps 0-7 and 8-15 form P, dS of the even and odd column tiles, warp 16 copies, warp 18 takes what
+// has landed, warp 17 issues the products: S, dP of the tile after next go out while the other buffer is being worked on.
 // Persistent: a CTA walks its units with one set of running phases; R is given back with the unit's last
 // S and dP, so the next unit's rows load beside this one's last sums and epilogue.  Four column stages:
 // three tiles are held by what is being computed.
@@ -38,7 +38,7 @@ int swa_bwd_take_timeout() {
 
 namespace {
 
-constexpr int BR = 128, BC = 64, kStages = 4, kWorkers = 16, kThreadsTc = (kWorkers + 2) * 32;
+constexpr int BR = 128, BC = 64, kStages = 4, kWorkers = 16, kThreadsTc = (kWorkers + 3) * 32;
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>
@@ -46,7 +46,7 @@ struct BwdSmem {
     __nv_bfloat16 r[2][D / 64][BR * 64];           // R1, R2
     __nv_bfloat16 c[kStages][2][D / 64][BC * 64];  // [stage][C1, C2]
     float2 ld[kStages][BC + 2];                    // (-lse log2 e, -delta) of the columns (KEYS), from an even index on
-    uint64_t rfull, rfree, cfull[kStages], cfree[kStages], sfull[2], dfull[2], accfull, accfree;
+    uint64_t rfull, rfree, cfull[kStages], cready[kStages], cfree[kStages], sfull[2], dfull[2], accfull, accfree;
     uint32_t tmem;
 };
 
@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         }
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&sm.cfull[i], 1);
+            mbar_init(&sm.cready[i], 1);
             mbar_init(&sm.cfree[i], 1);
         }
         mbar_init(&sm.rfull, 1);
@@ -178,23 +179,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         }
     } else if (warp == kWorkers + 1) {
         constexpr uint32_t iS = umma_idesc_bf16(BR, BC), iA = umma_idesc_bf16(BR, D) | kUmmaBmn;
-        // column tile number c (of all) has landed; its rows behind the sequence's end (they meet
-        // P = dS = 0 in the sums) become zero
         const uint64_t dr = umma_desc(smem_u32(sm.r)), dc = umma_desc(smem_u32(sm.c)), dct = umma_desc_mn(smem_u32(sm.c), BC * 128);
-        auto take = [&](int c, int there) {
-            const int s = c % kStages;
-            ok = wait(sm.cfull[s], c / kStages);
-            if (ok && there < BC) {
-                for (int y = 0; y < 2 * KH; ++y)
-                    for (int i = there * 8 + lane; i < BC * 8; i += 32)
-                        reinterpret_cast<uint4 *>(sm.c[s][y / KH][y % KH])[i] = make_uint4(0u, 0u, 0u, 0u);
-                fence_proxy_async_smem();
-                __syncwarp();
-            }
-        };
         // S, dP of the tile (by the elected lane)
-        auto issue_s = [&](int c, bool last) {
-            const uint64_t cols = desc_at(dc, c % kStages * (uint32_t)sizeof(sm.c[0]));
+        auto issue_s = [&](int c, int s, bool last) {
+            const uint64_t cols = desc_at(dc, s * (uint32_t)sizeof(sm.c[0]));
 #pragma unroll
             for (int y = 0; y < 2; ++y)
 #pragma unroll
@@ -204,28 +192,35 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             umma_commit(&sm.sfull[c & 1]);
             if (last) umma_commit(&sm.rfree);   // the next unit's rows load beside this one's last sums
         };
-        int done = 0;   // column tiles whose S, dP were issued
+        int done = 0;                    // column tiles whose S, dP were issued
+        int ss = 0, sp = 0, fs = 0;      // stage and phase of the next S, dP, stage of the next sums
+        auto step = [&] {
+            ss = ss + 1 == kStages ? 0 : ss + 1;
+            sp ^= ss == 0;
+            ++done;
+        };
         for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
             if (!w.set(a, u)) continue;
+            const int n = w.n;
             ok = wait(sm.rfull, nu);
-            for (int b = 0; b < min(2, w.n) && ok; ++b) {
-                take(nc + b, w.len - w.col0(b));
-                if (!ok) break;
+            for (int b = 0; b < min(2, n) && ok; ++b) {
+                if (!(ok = wait(sm.cready[ss], sp))) break;
                 tc_fence_after_sync();
-                if (elect_one()) issue_s(nc + b, b == w.n - 1);
+                if (elect_one()) issue_s(nc + b, ss, b == n - 1);
                 __syncwarp();
-                ++done;
+                step();
             }
-            for (int b = 0; b < w.n && ok; ++b, ++nc) {
-                // before the tile's P, dS are there: the sums and the next products then go out together
-                if (b + 2 < w.n) take(nc + 2, w.len - w.col0(b + 2));
+            // The queue of products is short, so what this warp does between them is seen in full: the
+            // tiles are taken by another warp, and the sums and the next products go out together.
+            for (int b = 0; b < n && ok; ++b, ++nc) {
+                const bool more = b + 2 < n;
+                if (more) ok = wait(sm.cready[ss], sp);
                 if (ok) ok = wait(sm.dfull[nc & 1], nc / 2);
                 if (ok && b == 0 && nu > 0) ok = wait(sm.accfree, nu - 1);
                 if (!ok) break;
                 tc_fence_after_sync();
                 if (elect_one()) {
-                    const int s = nc % kStages;
-                    const uint64_t cols = desc_at(dct, s * sizeof(sm.c[0]));
+                    const uint64_t cols = desc_at(dct, fs * (uint32_t)sizeof(sm.c[0]));
 #pragma unroll
                     for (int kk = 0; kk < BC / 16; ++kk)
                         umma_bf16_ta(tm + 256, tm + 128 + 64 * (nc & 1) + 8 * kk + (kk < 2 ? 0 : 16), desc_at(cols, 2048 * kk), iA,
@@ -236,18 +231,36 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                             umma_bf16_ta(tm + 384, tm + 64 * (nc & 1) + 8 * kk + (kk < 2 ? 0 : 16),
                                          desc_at(cols, BC * 128 * KH + 2048 * kk), iA, b > 0 || kk > 0);
                     }
-                    umma_commit(&sm.cfree[s]);
-                    if (b == w.n - 1) umma_commit(&sm.accfull);
-                    if (b + 2 < w.n) issue_s(nc + 2, b + 2 == w.n - 1);
+                    umma_commit(&sm.cfree[fs]);
+                    if (b == n - 1) umma_commit(&sm.accfull);
+                    if (more) issue_s(nc + 2, ss, b + 2 == n - 1);
                 }
                 __syncwarp();
-                if (b + 2 < w.n) ++done;
+                fs = fs + 1 == kStages ? 0 : fs + 1;
+                if (more) step();
             }
             ++nu;
         }
         if (!ok) {   // products in flight finish before the tensor memory is freed
             for (int i = max(0, done - 2); i < done; ++i) wait(sm.sfull[i & 1], i / 2);
             for (int i = max(0, nc - kStages); i < nc; ++i) wait(sm.cfree[i % kStages], i / kStages);
+        }
+    } else if (warp == kWorkers + 2) {
+        // takes the column tiles as they land: rows behind the sequence's end, which meet P = dS = 0 in the
+        // sums, become zero
+        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            if (!w.set(a, u)) continue;
+            for (int b = 0; b < w.n; ++b, ++nc) {
+                const int s = nc % kStages, there = w.len - w.col0(b);
+                if (!(ok = wait(sm.cfull[s], nc / kStages))) break;
+                if (there < BC) {
+                    for (int y = 0; y < 2 * KH; ++y)
+                        for (int i = there * 8 + lane; i < BC * 8; i += 32)
+                            reinterpret_cast<uint4 *>(sm.c[s][y / KH][y % KH])[i] = make_uint4(0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
+                }
+                mbar_arrive_warp(&sm.cready[s]);
+            }
         }
     } else {
         const int g = warp / 8, half = (warp / 4) % 2, quarter = warp % 4, t = quarter * 32 + lane;

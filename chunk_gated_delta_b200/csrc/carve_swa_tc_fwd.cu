@@ -235,9 +235,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             asm volatile("bar.sync %0, 64;\n" ::"r"(1 + 4 * t + quarter) : "memory");
             return sm.part[nx++ & 1][t][1 - half][r];
         };
-        for (int b = 0; b < blocks; ++b) {
-            const int j0 = w.kt.tile(b) * BN;
-            if (!w.sees(a, t, j0)) continue;
+        // the blocks that this tile sees, of those that the CTA walks
+        KeyTiles kt(w.i0[t], max(w.i1[t], w.i0[t] + 1), BN, a.window, a.sinks);
+        const int mine = w.i0[t] < w.i1[t] ? kt.count() : 0;
+        for (int b = 0; b < mine; ++b) {
+            const int j0 = kt.tile(b) * BN;
             ok = ok && wait(sm.sfull[t][nb & 1], nb / 2);
             tc_fence_after_sync();
             const uint32_t tS = tS0 + 64 * (nb & 1);
