@@ -416,3 +416,130 @@ def test_rows_of_a_window_do_not_depend_on_what_they_do_not_see(cuda_device):
         b = carve.carve_swa_fwd(q, k2, v2, window=50, sinks=3)["o"]
         assert torch.equal(a[:, :100], b[:, :100]) and torch.equal(a[:, 129 + 50:], b[:, 129 + 50:])
         assert not torch.equal(a[:, 130:150], b[:, 130:150])
+
+
+def _both_types(f, tensors, scalars):
+    """f on bf16 tensors and, on the same values, in fp32 (other kernels)."""
+    return f(*tensors, **scalars), f(*(x.float() for x in tensors), **scalars)
+
+
+@pytest.mark.parametrize("lens,Hk,Hv,dk,dv", [
+    ((4000,), 4, 8, 128, 128),                                   # more tiles than the GPU has processors, several heads a tile
+    ((64, 128, 1, 0, 640, 63, 65, 1500, 2, 192) * 2, 2, 2, 128, 64), ((320, 321, 319) * 4, 8, 8, 64, 128),
+    (None, 16, 16, 64, 64)])
+def test_delta_over_many_tiles(cuda_device, lens, Hk, Hv, dk, dv):
+    """Persistent work and long chains of chunks: the bf16 kernels against the fp32 ones (which the small
+    cases hold to the definition), packed sequences that end on, before and behind chunk borders.
+    Roundings as in the header: 4 u and 8 u, states 2e-5 and the fp32 kernels' own 1e-5."""
+    packed = lens is not None
+    rows = sum(lens) if packed else 1000
+    lead = (rows,) if packed else (3, rows)
+    g = torch.Generator(device="cuda").manual_seed(21)
+    r = lambda *s: torch.randn(*lead, *s, generator=g, device=cuda_device)  # noqa: E731
+    q, k, v, dO = r(Hk, dk), r(Hk, dk), r(Hv, dv), r(Hv, dv)
+    q, k = q / q.norm(dim=-1, keepdim=True), k / k.norm(dim=-1, keepdim=True)
+    gl, wl = 0.5 * r(Hv) - 3, r(Hv)
+    x = [y.to(torch.bfloat16) for y in (q, k, v, gl, wl, dO)]
+    N = len(lens) if packed else 3
+    S0 = 0.2 * torch.randn(N, Hv, dv, dk, generator=g, device=cuda_device)
+    A, tau = 0.3 * torch.randn(Hv, generator=g, device=cuda_device), 0.5 * torch.randn(Hv, generator=g, device=cuda_device)
+    cu = torch.tensor(np.cumsum((0,) + lens), dtype=torch.int32, device=cuda_device) if packed else None
+
+    def f(q, k, v, gl, wl, dO):
+        more = dict(A_dec=A, tau=tau, cu_seqlens=cu)
+        out = carve.carve_gdr_fwd(q, k, v, gl, wl, S0=S0, **more)
+        g = carve.carve_gdr_bwd(q, k, v, gl, wl, out["saved"], dO, dS_final=S0, **more)
+        return dict(o=out["o"], S=out["S_final"], **g)
+
+    got, want = _both_types(f, x, {})
+    u = U[torch.bfloat16]
+    for n, lim in dict(o=4 * u, S=3e-5, dq=4 * u, dk=8 * u, dv=4 * u, dg_logit=8 * u, dw_logit=8 * u, dS0=4 * u, dA_dec=32 * u,
+                       dtau=32 * u).items():
+        assert rel(got[n], want[n].double().cpu()) <= lim, (n, rel(got[n], want[n].double().cpu()))
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,d,W,sinks", [
+    ((3000,), 8, 2, 128, 700, 4), (None, 6, 6, 64, 129, 0), ((64, 128, 1, 0, 640, 63, 65, 1500, 2, 192) * 2, 6, 2, 128, 65, 70),
+    ((257, 255, 256) * 4, 4, 4, 64, 64, 1)])
+def test_window_over_many_tiles(cuda_device, lens, Hq, Hkv, d, W, sinks):
+    """More units than the GPU has processors, in both pairings of query tiles: the bf16 kernels against
+    the fp32 ones.  Relative L2: the roundings of the header are of either sign, over sums of terms
+    of either sign, so they count once each: 3 u for o, 4 u for the gradients."""
+    packed = lens is not None
+    rows = sum(lens) if packed else 900
+    lead = (rows,) if packed else (4, rows)
+    g = torch.Generator(device="cuda").manual_seed(22)
+    x = [torch.randn(*lead, h, d, generator=g, device=cuda_device).to(torch.bfloat16) for h in (Hq, Hkv, Hkv, Hq)]
+    cu = torch.tensor(np.cumsum((0,) + lens), dtype=torch.int32, device=cuda_device) if packed else None
+
+    def f(q, k, v, dO):
+        at = dict(window=W, sinks=sinks, cu_seqlens=cu)
+        out = carve.carve_swa_fwd(q, k, v, **at)
+        return dict(o=out["o"], lse=out["lse"], **carve.carve_swa_bwd(q, k, v, out["o"], out["lse"], dO, **at))
+
+    got, want = _both_types(f, x, {})
+    u = U[torch.bfloat16]
+    for n, lim in dict(o=3 * u, dq=4 * u, dk=4 * u, dv=3 * u).items():
+        assert rel(got[n], want[n].double().cpu()) <= lim, (n, rel(got[n], want[n].double().cpu()))
+    assert (got["lse"] - want["lse"]).abs().max() <= 1e-4
+
+
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+def test_delta_on_two_streams_at_once(cuda_device, dt):
+    """Forward and backward of two inputs in flight, repeatedly, give what each gives alone."""
+    def inputs(seed):
+        s = delta_inputs(500, 4, 8, 128, 128, dt, seed)
+        return [s[n].to(dt).to(cuda_device)[None].expand(3, -1, *(-1,) * (s[n].dim() - 1)).contiguous() for n in ("q", "k", "v", "g", "w", "dO")]
+
+    def run(x, stream=None):
+        out = carve.carve_gdr_fwd(*x[:5], stream=stream)
+        return [out["o"], out["S_final"], *carve.carve_gdr_bwd(*x[:5], out["saved"], x[5], stream=stream).values()]
+
+    xs = [inputs(s) for s in (1, 2)]
+    alone = [run(x) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    for _ in range(3):
+        got = []
+        for x, s in zip(xs, streams):
+            with torch.cuda.stream(s):
+                got.append(run(x, s))
+        torch.cuda.synchronize()
+        for a, b in zip(alone, got):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_a_state_in_place_of_the_start_state(cuda_device):
+    """S_final may be S0: the call then continues a state in place."""
+    for dt in TYPES:
+        s = delta_inputs(130, 2, 2, 64, 64, dt, 31)
+        x = [s[n].to(dt).to(cuda_device)[None] for n in ("q", "k", "v", "g", "w")]
+        S = torch.randn(1, 2, 64, 64, device=cuda_device)
+        want = carve.carve_gdr_fwd(*x, S0=S, save_for_bwd=False)["S_final"]
+        carve.carve_gdr_fwd(*x, S0=S, save_for_bwd=False, out=dict(S_final=S))
+        assert torch.equal(S, want)
+
+
+def test_refusals_on_the_device(cuda_device):
+    """What the binding refuses with tensors on the GPU: buffers that are too small, a key in the wrong
+    type, a state of the wrong shape; nothing is launched."""
+    dt = torch.bfloat16
+    z = lambda *s: torch.zeros(*s, device=cuda_device, dtype=dt)  # noqa: E731
+    x = (z(1, 70, 2, 64), z(1, 70, 2, 64), z(1, 70, 2, 64), z(1, 70, 2), z(1, 70, 2))
+    few = torch.zeros(64, dtype=torch.uint8, device=cuda_device)
+    with pytest.raises(ValueError, match="bytes"):
+        carve.carve_gdr_fwd(*x, out=dict(saved=few))
+    with pytest.raises(ValueError, match="bytes"):
+        carve.carve_gdr_fwd(*x, save_for_bwd=False, workspace=few)
+    with pytest.raises(ValueError, match="bytes"):
+        carve.carve_gdr_bwd(*x, few, x[2])
+    with pytest.raises(TypeError, match="k must be"):
+        carve.carve_gdr_fwd(x[0], x[1].float(), *x[2:])
+    with pytest.raises(ValueError, match="S0 must have shape"):
+        carve.carve_gdr_fwd(*x, S0=torch.zeros(1, 2, 64, 32, device=cuda_device))
+    with pytest.raises(ValueError, match="is on cpu"):
+        carve.carve_gdr_fwd(x[0], x[1], x[2].cpu(), *x[3:])
+    with pytest.raises(carve.CarveError, match="UNSUPPORTED"):
+        carve.carve_swa_fwd(z(1, 9, 2, 80), z(1, 9, 2, 80), z(1, 9, 2, 80), window=4)
+    with pytest.raises(ValueError, match="lse"):
+        carve.carve_swa_bwd(*x[:3], x[0], torch.zeros(1, 70, 3, device=cuda_device), x[0], window=4)
