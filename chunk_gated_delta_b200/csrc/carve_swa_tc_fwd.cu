@@ -73,7 +73,7 @@ struct Work {
 template <int D>
 __global__ void __launch_bounds__(kThreadsTc, 1)
     swa_tc_fwd(SwaArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-               const __grid_constant__ CUtensorMap mv, int paired) {
+               const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, int paired) {
     extern __shared__ __align__(16) unsigned char raw[];
     FwdSmem<D> &sm = *reinterpret_cast<FwdSmem<D> *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -91,7 +91,20 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                  {h0, paired ? h0 + 1 : h0}, h0 / (a.Hq / a.Hkv), KeyTiles(q0, min(q0 + rows, len), BN, a.window, a.sinks)};
     const int blocks = w.kt.count();
 
-    if (threadIdx.x == 0) {
+    // The copying lane initialises the barriers and sends for the first tiles before the CTA meets: their way
+    // here and the allocation of tensor memory take 1 us each.
+    bool ok = true;
+    const bool copier = warp == 16 && elect_one();
+    int filled = 0;
+    auto fill = [&](const CUtensorMap *map, int b) {
+        const int s = filled % kStages;
+        if (filled >= kStages) ok = mbar_wait(&sm.kvfree[s], (filled / kStages - 1) & 1, kSwaWait);
+        if (!ok) return;
+        mbar_expect_tx(&sm.kvfull[s], kTile);
+        for (int x = 0; x < KH; ++x) tma_load_3d(sm.kv[s][x], map, 64 * x, w.hk, (int)w.row0 + w.kt.tile(b) * BN, &sm.kvfull[s]);
+        ++filled;
+    };
+    if (copier) {
         mbar_init(&sm.qfull, 1);
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&sm.kvfull[i], 1);
@@ -106,35 +119,25 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             mbar_init(&sm.ofull[t][1], 1);
         }
         fence_mbar_init();
+        mbar_expect_tx(&sm.qfull, 2 * BM * D * 2);
+        for (int t = 0; t < 2; ++t)
+            for (int x = 0; x < KH; ++x)
+                tma_load_3d(sm.q[t][x], &mq, 64 * x, w.h[t], (int)(w.row0 + w.i0[t]), &sm.qfull);
+        // in the order in which they are used: K0, K1, V0, K2, V1, ...
+        fill(&mk, 0);
+        if (blocks > 1) fill(&mk, 1);
     }
     if (warp == 17) tmem_alloc(&sm.tmem, 512);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tm = sm.tmem;   // S of tile t at column 128 t, two buffers of 64, O at 256 + 128 t
-    bool ok = true;
     auto wait = [&](uint64_t &bar, int phase) {   // by a whole warp
         return mbar_wait_warp(&bar, phase & 1, kIdleWait);
     };
 
     if (warp == 16) {
-        if (elect_one()) {
-            mbar_expect_tx(&sm.qfull, 2 * BM * D * 2);
-            for (int t = 0; t < 2; ++t)
-                for (int x = 0; x < KH; ++x)
-                    tma_load_3d(sm.q[t][x], &mq, 64 * x, w.h[t], (int)(w.row0 + w.i0[t]), &sm.qfull);
-            int filled = 0;
-            auto fill = [&](const CUtensorMap *map, int b) {
-                const int s = filled % kStages;
-                if (filled >= kStages) ok = mbar_wait(&sm.kvfree[s], (filled / kStages - 1) & 1, kSwaWait);
-                if (!ok) return;
-                mbar_expect_tx(&sm.kvfull[s], kTile);
-                for (int x = 0; x < KH; ++x) tma_load_3d(sm.kv[s][x], map, 64 * x, w.hk, (int)w.row0 + w.kt.tile(b) * BN, &sm.kvfull[s]);
-                ++filled;
-            };
-            // in the order in which they are used: K0, K1, V0, K2, V1, ...
-            fill(&mk, 0);
-            if (blocks > 1 && ok) fill(&mk, 1);
+        if (copier) {
             for (int b = 0; b < blocks && ok; ++b) {
                 fill(&mv, b);
                 if (b + 2 < blocks && ok) fill(&mk, b + 2);
@@ -311,23 +314,37 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             tc_fence_after_sync();
             const float inv = 1.f / l;
             const size_t at = (size_t)(w.row0 + i) * a.Hq + w.h[t];
-            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.o) + at * D + (D / 2) * half;
+            // rows through the tile's query tile (its last S is done) and out by TMA; a last tile's straight to
+            // memory, since the rows behind it are others' (16 bytes a row and store: 2 us a CTA where the
+            // copy takes a quarter of that)
+            const bool whole = w.i1[t] - w.i0[t] == BM;
+            uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + at * D + (D / 2) * half);
 #pragma unroll
             for (int x = 0; x < D / 2; x += 32) {
                 uint32_t o[32];
                 tmem_ld32(tO + x, o);
                 tmem_wait_ld();
                 tmem_tie(o);
-                if (ok && i < w.i1[t]) {
 #pragma unroll
-                    for (int y = 0; y < 32; y += 8) {
-                        uint4 v;
-                        v.x = pack_bf16(__uint_as_float(o[y]) * inv, __uint_as_float(o[y + 1]) * inv);
-                        v.y = pack_bf16(__uint_as_float(o[y + 2]) * inv, __uint_as_float(o[y + 3]) * inv);
-                        v.z = pack_bf16(__uint_as_float(o[y + 4]) * inv, __uint_as_float(o[y + 5]) * inv);
-                        v.w = pack_bf16(__uint_as_float(o[y + 6]) * inv, __uint_as_float(o[y + 7]) * inv);
-                        *reinterpret_cast<uint4 *>(out + x + y) = v;
-                    }
+                for (int y = 0; y < 32; y += 8) {
+                    uint4 v;
+                    v.x = pack_bf16(__uint_as_float(o[y]) * inv, __uint_as_float(o[y + 1]) * inv);
+                    v.y = pack_bf16(__uint_as_float(o[y + 2]) * inv, __uint_as_float(o[y + 3]) * inv);
+                    v.z = pack_bf16(__uint_as_float(o[y + 4]) * inv, __uint_as_float(o[y + 5]) * inv);
+                    v.w = pack_bf16(__uint_as_float(o[y + 6]) * inv, __uint_as_float(o[y + 7]) * inv);
+                    if (whole)
+                        *reinterpret_cast<uint4 *>(sm.q[t][0] + umma_off(r, (D / 2) * half + x + y, BM)) = v;
+                    else if (ok && i < w.i1[t])
+                        out[(x + y) / 8] = v;
+                }
+            }
+            if (whole) {
+                fence_proxy_async_smem();
+                asm volatile("bar.sync %0, 256;\n" ::"r"(9 + t) : "memory");   // the tile's eight warps
+                if (warp % 8 == 0 && ok && elect_one()) {
+                    for (int x = 0; x < KH; ++x) tma_store_3d(&mo, sm.q[t][x], 64 * x, w.h[t], (int)(w.row0 + w.i0[t]));
+                    bulk_commit();
+                    bulk_wait_read<0>();
                 }
             }
             if (ok && a.lse && half == 0 && i < w.i1[t]) a.lse[at] = (m * sc + log2f(l)) * 0.6931471805599453f;
@@ -346,14 +363,15 @@ cudaError_t fwd_t(const SwaArgs &a, cudaStream_t st) {
     const int bytes = (int)sizeof(FwdSmem<D>) + 1024;
     cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), bytes);
     const long long rows = a.seq.cu ? a.seq.total : (long long)a.seq.N * a.seq.T;
-    CUtensorMap mq, mk, mv;
+    CUtensorMap mq, mk, mv, mo;
     if (e == cudaSuccess) e = make_operand_tile_map(&mq, a.q, D, a.Hq, rows, BM);
+    if (e == cudaSuccess) e = make_operand_tile_map(&mo, a.o, D, a.Hq, rows, BM);
     if (e == cudaSuccess) e = make_operand_tile_map(&mk, a.k, D, a.Hkv, rows, BN);
     if (e == cudaSuccess) e = make_operand_tile_map(&mv, a.v, D, a.Hkv, rows, BN);
     if (e != cudaSuccess) return e;
     const int paired = (a.Hq / a.Hkv) % 2 == 0;
     const long long grid = paired ? a.seq.n_tiles(BM) * (a.Hq / 2) : a.seq.n_tiles(2 * BM) * a.Hq;
-    kern<<<(unsigned)grid, kThreadsTc, bytes, st>>>(a, mq, mk, mv, paired);
+    kern<<<(unsigned)grid, kThreadsTc, bytes, st>>>(a, mq, mk, mv, mo, paired);
     return cudaGetLastError();
 }
 
