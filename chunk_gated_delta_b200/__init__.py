@@ -10,7 +10,7 @@ CPU fallback: if libcarve.so is missing or fails to load, every call raises.
     o = carve.carve_step(q1, k1, v1, g1, bx1, w1, A, B, S)      # one decode token, S in place
 
 The two other mixers of a hybrid stack (include/carve_mixers.h) are bound in mixers.py and
-exported here: carve_gdr_fwd / _bwd / _step, the scalar-gated delta rule, and carve_swa_fwd /
+exported here (checks and allocations in _carve_bind.so): carve_gdr_fwd / _bwd / _step, the scalar-gated delta rule, and carve_swa_fwd /
 _bwd / _fill / _step, sliding-window attention with sink tokens.
 """
 from __future__ import annotations
