@@ -399,10 +399,11 @@ cudaError_t launch_swa_fill(bool bf16, const SwaArgs &a, cudaStream_t st) {
 cudaError_t launch_swa_step(bool bf16, const SwaArgs &a, cudaStream_t st) {
     const int share = a.Hq / a.Hkv, groups = (share + kHeads - 1) / kHeads;
     const long long units = (long long)a.seq.N * a.Hkv * groups;
-    // a part holds at least 64 slots (a block of 16 for each warp); more parts only while the
-    // GPU has room for them
+    // a part holds at least 64 slots (a block of 16 for each warp); more parts only while SMs are
+    // without one: their join costs more than it gains beside other units (window 1024, 4 key heads,
+    // 64 sequences: 29 us in one part each, 37 in two, 47 in four)
     int parts = 1;
-    while (parts < 8 && units * parts < 4 * 148 && (a.sinks + a.window) / (2 * parts) >= 64) parts *= 2;
+    while (parts < 8 && units * parts < 148 && (a.sinks + a.window) / (2 * parts) >= 64) parts *= 2;
     if (!bf16) return a.d == 64 ? launch_clusters(swa_step_fp32<64>, a, groups, parts, st) : launch_clusters(swa_step_fp32<128>, a, groups, parts, st);
     if (share <= 8)
         return a.d == 64 ? launch_clusters(swa_step_bf16<64, false>, a, groups, parts, st) : launch_clusters(swa_step_bf16<128, false>, a, groups, parts, st);
