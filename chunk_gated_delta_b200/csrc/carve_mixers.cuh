@@ -98,6 +98,8 @@ struct SwaArgs {
     const void *dO;
     void *dq, *dk, *dv;
     float *delta;              // rowsum(dO * o), [rows, Hq] (tensor-core path: see there)
+    float *partial;            // dk, dv of the parts of the keys' pass [2][parts][rows, Hkv, d], when there are parts
+    int parts;
     // cache
     void *k_cache, *v_cache;
     const long long *pos;
@@ -153,6 +155,7 @@ cudaError_t launch_swa_fwd_simt(const SwaArgs &a, cudaStream_t st);
 cudaError_t launch_swa_bwd_simt(const SwaArgs &a, cudaStream_t st);
 cudaError_t launch_swa_fwd_tc(const SwaArgs &a, cudaStream_t st);
 cudaError_t launch_swa_bwd_tc(const SwaArgs &a, cudaStream_t st);
+int swa_bwd_parts(const SwaArgs &a);
 int swa_fwd_take_timeout();
 int swa_bwd_take_timeout();
 cudaError_t launch_swa_fill(bool bf16, const SwaArgs &a, cudaStream_t st);

@@ -84,6 +84,14 @@ carve::SwaArgs swa_args(const carve_swa_dims *d, const int32_t *cu) {
     return a;
 }
 
+// the backward's scratch: two floats a row and head (the CUDA-core path uses one), and the partial
+// dk, dv where the keys' pass is split
+int swa_parts(const carve_swa_dims *d, const carve::SwaArgs &a) { return d->io == CARVE_IO_BF16 ? carve::swa_bwd_parts(a) : 1; }
+size_t swa_table_bytes(const carve_swa_dims *d, bool packed) { return up(2 * sizeof(float) * (size_t)rows_of(d, packed) * d->Hq) + 1024; }
+size_t swa_partial_bytes(const carve_swa_dims *d, bool packed, int parts) {
+    return parts > 1 ? up(2 * sizeof(float) * (size_t)parts * rows_of(d, packed) * d->Hkv * d->d) : 0;
+}
+
 }  // namespace
 
 extern "C" {
@@ -193,8 +201,9 @@ carve_status carve_swa_fwd(const carve_swa_dims *d, const int32_t *cu_seqlens, c
 
 size_t carve_swa_bwd_workspace_bytes(const carve_swa_dims *d, int packed) {
     if (check(d, true, packed != 0) != CARVE_OK) return 0;
-    // two floats a row and head (the CUDA-core path uses one)
-    return up(2 * sizeof(float) * (size_t)rows_of(d, packed != 0) * d->Hq) + 256;
+    static const int32_t dummy = 0;   // only whether the call is packed counts
+    const carve::SwaArgs a = swa_args(d, packed ? &dummy : nullptr);
+    return swa_table_bytes(d, packed != 0) + swa_partial_bytes(d, packed != 0, swa_parts(d, a)) + 256;
 }
 
 carve_status carve_swa_bwd(const carve_swa_dims *d, const int32_t *cu_seqlens, const void *q,
@@ -213,6 +222,8 @@ carve_status carve_swa_bwd(const carve_swa_dims *d, const int32_t *cu_seqlens, c
     carve::SwaArgs a = swa_args(d, cu_seqlens);
     a.q = q; a.k = k; a.v = v; a.o = const_cast<void *>(o); a.lse = const_cast<float *>(lse);
     a.dO = dO; a.dq = dq; a.dk = dk; a.dv = dv; a.delta = static_cast<float *>(workspace);
+    a.parts = swa_parts(d, a);
+    a.partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + swa_table_bytes(d, packed));
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     return status(d->io == CARVE_IO_BF16 ? carve::launch_swa_bwd_tc(a, cs) : carve::launch_swa_bwd_simt(a, cs));
 }

@@ -4,7 +4,7 @@
 // With lse and delta_i = sum_c dO_ic o_ic from the forward's results,
 //   p_ij = e^{scale q_i.k_j - lse_i},  ds_ij = p_ij (dO_i.v_j - delta_i)
 //   dv_j = sum_i p_ij dO_i,  dk_j = scale sum_i ds_ij q_i,  dq_i = scale sum_j ds_ij k_j
-// Two passes of one kernel, so that every sum stays in one accumulator in a fixed order (one pass
+// Two passes of one kernel (and, for few keys, one that joins the first's parts), so that every sum stays in one accumulator in a fixed order (one pass
 // with dq summed by atomics needs 5 products instead of 7, but its results would depend on the
 // order of arrival).  A unit holds 128 rows (KEYS: keys with dk, dv; else queries with dq) as two
 // resident operand tiles R1, R2 and streams the other side in tiles C1, C2 of 64:
@@ -77,11 +77,17 @@ template <bool KEYS>
 struct Unit {
     long long row0;
     int len, r0, r1, head;   // rows r0 .. r1 - 1, their head
-    int n, per, c0;          // column tiles in all; KEYS: per query head, from tile c0
+    int n, per, c0;          // column tiles; KEYS: per query head, from tile c0
+    int part, b0;            // KEYS: the part of the unit, its first tile of them all
     KeyTiles kt;
     __device__ __forceinline__ bool set(const SwaArgs &a, int u) {
         const int heads = KEYS ? a.Hkv : a.Hq;
         int s, c;
+        part = 0;
+        if (KEYS) {
+            part = u % a.parts;
+            u /= a.parts;
+        }
         if (!a.seq.find(u / heads, BR, s, c, row0, len)) return false;
         head = u % heads;
         r0 = c * BR;
@@ -89,17 +95,19 @@ struct Unit {
         if (KEYS) {
             c0 = r0 / BC;
             per = last_query(r0, r1, len, a.window, a.sinks) / BC - c0 + 1;
-            n = per * (a.Hq / a.Hkv);
+            const long long all = (long long)per * (a.Hq / a.Hkv);
+            b0 = (int)(all * part / a.parts);
+            n = (int)(all * (part + 1) / a.parts) - b0;
         } else {
             kt = KeyTiles(r0, r1, BC, a.window, a.sinks);
             n = kt.count();
         }
         return true;
     }
-    __device__ __forceinline__ int col0(int b) const { return (KEYS ? c0 + b - b / per * per : kt.tile(b)) * BC; }
+    __device__ __forceinline__ int col0(int b) const { return (KEYS ? c0 + b0 + b - (b0 + b) / per * per : kt.tile(b)) * BC; }
     __device__ __forceinline__ int col_head(const SwaArgs &a, int b) const {
         const int share = a.Hq / a.Hkv;
-        return KEYS ? head * share + b / per : head / share;
+        return KEYS ? head * share + (b0 + b) / per : head / share;
     }
 };
 
@@ -144,7 +152,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 
     if (warp == kWorkers) {
         for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-            if (!w.set(a, u)) continue;
+            if (!w.set(a, u) || w.n == 0) continue;
             for (int b = 0; b < w.n; ++b) {
                 if (b == 0) {
                     if (nu > 0) ok = wait(sm.rfree, nu - 1);
@@ -200,7 +208,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             ++done;
         };
         for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-            if (!w.set(a, u)) continue;
+            if (!w.set(a, u) || w.n == 0) continue;
             const int n = w.n;
             ok = wait(sm.rfull, nu);
             for (int b = 0; b < min(2, n) && ok; ++b) {
@@ -249,7 +257,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         // takes the column tiles as they land: rows behind the sequence's end, which meet P = dS = 0 in the
         // sums, become zero
         for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-            if (!w.set(a, u)) continue;
+            if (!w.set(a, u) || w.n == 0) continue;
             for (int b = 0; b < w.n; ++b, ++nc) {
                 const int s = nc % kStages, there = w.len - w.col0(b);
                 if (!(ok = wait(sm.cfull[s], nc / kStages))) break;
@@ -331,10 +339,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 mbar_arrive_warp(&sm.dfull[g]);
             }
             if (!ok) break;
-            ok = wait(sm.accfull, nu);
-            if (!ok) break;
-            ++nu;
-            tc_fence_after_sync();
+            if (w.n > 0) {
+                ok = wait(sm.accfull, nu);
+                if (!ok) break;
+                ++nu;
+                tc_fence_after_sync();
+            }
             // KEYS: group 0 writes dv, 1 dk, a thread half the channels; else a quarter of dq's
             constexpr int W = KEYS ? D / 2 : D / 4;
             const int x0 = W * (KEYS ? half : 2 * g + half);
@@ -342,13 +352,25 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             const float f = KEYS && g == 0 ? 1.f : a.scale;
             const size_t at = ((size_t)(w.row0 + row) * (KEYS ? a.Hkv : a.Hq) + w.head) * D + x0;
             __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(KEYS ? (g == 0 ? a.dv : a.dk) : a.dq) + at;
+            float *sums = KEYS && a.parts > 1 ? a.partial + (size_t)((1 - g) * a.parts + w.part) * rows * a.Hkv * D + at : nullptr;
 #pragma unroll
             for (int x = 0; x < W; x += 16) {
                 uint32_t o[16];
-                tmem_ld16(src + x, o);
-                tmem_wait_ld();
-                tmem_tie16(o);
-                if (row < w.r1) {
+                if (w.n > 0) {
+                    tmem_ld16(src + x, o);
+                    tmem_wait_ld();
+                    tmem_tie16(o);
+                } else {
+#pragma unroll
+                    for (int y = 0; y < 16; ++y) o[y] = 0u;
+                }
+                if (sums) {
+                    if (row < w.r1)
+#pragma unroll
+                        for (int y = 0; y < 16; y += 4)
+                            *reinterpret_cast<float4 *>(sums + x + y) =
+                                make_float4(__uint_as_float(o[y]) * f, __uint_as_float(o[y + 1]) * f, __uint_as_float(o[y + 2]) * f, __uint_as_float(o[y + 3]) * f);
+                } else if (row < w.r1) {
 #pragma unroll
                     for (int y = 0; y < 16; y += 8) {
                         uint4 v;
@@ -361,7 +383,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 }
             }
             tc_fence_before_sync();
-            mbar_arrive_warp(&sm.accfree);
+            if (w.n > 0) mbar_arrive_warp(&sm.accfree);
         }
     }
     if (!ok && lane == 0) atomicOr(&g_swa_bwd_timeout, 1);
@@ -371,6 +393,28 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     if (warp == kWorkers + 1) tmem_dealloc(tm, 512);
 }
 
+// dk, dv of JR rows of a key head: their parts' sums, in order
+constexpr int JR = 8;
+template <int D>
+__global__ void __launch_bounds__(2 * JR * D / 4) swa_join(SwaArgs a, long long rows) {
+    constexpr int X = D / 4;
+    int s, c, len;
+    long long row0;
+    const int u = blockIdx.x / (BR / JR), head = u % a.Hkv;
+    if (!a.seq.find(u / a.Hkv, BR, s, c, row0, len)) return;
+    const int z = threadIdx.x / (JR * X), r = c * BR + blockIdx.x % (BR / JR) * JR + threadIdx.x / X % JR;
+    if (r >= len) return;
+    const size_t per = (size_t)rows * a.Hkv * D, at = ((size_t)(row0 + r) * a.Hkv + head) * D + threadIdx.x % X * 4;
+    const float *src = a.partial + (size_t)z * a.parts * per + at;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int p = 0; p < a.parts; ++p) {
+        const float4 v = *reinterpret_cast<const float4 *>(src + p * per);
+        y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
+    }
+    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(z ? a.dv : a.dk) + at) = make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+}
+
 template <int D, bool KEYS>
 cudaError_t pass(const SwaArgs &a, const CUtensorMap &r1, const CUtensorMap &r2, const CUtensorMap &c1, const CUtensorMap &c2,
                  long long rows, cudaStream_t st) {
@@ -378,7 +422,7 @@ cudaError_t pass(const SwaArgs &a, const CUtensorMap &r1, const CUtensorMap &r2,
     const int bytes = (int)sizeof(BwdSmem<D>) + 1024;
     const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), bytes);
     if (e != cudaSuccess) return e;
-    const int units = (int)(a.seq.n_tiles(BR) * (KEYS ? a.Hkv : a.Hq)), sms = sm_count();
+    const int units = (int)(a.seq.n_tiles(BR) * (KEYS ? a.Hkv * a.parts : a.Hq)), sms = sm_count();
     kern<<<units < sms ? units : sms, kThreadsTc, bytes, st>>>(a, r1, r2, c1, c2, units, rows);
     return cudaGetLastError();
 }
@@ -396,11 +440,25 @@ cudaError_t bwd_t(const SwaArgs &a, cudaStream_t st) {
     }
     swa_rows<D><<<(unsigned)((rows * a.Hq * (D / 8) + 255) / 256), 256, 0, st>>>(a, rows);
     cudaError_t e = pass<D, true>(a, big[1], big[2], small[0], small[3], rows, st);
+    if (e == cudaSuccess && a.parts > 1) swa_join<D><<<(unsigned)(a.seq.n_tiles(BR) * a.Hkv * (BR / JR)), 2 * JR * D / 4, 0, st>>>(a, rows);
     if (e == cudaSuccess) e = pass<D, false>(a, big[0], big[3], small[1], small[2], rows, st);
     return e;
 }
 
 }  // namespace
+
+// Parts that the keys' pass takes a unit's column tiles in, when the units (128 keys of a key head) leave SMs
+// idle: as many as there are SMs for, of four tiles at least.  Partial sums in fp32, joined in order (1 sequence
+// of 1000 tokens, 8 query and 2 key heads, window 200: pass and join 33 us from 75 us; 2 of 4000, 4 and 1 heads,
+// window 1500: 156 us from 271 us).  The rule asks for sizes alone, so that the scratch can be sized without
+// a device; packed calls of very many sequences have too many tile numbers for it.
+int swa_bwd_parts(const SwaArgs &a) {
+    const long long rows = a.seq.cu ? a.seq.total : a.seq.T, units = (a.seq.cu ? a.seq.total / BR + 1 : a.seq.n_tiles(BR)) * a.Hkv;
+    const long long tiles = (a.Hq / a.Hkv) * ((rows < a.window ? rows : a.window) / BC + 2);
+    if (units < 1 || a.seq.N > 4096) return 1;
+    const long long parts = 148 / units < tiles / 4 ? 148 / units : tiles / 4;
+    return parts < 2 ? 1 : parts > 16 ? 16 : (int)parts;
+}
 
 cudaError_t launch_swa_bwd_tc(const SwaArgs &a, cudaStream_t st) {
     return a.d == 64 ? bwd_t<64>(a, st) : bwd_t<128>(a, st);
