@@ -64,7 +64,7 @@ struct PrepSmem {
         };
     };
     __nv_bfloat16 A[kC * 64];
-    float eG[kC], eK[kC], w[kC], G[kC], eB[kC];
+    float eG[kC], eK[kC], w[kC], G[kC], eB[kC], half;
     uint64_t full, done;
     uint32_t tmem;
 };
@@ -162,8 +162,13 @@ __device__ __forceinline__ void invert64(float (*M)[LM], float (*X)[LM]) {
 template <int K>
 __global__ void __launch_bounds__(128) gdr_tc_prep(GdrArgs a, const __grid_constant__ CUtensorMap mq,
                                                    const __grid_constant__ CUtensorMap mk) {
-    extern __shared__ __align__(16) unsigned char raw[];
-    PrepSmem<K> &sm = *reinterpret_cast<PrepSmem<K> *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    // Without room for alignment five CTAs share an SM (four with it); no static shared memory stands before this
+    extern __shared__ __align__(1024) unsigned char raw[];
+    PrepSmem<K> &sm = *reinterpret_cast<PrepSmem<K> *>(raw);
+    if (smem_u32(raw) & 1023u) {
+        if (threadIdx.x == 0) atomicOr(&g_gdr_timeout, 1);
+        return;
+    }
     const int tile = blockIdx.x / a.Hk, hk = blockIdx.x % a.Hk, share = a.Hv / a.Hk;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     int n, c, len;
@@ -182,7 +187,7 @@ __global__ void __launch_bounds__(128) gdr_tc_prep(GdrArgs a, const __grid_const
     tc_fence_after_sync();
     const uint32_t tm = sm.tmem;
     bool ok = true;
-    if (warp == 0) {
+    if (warp == 3) {
         if (elect_one()) {
             mbar_expect_tx(&sm.full, 128 * K * 2);
             for (int x = 0; x < K / 64; ++x) {
@@ -200,6 +205,32 @@ __global__ void __launch_bounds__(128) gdr_tc_prep(GdrArgs a, const __grid_const
         }
         __syncwarp();
     }
+    // gates of a head and the running sums of log a, by warps 0 and 1; rows behind the end: log a = 0, w = 0
+    auto gates = [&](int h) {
+        if (tid >= kC) return;
+        float la = 0.f, w = 0.f;
+        if (tid < m) {
+            const size_t at = (size_t)(row + tid) * a.Hv + h;
+            const float x = ld_io(static_cast<const __nv_bfloat16 *>(a.g_logit) + at) + (a.tau ? a.tau[h] : 0.f);
+            la = -1.4426950408889634f * decay_amp(a.A_dec, h) * softplus_f(x);
+            w = sigmoid_f(ld_io(static_cast<const __nv_bfloat16 *>(a.w_logit) + at));
+        }
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const float up = __shfl_up_sync(0xffffffffu, la, off);
+            if (lane >= off) la += up;
+        }
+        if (tid == 31) sm.half = la;
+        asm volatile("bar.sync 1, 64;\n" ::: "memory");
+        if (warp == 1) la += sm.half;
+        sm.G[tid] = la;
+        sm.w[tid] = w;
+        asm volatile("bar.sync 1, 64;\n" ::: "memory");
+        sm.eG[tid] = exp2f(la);
+        sm.eK[tid] = exp2f(sm.G[kC - 1] - la);
+        sm.eB[tid] = exp2f(sm.G[tid | 15] - la);
+    };
+    gates(hk * share);   // the first head's while the tiles and their product are under way
     ok = ok && mbar_wait(&sm.done, 0, kSwaWait);
     if (__syncthreads_or(!ok)) {   // give up together, with the copy landed and the product finished
         if (tid == 0) {
@@ -219,33 +250,12 @@ __global__ void __launch_bounds__(128) gdr_tc_prep(GdrArgs a, const __grid_const
     for (int i = tid; i < kC * LM / 4; i += 128) reinterpret_cast<float4 *>(sm.X)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
     for (int h = hk * share; h < (hk + 1) * share; ++h) {
-        if (tid == 0) bulk_wait_read<0>();   // the last head's copies out have left the buffers
-        __syncthreads();
-        if (tid < kC) {   // gates and the running sum of log a; rows behind the end: log a = 0, w = 0
-            float la = 0.f, w = 0.f;
-            if (tid < m) {
-                const size_t at = (size_t)(row + tid) * a.Hv + h;
-                const float x = ld_io(static_cast<const __nv_bfloat16 *>(a.g_logit) + at) + (a.tau ? a.tau[h] : 0.f);
-                la = -1.4426950408889634f * decay_amp(a.A_dec, h) * softplus_f(x);
-                w = sigmoid_f(ld_io(static_cast<const __nv_bfloat16 *>(a.w_logit) + at));
-            }
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const float up = __shfl_up_sync(0xffffffffu, la, off);
-                if (lane >= off) la += up;
-            }
-            sm.G[tid] = la;
-            sm.w[tid] = w;
+        if (h > hk * share) {
+            if (tid == 0) bulk_wait_read<0>();   // the last head's copies out have left the buffers
+            __syncthreads();
+            gates(h);
+            __syncthreads();
         }
-        __syncthreads();
-        if (tid >= 32 && tid < kC) sm.G[tid] += sm.G[31];
-        __syncthreads();
-        if (tid < kC) {
-            sm.eG[tid] = exp2f(sm.G[tid]);
-            sm.eK[tid] = exp2f(sm.G[kC - 1] - sm.G[tid]);
-            sm.eB[tid] = exp2f(sm.G[tid | 15] - sm.G[tid]);
-        }
-        __syncthreads();
         const float Gt = sm.G[t], f0 = key ? sm.w[t] : 1.f;
 #pragma unroll 1
         for (int s0 = 0; s0 <= (t | 31); s0 += 16) {
@@ -296,7 +306,7 @@ __global__ void __launch_bounds__(128) gdr_tc_prep(GdrArgs a, const __grid_const
             bulk_commit();
         }
     }
-    if (tid == 0) bulk_wait<0>();
+    if (tid == 0) bulk_wait_read<0>();
     __syncthreads();
     if (warp == 0) tmem_dealloc(tm, 64);
 }
@@ -317,7 +327,7 @@ template <int K, int V, bool SAVE>
 __global__ void __launch_bounds__(kSweepThreads, 1)
     gdr_tc_sweep(GdrArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                  const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo) {
-    extern __shared__ __align__(16) unsigned char raw[];
+    extern __shared__ __align__(1024) unsigned char raw[];
     typedef SweepSmem<K, V, SAVE> Smem;
     Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     constexpr int KH = K / 64, KQ = K / 4;
@@ -600,7 +610,7 @@ cudaError_t fwd_t(const GdrArgs &a, bool save, cudaStream_t st) {
         if (e == cudaSuccess) e = make_operand_tile_map(&mv, a.v, V, a.Hv, rows, kC);
         if (e == cudaSuccess) e = make_operand_tile_map(&mo, a.o, V, a.Hv, rows, kC);
         auto prep = gdr_tc_prep<K>;
-        const int bytes = (int)sizeof(PrepSmem<K>) + 1024;
+        const int bytes = (int)sizeof(PrepSmem<K>);
         if (e == cudaSuccess) e = set_smem_once(reinterpret_cast<const void *>(prep), bytes);
         if (e != cudaSuccess) return e;
         prep<<<(unsigned)(a.seq.n_tiles(kC) * a.Hk), 128, bytes, st>>>(a, mq, mk);
