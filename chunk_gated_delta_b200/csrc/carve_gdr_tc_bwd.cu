@@ -7,7 +7,7 @@
 //   dY = dU Tm (three terms)         -> -w e^G dY, split; dV = w dY; dY
 //   dS0 = e^{G_C} dS1 + (e^G dO)^T Q - (w e^G dY)^T K   (hi, lo) -> split for the next chunk
 // It leaves dS1 and dY of every chunk in bf16.  Bound as the forward's sweep, by the chain and by what it
-// leaves: 8 sequences of 4096 tokens, 16 heads, d = 128 take 205 us.
+// leaves: 8 sequences of 4096 tokens, 16 heads, d = 128 take 208 us.
 //
 // gdr_tc_grad: with S0, U (forward) and dS1, dY known, the gradients of q, k and the gates have no
 // order: persistent CTAs take (tile, key head), all value heads of the key head in turn.  Tokens are the
@@ -17,7 +17,7 @@
 //   [P1; P2] K + [0; P1^T] Q + [0; P2^T] K  accumulated over the value heads
 // P1^T and P2^T are the same tile read along its other index; the zero block beside it fills the
 // lanes that have no part.  It reads two states, U, dY, dO, q and k a chunk: 1.5 GB of the sizes above
-// in 330 us, 4.5 TB/s; beside HBM it is bound by instruction issue (20 thousand warp instructions a
+// in 320 us, 4.6 TB/s; beside HBM it is bound by instruction issue (20 thousand warp instructions a
 // tile and head, a quarter of them waits and arrivals).  A pass that would fuse it with the sweep
 // saves 0.9 GB but needs 448 more columns of tensor memory than there are.
 #include "carve_gdr_tc.cuh"

@@ -3,8 +3,9 @@
 // gdr_tc_prep: one CTA per (tile, key head) forms [Q; K] K^T with one M = 128 product and, for each
 // value head of the key head, the decayed A and M, Tm by blocked inversion (fp32 substitution on the
 // diagonal, three tf32 products off it), and the gate vectors.  It needs no state, so all tiles run
-// at once; instruction issue bounds it (8 sequences of 4096 tokens, 16 heads, d = 128: 123 us, 3.9
-// TB/s; with the inverse in plain fp32 and an exponential a pair 204 us).
+// at once; instruction issue and latency bound it (8 sequences of 4096 tokens, 16 heads, d = 128: 109
+// us, 4.5 TB/s; four CTAs an SM and gates after the product 123, with the inverse in plain fp32 and an
+// exponential a pair 204).
 //
 // gdr_tc_sweep: one CTA per (sequence, value head) carries the state through the chunks.  The state is
 // a tensor-memory accumulator with the value channels as its 128 lanes, so every product of the
