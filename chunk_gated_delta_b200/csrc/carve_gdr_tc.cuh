@@ -183,6 +183,26 @@ __device__ __forceinline__ void store_row(float *dst, const float *S) {
     for (int x = 0; x < COLS; x += 4) *reinterpret_cast<float4 *>(dst + x) = make_float4(S[x], S[x + 1], S[x + 2], S[x + 3]);
 }
 
+// A kernel that reads what the one before it in the stream writes may start beside that one's last CTAs
+// (launch_after) and sets itself up; what it reads of it comes after wait_for_last().  Its own
+// outputs touch nothing that the last kernel reads.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+__device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+template <class... P, class... A>
+cudaError_t launch_after(void (*kern)(P...), unsigned grid, unsigned block, int smem, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 constexpr uint32_t kUmmaAmn = 1u << 15;   // instruction descriptor: A is MN-contiguous
 
 }  // namespace carve

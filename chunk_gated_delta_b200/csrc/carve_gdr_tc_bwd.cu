@@ -61,6 +61,7 @@ template <int K, int V>
 __global__ void __launch_bounds__(kSweepThreads, 1)
     gdr_tc_bsweep(GdrArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                   const __grid_constant__ CUtensorMap md, const __grid_constant__ CUtensorMap mdv) {
+    let_next_start();
     extern __shared__ __align__(16) unsigned char raw[];
     typedef BsweepSmem<K, V> Smem;
     Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
@@ -429,6 +430,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
 
     if (warp >= kRegWarps) regs_down<64>();
     if (warp == kRegWarps) {
+        wait_for_last();   // the sweep
 #pragma unroll 1
         for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
             const int tile = w / a.Hk, hk = w - tile * a.Hk;
@@ -879,7 +881,8 @@ cudaError_t bwd_t(const GdrArgs &a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     sweep<<<a.seq.N * a.Hv, kSweepThreads, sb, st>>>(a, mq, mk, md, mdv);
     const long long tiles = a.seq.n_tiles(kC), items = tiles * a.Hk;
-    if (items) grad<<<(unsigned)(items < sm_count() ? items : sm_count()), kSweepThreads, gb, st>>>(a, mq, mk, md, mdq, mdk);
+    if (items) e = launch_after(grad, (unsigned)(items < sm_count() ? items : sm_count()), kSweepThreads, gb, st, a, mq, mk, md, mdq, mdk);
+    if (e != cudaSuccess) return e;
     if (a.dA_dec || a.dtau)
         launch_gdr_reduce_decay(reinterpret_cast<const float *>(a.ws + (size_t)tiles * a.Hv * sizeof(GdrKeep<K, V>)), tiles, a.Hv,
                                 a.dA_dec, a.dtau, st);

@@ -170,6 +170,7 @@ __global__ void __launch_bounds__(128) gdr_tc_prep(GdrArgs a, const __grid_const
         if (threadIdx.x == 0) atomicOr(&g_gdr_timeout, 1);
         return;
     }
+    let_next_start();
     const int tile = blockIdx.x / a.Hk, hk = blockIdx.x % a.Hk, share = a.Hv / a.Hk;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     int n, c, len;
@@ -361,6 +362,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
 
     if (warp >= kRegWarps) regs_down<64>();
     if (warp == kRegWarps) {
+        wait_for_last();   // the preparation
         int c = 0;
         for (; c < chunks; ++c) {
             const int s = c & 1;
@@ -597,8 +599,7 @@ cudaError_t sweep_t(const GdrArgs &a, const CUtensorMap &mq, const CUtensorMap &
     const int bytes = (int)sizeof(SweepSmem<K, V, SAVE>) + 1024;
     const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), bytes);
     if (e != cudaSuccess) return e;
-    kern<<<a.seq.N * a.Hv, kSweepThreads, bytes, st>>>(a, mq, mk, mv, mo);
-    return cudaGetLastError();
+    return launch_after(kern, (unsigned)(a.seq.N * a.Hv), kSweepThreads, bytes, st, a, mq, mk, mv, mo);
 }
 
 template <int K, int V>
