@@ -121,7 +121,8 @@ carve_status carve_gdr_fwd(const carve_gdr_dims *d, const int32_t *cu_seqlens, c
     if (st != CARVE_OK) return st;
     const long long rows = rows_of(d, packed);
     if (!ok_elem_opt(cu_seqlens) || !ok_ptr(q, rows) || !ok_ptr(k, rows) || !ok_ptr(v, rows) ||
-        !ok_elem(g_logit, io_bytes(d->io), rows) || !ok_elem(w_logit, io_bytes(d->io), rows) || !ok_ptr(o, rows) || !ok_elem_opt(A_dec) || !ok_elem_opt(tau) ||
+        !ok_elem(g_logit, io_bytes(d->io), rows) || !ok_elem(w_logit, io_bytes(d->io), rows) || !ok_ptr(o, rows) ||
+        !ok_elem_opt(A_dec) || !ok_elem_opt(tau) ||
         !ok_opt(S0) || !ok_opt(S_final) || !ok_opt(saved) || !ok_opt(workspace) || (!saved && !workspace))
         return CARVE_ERR_INVALID_ARG;
     carve::GdrArgs a{};

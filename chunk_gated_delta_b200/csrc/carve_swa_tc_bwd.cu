@@ -4,9 +4,9 @@
 // With lse and delta_i = sum_c dO_ic o_ic from the forward's results,
 //   p_ij = e^{scale q_i.k_j - lse_i},  ds_ij = p_ij (dO_i.v_j - delta_i)
 //   dv_j = sum_i p_ij dO_i,  dk_j = scale sum_i ds_ij q_i,  dq_i = scale sum_j ds_ij k_j
-// Two passes of one kernel (and, for few keys, one that joins the first's parts), so that every sum stays in one accumulator in a fixed order (one pass
-// with dq summed by atomics needs 5 products instead of 7, but its results would depend on the
-// order of arrival).  A unit holds 128 rows (KEYS: keys with dk, dv; else queries with dq) as two
+// Two passes of one kernel (and, for few keys, one that joins the first's parts), so that every sum
+// stays in one accumulator in a fixed order (one pass with dq summed by atomics needs 5 products
+// instead of 7, but its results would depend on the order of arrival).  A unit holds 128 rows (KEYS: keys with dk, dv; else queries with dq) as two
 // resident operand tiles R1, R2 and streams the other side in tiles C1, C2 of 64:
 //             R1   R2   C1   C2
 //   KEYS      k    v    q    dO     over the query heads of the key head
@@ -15,10 +15,14 @@
 //   P, dS                       two threads a row, 32 columns each; back to tensor memory as bf16 over S, dP
 //   acc1 += dS C1 (dk or dq),  acc2 += P C2 (dv)   A from tensor memory, C's rows contracted
 // Roles: warps 0-7 and 8-15 form P, dS of the even and odd column tiles, warp 16 copies, warp 18 takes what
-// has landed, warp 17 issues the products: S, dP of the tile after next go out while the other buffer is being worked on.
+// has landed, warp 17 issues the products: S, dP of the tile after next go out while the other buffer
+// is being worked on.
 // Persistent: a CTA walks its units with one set of running phases; R is given back with the unit's last
 // S and dP, so the next unit's rows load beside this one's last sums and epilogue.  Four column stages:
-// three tiles are held by what is being computed.
+// three tiles are held by what is being computed (a fifth changes nothing).  A tile of 128 x 64 takes
+// 1900 cycles: the tensor core 1280 (keys) or 1024 (queries), most of it at the rate at which shared memory
+// gives S and dP their operands, and the product warp's way from one tile to the next the rest.  8
+// sequences of 4096 tokens, 16 query and 4 key heads, d = 128, W = 1024: keys 780 us, queries 520 us.
 #include "carve_mixers.cuh"
 #include "carve_umma.cuh"
 
