@@ -19,7 +19,7 @@
 // warps 17 and 18 issue the products of a tile each.  Persistent: a unit's copies and first products run
 // beside the last one's outputs (the two took a fifth of a CTA's time at W = 1024, a quarter at 512).
 // Softmax bounds it: 2000 cycles for 64 keys of both tiles, of which the exponentials need 1024 and the
-// products 1280.  8 sequences of 4096 tokens, 16 query and 4 key heads, d = 128, W = 1024: 314 us, 730
+// products 1280.  8 sequences of 4096 tokens, 16 query and 4 key heads, d = 128, W = 1024: 314 us, 770
 // TFLOP/s of products; 4 of 2048, W = 512: 69 us.
 //
 // Blocks that a tile does not see are skipped; only blocks that a window edge or the diagonal
@@ -271,6 +271,15 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             asm volatile("bar.sync %0, 64;\n" ::"r"(1 + 4 * t + quarter) : "memory");
             return sm.part[nx++ & 1][t][1 - half][r];
         };
+        auto any_of_both = [&](bool x) {   // of the two warps' lanes
+            uint32_t y;
+            asm volatile(
+                "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 64, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+                : "=r"(y)
+                : "r"((uint32_t)x), "r"(1 + 4 * t + quarter)
+                : "memory");
+            return y != 0;
+        };
         for (int u = blockIdx.x; u < items; u += gridDim.x) {
             if (!w.set(a, u, paired)) continue;
             const int x2 = nu++ & 1, i = w.i0[t] + r;
@@ -308,9 +317,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 #pragma unroll
                 for (int x = 0; x < 32; x += 2) mx[x / 2 & 3] = max3(mx[x / 2 & 3], __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
                 float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                mb = fmaxf(mb, other(mb));
-                const bool grown = (mb - m) * sc > kLazy;   // of this row alone: a row's result depends on no other
-                if (__any_sync(0xffffffffu, grown)) {       // rare after the first block
+                if (any_of_both((mb - m) * sc > kLazy)) {       // rare after the first block
+                    mb = fmaxf(mb, other(mb));
+                    const bool grown = (mb - m) * sc > kLazy;   // of this row alone: a row's result depends on no other
                     const float m1 = grown ? mb : m, f = grown ? ex2((m - m1) * sc) : 1.f;
                     if (b > 0) {
                         ok = ok && wait(sm.ofull[t][(nb - 1) & 1], (nb - 1) / 2);
