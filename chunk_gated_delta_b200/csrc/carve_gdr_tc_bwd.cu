@@ -322,7 +322,7 @@ struct GradSmem {
     float vec[2][5][kC];                       // [stage]: e^G, e^{G_C - G}, w, G, e^{G_r - G}
     float dg[4][128], dw[kC], kb[4][kC], tot[3][128], col[4][kC], last[8];   // partial sums of a head
     uint64_t vfull[2], vfree[2], qkfull[2], qkfree[2], dfull, dfree, s0full, s0free, s1full, s1free, Dfull, Dfree, xfull,
-        xfree, yfull, yfree, pready, pfull, afree, gready, gfree, oready, drain;
+        xfree, yfull, yfree, pready, pfull, afree, gready, gfree, oready[2], drain;   // oready: [stage]
     uint32_t tmem;
 };
 
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
         for (uint64_t *b : {&sm.vfull[0], &sm.vfull[1], &sm.qkfull[0], &sm.qkfull[1], &sm.qkfree[0], &sm.qkfree[1], &sm.dfull,
                             &sm.dfree, &sm.s0full, &sm.s1full, &sm.Dfull, &sm.xfull, &sm.yfull, &sm.pfull, &sm.gfree, &sm.drain})
             mbar_init(b, 1);
-        for (uint64_t *b : {&sm.vfree[0], &sm.vfree[1], &sm.Dfree, &sm.xfree, &sm.pready, &sm.afree, &sm.gready, &sm.oready})
+        for (uint64_t *b : {&sm.vfree[0], &sm.vfree[1], &sm.Dfree, &sm.xfree, &sm.pready, &sm.afree, &sm.gready, &sm.oready[0], &sm.oready[1]})
             mbar_init(b, kRegWarps);
         for (uint64_t *b : {&sm.s0free, &sm.s1free}) mbar_init(b, kRegWarps / 2 + 1);   // readers and the products
         mbar_init(&sm.yfree, kRegWarps / 2);
@@ -684,7 +684,9 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
             long long row;
             if (!a.seq.find(tile, kC, n, c, row, len)) continue;
             row += (long long)c * kC;
-            if (!(ok = wait(sm.oready, it))) break;
+            // one barrier a stage: the register warps may finish the next item before this warp has seen this one, and
+            // the one after it only when this stage was given back
+            if (!(ok = wait(sm.oready[it & 1], it / 2))) break;
             if (elect_one()) {
                 if (len - c * kC >= kC)
                     for (int x = 0; x < KH; ++x) {
@@ -850,7 +852,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                 }
             }
             fence_proxy_async_smem();
-            mbar_arrive_warp(&sm.oready);
+            mbar_arrive_warp(&sm.oready[it & 1]);
             ++it;
         }
     }

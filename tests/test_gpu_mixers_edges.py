@@ -1,0 +1,54 @@
+"""Calls of the mixers of include/carve_mixers.h that stand at an edge: very many short sequences, no
+rows, other streams, tokens that reset a state.  Tolerances as in test_gpu_mixers.py, whose fp64
+comparisons hold the fp32 kernels to the definition."""
+import numpy as np
+import pytest
+import torch
+
+import chunk_gated_delta_b200 as carve
+from tests.test_gpu_mixers import TYPES, U, delta_inputs, ids, rel  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(autouse=True)
+def device_status(cuda_device):
+    yield
+    assert carve.carve_check() == 0
+
+
+def offsets(lens, device):
+    return torch.tensor(np.cumsum([0] + list(lens)), dtype=torch.int32, device=device)
+
+
+def delta_tensors(lead, Hk, Hv, dk, dv, seed, device):
+    """q, k, v, g_logit, w_logit, dO in bf16."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    r = lambda *s: torch.randn(*lead, *s, generator=g, device=device)  # noqa: E731
+    q, k = r(Hk, dk), r(Hk, dk)
+    q, k = q / q.norm(dim=-1, keepdim=True), k / k.norm(dim=-1, keepdim=True)
+    return [x.to(BF16) for x in (q, k, r(Hv, dv), 0.5 * r(Hv) - 3, r(Hv), r(Hv, dv))]
+
+
+def delta_both(x, cu=None, stream=None, **more):
+    out = carve.carve_gdr_fwd(*x[:5], cu_seqlens=cu, stream=stream, **more)
+    g = carve.carve_gdr_bwd(*x[:5], out["saved"], x[5], cu_seqlens=cu, stream=stream, **more)
+    return dict(o=out["o"], S=out["S_final"], **g)
+
+
+@pytest.mark.parametrize("Hk,Hv,dk,dv", [(1, 1, 64, 64), (2, 4, 128, 64)])
+def test_delta_gradients_of_very_many_short_sequences(cuda_device, Hk, Hv, dk, dv):
+    """Thousands of items of a tile or less, so that the warps of a gradient CTA drift apart by as much as
+    their hand-overs allow: the bf16 kernels against the fp32 ones, and bits from call to call."""
+    g = np.random.default_rng(5)
+    lens = g.integers(0, 70, 3000).tolist()
+    x, cu = delta_tensors((sum(lens),), Hk, Hv, dk, dv, 31, cuda_device), offsets(lens, cuda_device)
+    got, want = delta_both(x, cu), delta_both([y.float() for y in x], cu)
+    u = U[BF16]
+    for n, lim in dict(o=4 * u, S=3e-5, dq=4 * u, dk=8 * u, dv=4 * u, dg_logit=8 * u, dw_logit=8 * u, dS0=4 * u).items():
+        assert rel(got[n], want[n].double().cpu()) <= lim, (n, rel(got[n], want[n].double().cpu()))
+    for _ in range(3):
+        for n, y in delta_both(x, cu).items():
+            assert torch.equal(y, got[n]), n
