@@ -212,6 +212,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             bool s0 = sees(0), s1 = sees(1), some = false;   // of blocks b and b + 1; any P V yet
             dq = desc_at(dq0, (nu & 1) * (uint32_t)sizeof(sm.q[0]));
             ok = wait(sm.qfull[nu & 1], nu / 2);
+            // a tile without rows: nothing else of it waits for the queries, and they may be copied over only once
+            // this warp has seen them
+            if (ok && w.i0[t] >= w.i1[t]) {
+                if (elect_one()) mbar_arrive(&sm.qfree[nu & 1]);
+                __syncwarp();
+            }
             ++nu;
             if (ok) issue_s(s0);
             if (ok && w.blocks > 1) issue_s(s1);
@@ -397,10 +403,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 }
                 if (ok && a.lse && half == 0 && i < w.i1[t]) a.lse[at] = (m * sc + log2f(l)) * 0.6931471805599453f;
             }
-            // The tile's last S is done, its outputs have left.  (A tile without rows has waited for nothing: it
-            // waits here for its queries, so as not to run ahead of the other tile's turn.)
-            if (warp % 8 == 0) {
-                if (mine == 0) ok = ok && wait(sm.qfull[x2], (nu - 1) / 2);
+            // The tile's last S is done, its outputs have left.  (The queries of a tile without rows are given back by
+            // its product warp.)
+            if (warp % 8 == 0 && mine > 0) {
                 if (elect_one()) mbar_arrive(&sm.qfree[x2]);
                 __syncwarp();
             }

@@ -52,3 +52,25 @@ def test_delta_gradients_of_very_many_short_sequences(cuda_device, Hk, Hv, dk, d
     for _ in range(3):
         for n, y in delta_both(x, cu).items():
             assert torch.equal(y, got[n]), n
+
+
+def window_tensors(lead, Hq, Hkv, d, seed, device):
+    """q, k, v, dO in bf16."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return [torch.randn(*lead, h, d, generator=g, device=device).to(BF16) for h in (Hq, Hkv, Hkv, Hq)]
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(3, 3, 64), (3, 1, 128), (2, 1, 64)])
+def test_window_of_very_many_short_sequences(cuda_device, Hq, Hkv, d):
+    """Thousands of units of one key block, whose second query tile is empty where heads do not pair: the
+    query buffers pass from unit to unit as fast as they can.  bf16 against fp32 (3 u: see
+    test_window_over_many_tiles), and bits from call to call."""
+    lens = np.random.default_rng(6).integers(0, 70, 3000).tolist()
+    q, k, v, _ = window_tensors((sum(lens),), Hq, Hkv, d, 32, cuda_device)
+    at = dict(window=20, sinks=2, cu_seqlens=offsets(lens, cuda_device))
+    got, want = carve.carve_swa_fwd(q, k, v, **at), carve.carve_swa_fwd(q.float(), k.float(), v.float(), **at)
+    assert rel(got["o"], want["o"].double().cpu()) <= 3 * U[BF16]
+    assert (got["lse"] - want["lse"]).abs().max() <= 1e-4
+    for _ in range(10):
+        again = carve.carve_swa_fwd(q, k, v, **at)
+        assert torch.equal(again["o"], got["o"]) and torch.equal(again["lse"], got["lse"])
