@@ -188,8 +188,9 @@ __device__ __forceinline__ void store_row(float *dst, const float *S) {
 // outputs touch nothing that the last kernel reads.
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 __device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+// `early` false: an ordinary launch, after everything before it (where that is not a kernel of the same call)
 template <class... P, class... A>
-cudaError_t launch_after(void (*kern)(P...), unsigned grid, unsigned block, int smem, cudaStream_t st, A... args) {
+cudaError_t launch_after(bool early, void (*kern)(P...), unsigned grid, unsigned block, int smem, cudaStream_t st, A... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(block);
@@ -199,7 +200,7 @@ cudaError_t launch_after(void (*kern)(P...), unsigned grid, unsigned block, int 
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = early ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 

@@ -883,7 +883,7 @@ cudaError_t bwd_t(const GdrArgs &a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     sweep<<<a.seq.N * a.Hv, kSweepThreads, sb, st>>>(a, mq, mk, md, mdv);
     const long long tiles = a.seq.n_tiles(kC), items = tiles * a.Hk;
-    if (items) e = launch_after(grad, (unsigned)(items < sm_count() ? items : sm_count()), kSweepThreads, gb, st, a, mq, mk, md, mdq, mdk);
+    if (items) e = launch_after(true, grad, (unsigned)(items < sm_count() ? items : sm_count()), kSweepThreads, gb, st, a, mq, mk, md, mdq, mdk);
     if (e != cudaSuccess) return e;
     if (a.dA_dec || a.dtau)
         launch_gdr_reduce_decay(reinterpret_cast<const float *>(a.ws + (size_t)tiles * a.Hv * sizeof(GdrKeep<K, V>)), tiles, a.Hv,

@@ -594,12 +594,13 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
 
 template <int K, int V, bool SAVE>
 cudaError_t sweep_t(const GdrArgs &a, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const CUtensorMap &mo,
-                    cudaStream_t st) {
+                    bool prepared, cudaStream_t st) {
     auto kern = gdr_tc_sweep<K, V, SAVE>;
     const int bytes = (int)sizeof(SweepSmem<K, V, SAVE>) + 1024;
     const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), bytes);
     if (e != cudaSuccess) return e;
-    return launch_after(kern, (unsigned)(a.seq.N * a.Hv), kSweepThreads, bytes, st, a, mq, mk, mv, mo);
+    // beside the preparation, an ordinary launch, so that the states and offsets are there; without one, after all
+    return launch_after(prepared, kern, (unsigned)(a.seq.N * a.Hv), kSweepThreads, bytes, st, a, mq, mk, mv, mo);
 }
 
 template <int K, int V>
@@ -617,7 +618,7 @@ cudaError_t fwd_t(const GdrArgs &a, bool save, cudaStream_t st) {
         if (e != cudaSuccess) return e;
         prep<<<(unsigned)(a.seq.n_tiles(kC) * a.Hk), 128, bytes, st>>>(a, mq, mk);
     }
-    return save ? sweep_t<K, V, true>(a, mq, mk, mv, mo, st) : sweep_t<K, V, false>(a, mq, mk, mv, mo, st);
+    return save ? sweep_t<K, V, true>(a, mq, mk, mv, mo, rows > 0, st) : sweep_t<K, V, false>(a, mq, mk, mv, mo, rows > 0, st);
 }
 
 }  // namespace

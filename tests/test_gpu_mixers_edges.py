@@ -74,3 +74,19 @@ def test_window_of_very_many_short_sequences(cuda_device, Hq, Hkv, d):
     for _ in range(10):
         again = carve.carve_swa_fwd(q, k, v, **at)
         assert torch.equal(again["o"], got["o"]) and torch.equal(again["lse"], got["lse"])
+
+
+def test_states_pass_through_calls_without_rows_in_order(cuda_device):
+    """Calls without tokens hand the state on, each after what the stream holds before it: a backward, a
+    forward that starts from its dS0, and a forward in place, on states that change from turn to turn."""
+    z = lambda *s: torch.zeros(*s, device=cuda_device, dtype=BF16)  # noqa: E731
+    x = (z(40, 0, 8, 128), z(40, 0, 8, 128), z(40, 0, 8, 128), z(40, 0, 8), z(40, 0, 8))
+    saved = carve.carve_gdr_fwd(*x)["saved"]
+    state = torch.zeros(40, 8, 128, 128, device=cuda_device)
+    mid, last = torch.empty_like(state), torch.empty_like(state)
+    for i in range(1, 40):
+        state += 1.0
+        carve.carve_gdr_bwd(*x, saved, x[2], dS_final=state, out=dict(dS0=mid))
+        carve.carve_gdr_fwd(*x, S0=mid, out=dict(S_final=last, saved=saved))
+        carve.carve_gdr_fwd(*x, S0=last, out=dict(S_final=last, saved=saved))
+        assert torch.equal(last, torch.full_like(last, float(i))), i
