@@ -428,9 +428,11 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
     const int items = (int)a.seq.n_tiles(kC) * a.Hk;   // below 2^28
     int it = 0, j = 0;   // items and heads so far (those of used tiles)
 
+    // The sweep, by every warp: a long sequence may keep it busy for seconds after this CTA has started, beyond
+    // what the waits below allow for
+    wait_for_last();
     if (warp >= kRegWarps) regs_down<64>();
     if (warp == kRegWarps) {
-        wait_for_last();   // the sweep
 #pragma unroll 1
         for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
             const int tile = w / a.Hk, hk = w - tile * a.Hk;

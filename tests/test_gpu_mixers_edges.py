@@ -90,3 +90,14 @@ def test_states_pass_through_calls_without_rows_in_order(cuda_device):
         carve.carve_gdr_fwd(*x, S0=mid, out=dict(S_final=last, saved=saved))
         carve.carve_gdr_fwd(*x, S0=last, out=dict(S_final=last, saved=saved))
         assert torch.equal(last, torch.full_like(last, float(i))), i
+
+
+def test_delta_gradients_wait_for_the_longest_sequence(cuda_device):
+    """One sequence of 60 thousand tokens beside short ones: the gradients' kernel starts on the SMs that the
+    short ones leave and waits there (for 3 ms; its bounded waits begin behind that)."""
+    lens = [3, 60000, 5, 64, 1]
+    x, cu = delta_tensors((sum(lens),), 1, 1, 64, 64, 33, cuda_device), offsets(lens, cuda_device)
+    got, want = delta_both(x, cu), delta_both([y.float() for y in x], cu)
+    u = U[BF16]
+    for n, lim in dict(o=4 * u, S=3e-5, dq=4 * u, dk=8 * u, dv=4 * u, dg_logit=8 * u, dw_logit=8 * u, dS0=4 * u).items():
+        assert rel(got[n], want[n].double().cpu()) <= lim, (n, rel(got[n], want[n].double().cpu()))
