@@ -146,11 +146,15 @@ void raise(const char *fn, int rc) {
     throw py::error_already_set();
 }
 
-// The device of `like` current, and a stream of it: the caller's or its current one.
+// The device of `like` and the stream of the call current: the caller's stream or the device's current one.  Stands
+// before the call's allocations, so that what it allocates belongs to the stream that uses it (as within
+// torch.cuda.stream): scratch is released when the call returns, and the memory may then serve other
+// streams only behind this one's work.
 struct On {
-    c10::cuda::CUDAGuard guard;
+    c10::cuda::CUDAGuard device;
+    c10::cuda::OptionalCUDAStreamGuard current;
     void *stream;
-    On(const Tensor &like, const py::object &s) : guard(like.device()) {
+    On(const Tensor &like, const py::object &s) : device(like.device()) {
         if (s.is_none()) {
             stream = c10::cuda::getCurrentCUDAStream(like.device().index()).stream();
             return;
@@ -162,6 +166,7 @@ struct On {
             throw py::value_error(o.str());
         }
         stream = reinterpret_cast<void *>(s.attr("cuda_stream").cast<uintptr_t>());
+        current.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), d.index()));
     }
 };
 
@@ -234,6 +239,7 @@ py::dict gdr_fwd(const Tensor &q, const Tensor &k, const Tensor &v, const Tensor
     const int io = io_of(q);
     const Gdr c(q, k, v, g, w, A_dec, tau, cu, io);
     const bool packed = c.lead.packed;
+    const On on(q, stream);
     py::dict out = copy_of(out_);
     const Tensor o = result(out, "o", v.sizes(), v.options());
     const Tensor S = result(out, "S_final", c.state, v.options().dtype(at::kFloat));
@@ -247,7 +253,6 @@ py::dict gdr_fwd(const Tensor &q, const Tensor &k, const Tensor &v, const Tensor
     }
     if (!save || ws_)
         ws = buffer("workspace", ws_, "carve_gdr_fwd_workspace_bytes", carve_gdr_fwd_workspace_bytes(&c.d, packed), q);
-    const On on(q, stream);
     raise("carve_gdr_fwd", carve_gdr_fwd(&c.d, as<int32_t>(cu), ptr(q), ptr(k), ptr(v), ptr(g), ptr(w), as<float>(A_dec),
                                          as<float>(tau), as<float>(S0), ptr(o), as<float>(S), ptr(saved), ptr(ws), on.stream));
     return out;
@@ -259,6 +264,7 @@ py::dict gdr_bwd(const Tensor &q, const Tensor &k, const Tensor &v, const Tensor
     const int io = io_of(q);
     const Gdr c(q, k, v, g, w, A_dec, tau, cu, io);
     const bool packed = c.lead.packed;
+    const On on(q, stream);
     const auto f32 = v.options().dtype(at::kFloat);
     py::dict out = copy_of(out_);
     auto grad = [&](const char *key, at::IntArrayRef shape, const at::TensorOptions &opt) {
@@ -277,7 +283,6 @@ py::dict gdr_bwd(const Tensor &q, const Tensor &k, const Tensor &v, const Tensor
     if (tau) dt = grad("dtau", {c.d.Hv}, f32);
     buffer("saved", saved, "carve_gdr_saved_bytes", carve_gdr_saved_bytes(&c.d, packed), q);
     const Tensor ws = buffer("workspace", ws_, "carve_gdr_bwd_workspace_bytes", carve_gdr_bwd_workspace_bytes(&c.d, packed), q);
-    const On on(q, stream);
     raise("carve_gdr_bwd",
           carve_gdr_bwd(&c.d, as<int32_t>(cu), ptr(q), ptr(k), ptr(v), ptr(g), ptr(w), as<float>(A_dec), as<float>(tau), ptr(saved),
                         ptr(dO), as<float>(dS), ptr(dq), ptr(dk), ptr(dv), ptr(dg), ptr(dw), as<float>(dA), as<float>(dt),
@@ -303,9 +308,9 @@ Tensor gdr_step(const Tensor &q, const Tensor &k, const Tensor &v, const Tensor 
     want(q, "tau", tau, {Hv}, at::kFloat);
     want(q, "o", o_, v.sizes(), dt);
     want_cuda(q);
+    const On on(q, stream);
     const Tensor o = o_ ? *o_ : at::empty(v.sizes(), v.options());
     const carve_gdr_dims d{small(B), 1, small(Hk), small(Hv), small(dk), small(dv), io, 0};
-    const On on(q, stream);
     raise("carve_gdr_step", carve_gdr_step(&d, ptr(q), ptr(k), ptr(v), ptr(g), ptr(w), as<float>(A_dec), as<float>(tau), as<float>(S),
                                            ptr(o), on.stream));
     return o;
@@ -347,6 +352,7 @@ py::dict swa_fwd(const Tensor &q, const Tensor &k, const Tensor &v, int64_t wind
     want_window(window, sinks);
     const int io = io_of(q);
     const Swa c(q, k, v, window, sinks, scale, cu, io);
+    const On on(q, stream);
     py::dict out = copy_of(out_);
     const Tensor o = result(out, "o", q.sizes(), q.options());
     Opt lse = given(out, "lse");
@@ -357,7 +363,6 @@ py::dict swa_fwd(const Tensor &q, const Tensor &k, const Tensor &v, int64_t wind
     }
     want(q, "o", o, q.sizes(), c.dt);
     want(q, "lse", lse, rows, at::kFloat);
-    const On on(q, stream);
     raise("carve_swa_fwd", carve_swa_fwd(&c.d, as<int32_t>(cu), ptr(q), ptr(k), ptr(v), ptr(o), want_lse ? as<float>(lse) : nullptr,
                                          on.stream));
     return out;
@@ -369,6 +374,7 @@ py::dict swa_bwd(const Tensor &q, const Tensor &k, const Tensor &v, const Tensor
     want_window(window, sinks);
     const int io = io_of(q);
     const Swa c(q, k, v, window, sinks, scale, cu, io);
+    const On on(q, stream);
     py::dict out = copy_of(out_);
     const Tensor dq = result(out, "dq", q.sizes(), q.options()), dk = result(out, "dk", k.sizes(), k.options()),
                  dv = result(out, "dv", v.sizes(), v.options());
@@ -380,7 +386,6 @@ py::dict swa_bwd(const Tensor &q, const Tensor &k, const Tensor &v, const Tensor
     want(q, "dv", dv, k.sizes(), c.dt);
     const Tensor ws =
         buffer("workspace", ws_, "carve_swa_bwd_workspace_bytes", carve_swa_bwd_workspace_bytes(&c.d, c.lead.packed), q);
-    const On on(q, stream);
     raise("carve_swa_bwd", carve_swa_bwd(&c.d, as<int32_t>(cu), ptr(q), ptr(k), ptr(v), ptr(o), as<float>(lse), ptr(dO), ptr(dq),
                                          ptr(dk), ptr(dv), ptr(ws), on.stream));
     return out;
@@ -391,10 +396,10 @@ void swa_fill(const Tensor &k, const Tensor &v, const Tensor &kc, const Tensor &
     want_window(window, sinks);
     const int io = io_of(k);
     const Swa c(k, k, v, window, sinks, 1.0, cu, io);
+    const On on(k, stream);
     const at::DimVector slots = {c.d.B, sinks + window, c.d.Hkv, c.d.d};
     want(k, "k_cache", kc, slots, c.dt);
     want(k, "v_cache", vc, slots, c.dt);
-    const On on(k, stream);
     raise("carve_swa_fill", carve_swa_fill(&c.d, as<int32_t>(cu), ptr(k), ptr(v), ptr(kc), ptr(vc), on.stream));
 }
 
@@ -415,9 +420,9 @@ Tensor swa_step(const Tensor &q, const Tensor &k, const Tensor &v, const Tensor 
     want(q, "k_cache", kc, {B, sinks + window, Hkv, D}, dt);
     want(q, "v_cache", vc, {B, sinks + window, Hkv, D}, dt);
     want_cuda(q);
+    const On on(q, stream);
     const Tensor o = o_ ? *o_ : at::empty(q.sizes(), q.options());
     const carve_swa_dims d{small(B), 1, small(Hq), small(Hkv), small(D), (int)window, (int)sinks, io, scale_of(scale, D), 0};
-    const On on(q, stream);
     raise("carve_swa_step", carve_swa_step(&d, ptr(q), ptr(k), ptr(v), ptr(kc), ptr(vc), as<int64_t>(pos), ptr(o), on.stream));
     return o;
 }

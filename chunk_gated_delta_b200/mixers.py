@@ -4,8 +4,10 @@ sliding-window attention with sink tokens (carve_swa_*).
 Argument checks and marshalling only, as in the package's other calls; here they are in C++
 (csrc/carve_bind.cpp, _carve_bind.so), since a decoding step's kernel is shorter than they were in
 Python.  Tensors are contiguous, on one CUDA device (which need not be the current one) and
-launched on that device's current stream, or on `stream`.  What does not fit raises TypeError (a
-dtype) or ValueError; what the library refuses, CarveError.
+launched on that device's current stream, or on `stream`.  What a call allocates (results, scratch)
+belongs to the stream that it is launched on, as within `torch.cuda.stream(stream)`; inputs and
+buffers that the caller brings from another stream are the caller's to order.  What does not fit
+raises TypeError (a dtype) or ValueError; what the library refuses, CarveError.
 
     out  = carve.carve_gdr_fwd(q, k, v, g_logit, w_logit)
     g    = carve.carve_gdr_bwd(q, k, v, g_logit, w_logit, out["saved"], dO)

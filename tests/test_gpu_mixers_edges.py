@@ -101,3 +101,70 @@ def test_delta_gradients_wait_for_the_longest_sequence(cuda_device):
     u = U[BF16]
     for n, lim in dict(o=4 * u, S=3e-5, dq=4 * u, dk=8 * u, dv=4 * u, dg_logit=8 * u, dw_logit=8 * u, dS0=4 * u).items():
         assert rel(got[n], want[n].double().cpu()) <= lim, (n, rel(got[n], want[n].double().cpu()))
+
+
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+def test_scratch_belongs_to_the_stream_of_the_call(cuda_device, dt):
+    """Calls on `stream=`, made from the default stream, whose scratch the binding allocates: two at once, and
+    memory of the scratch's size that the default stream takes and writes as soon as each call is back."""
+    def inputs(seed):
+        return ([y.to(dt) for y in delta_tensors((2, 1500), 2, 4, 128, 128, seed, cuda_device)],
+                [y.to(dt) for y in window_tensors((1, 1500), 4, 2, 128, seed, cuda_device)])
+
+    def prompt(x, y, kept, stream):
+        out = carve.carve_gdr_fwd(*x[:5], save_for_bwd=False, stream=stream)
+        return [out["o"], out["S_final"]]
+
+    def delta(x, y, kept, stream):
+        return list(carve.carve_gdr_bwd(*x[:5], kept["saved"], x[5], stream=stream).values())
+
+    def window(x, y, kept, stream):
+        return list(carve.carve_swa_bwd(*y[:3], kept["o"], kept["lse"], y[3], window=300, sinks=4, stream=stream).values())
+
+    xs = [inputs(s) for s in (41, 42)]
+    kept = [dict(carve.carve_swa_fwd(*y[:3], window=300, sinks=4), saved=carve.carve_gdr_fwd(*x[:5])["saved"]) for x, y in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    for f in (prompt, delta, window):
+        alone = [f(*x, kp, None) for x, kp in zip(xs, kept)]
+        torch.cuda.synchronize()
+        for _ in range(4):
+            got, junk = [], []
+            for x, kp, s in zip(xs, kept, streams):
+                got.append(f(*x, kp, s))
+                junk += [torch.full((n,), float("nan"), device=cuda_device) for n in (1 << 16, 1 << 19, 1 << 20, 1 << 21, 1 << 22)]
+            torch.cuda.synchronize()
+            for a, b in zip(alone, got):
+                assert all(torch.equal(y, z) for y, z in zip(a, b)), f.__name__
+
+
+def test_results_belong_to_the_stream_of_the_call(cuda_device):
+    """A result's memory returns to the stream that wrote it: what the default stream allocates after the call
+    and its result are gone is other memory."""
+    x = delta_tensors((1, 3000), 2, 2, 128, 128, 43, cuda_device)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    at = carve.carve_gdr_fwd(*x[:5], save_for_bwd=False, stream=side)["o"].data_ptr()
+    size = x[2].numel()
+    mine = [torch.empty(size, dtype=BF16, device=cuda_device) for _ in range(8)]
+    assert at not in [y.data_ptr() for y in mine]
+    with torch.cuda.stream(side):
+        assert at in [torch.empty(size, dtype=BF16, device=cuda_device).data_ptr()]
+    torch.cuda.synchronize()
+
+
+def test_streams_that_do_not_fit_are_refused(cuda_device):
+    x = delta_tensors((1, 70), 2, 2, 64, 64, 44, cuda_device)
+
+    class Elsewhere:
+        device, cuda_stream = torch.device("cuda", 1), 0
+
+    with pytest.raises(ValueError, match="the stream is on"):
+        carve.carve_gdr_fwd(*x[:5], stream=Elsewhere())
+    handle = torch.cuda.Stream()
+    ext = torch.cuda.ExternalStream(handle.cuda_stream)
+    want = carve.carve_gdr_fwd(*x[:5])["o"]
+    for s in (handle, ext, torch.cuda.default_stream()):
+        torch.cuda.synchronize()
+        o = carve.carve_gdr_fwd(*x[:5], stream=s)["o"]
+        torch.cuda.synchronize()
+        assert torch.equal(o, want) and torch.cuda.current_stream() == torch.cuda.default_stream()
