@@ -15,6 +15,7 @@ _bwd / _fill / _step, sliding-window attention with sink tokens.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -96,6 +97,18 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _on(stream, device):
+    """The context in which a call allocates: its memory belongs to the stream that it is launched on, so
+    that scratch which is released when the call returns serves no other stream meanwhile."""
+    torch = _torch()
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream.cuda_stream
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
 def _io_of(x):
     torch = _torch()
     if x.dtype == torch.float32:
@@ -175,17 +188,18 @@ def _fwd(d, pk, q, k, v, g_logit, bx, w_logit, A, B, S0, m_prev_in, save_for_bwd
     lib = load()
     out = dict(out or {})
     dev = q.device
-    if "o" not in out:
-        out["o"] = torch.empty(v.shape, dtype=q.dtype, device=dev)
-    if "S_final" not in out:
-        out["S_final"] = torch.empty((d.B, d.H, d.dv, d.dk), dtype=torch.float32, device=dev)
-    if "m_prev_out" not in out:
-        out["m_prev_out"] = torch.empty((d.B, d.H, d.dv), dtype=torch.float32, device=dev)
-    if save_for_bwd and out.get("saved") is None:
-        n = saved_bytes(d)
-        if n == 0:
-            raise CarveError("carve_saved_bytes", 1)
-        out["saved"] = torch.empty(n, dtype=torch.uint8, device=dev)
+    with _on(stream, dev):
+        if "o" not in out:
+            out["o"] = torch.empty(v.shape, dtype=q.dtype, device=dev)
+        if "S_final" not in out:
+            out["S_final"] = torch.empty((d.B, d.H, d.dv, d.dk), dtype=torch.float32, device=dev)
+        if "m_prev_out" not in out:
+            out["m_prev_out"] = torch.empty((d.B, d.H, d.dv), dtype=torch.float32, device=dev)
+        if save_for_bwd and out.get("saved") is None:
+            n = saved_bytes(d)
+            if n == 0:
+                raise CarveError("carve_saved_bytes", 1)
+            out["saved"] = torch.empty(n, dtype=torch.uint8, device=dev)
     fn = lib.carve_fwd if pk is None else lib.carve_fwd_varlen
     rc = fn(ctypes.byref(d), *(pk or []), _ptr(q), _ptr(k), _ptr(v), _ptr(g_logit), _ptr(bx), _ptr(w_logit),
             _ptr(A), _ptr(B), _ptr(Aw), _ptr(A_dec), _ptr(tau), _ptr(S0), _ptr(m_prev_in), _ptr(out["o"]),
@@ -230,11 +244,12 @@ def _bwd(d, pk, q, k, v, g_logit, bx, w_logit, A, B, saved, dO, S0, m_prev_in, d
     for name, x in (("dAw", Aw), ("dA_dec", A_dec), ("dtau", tau)):
         if x is not None:
             shapes[name] = (x.shape, torch.float32)
-    for key, (shp, dt) in shapes.items():
-        if key not in out:
-            out[key] = torch.empty(shp, dtype=dt, device=dev)
-    if workspace is None:
-        workspace = torch.empty(bwd_workspace_bytes(d), dtype=torch.uint8, device=dev)
+    with _on(stream, dev):
+        for key, (shp, dt) in shapes.items():
+            if key not in out:
+                out[key] = torch.empty(shp, dtype=dt, device=dev)
+        if workspace is None:
+            workspace = torch.empty(bwd_workspace_bytes(d), dtype=torch.uint8, device=dev)
     fn = lib.carve_bwd if pk is None else lib.carve_bwd_varlen
     rc = fn(ctypes.byref(d), *(pk or []), _ptr(q), _ptr(k), _ptr(v), _ptr(g_logit), _ptr(bx), _ptr(w_logit), _ptr(A),
             _ptr(B), _ptr(Aw), _ptr(A_dec), _ptr(tau), _ptr(S0), _ptr(m_prev_in), _ptr(saved), _ptr(dO),
@@ -258,7 +273,8 @@ def carve_step(q, k, v, g_logit, bx, w_logit, A, B, S, mc_mode: int = 0, chunk: 
     Bn, H, K = q.shape
     d = Dims(Bn, H, 1, K, v.shape[-1], A.shape[-1], chunk, _io_of(q), mc_mode)
     if o is None:
-        o = torch.empty((Bn, H, d.dv), dtype=q.dtype, device=q.device)
+        with _on(stream, q.device):
+            o = torch.empty((Bn, H, d.dv), dtype=q.dtype, device=q.device)
     rc = lib.carve_step(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(g_logit), _ptr(bx), _ptr(w_logit), _ptr(A),
                         _ptr(B), _ptr(Aw), _ptr(A_dec), _ptr(tau), _ptr(S), _ptr(mstate), _ptr(pos), _ptr(o),
                         _stream(stream))

@@ -168,3 +168,30 @@ def test_streams_that_do_not_fit_are_refused(cuda_device):
         o = carve.carve_gdr_fwd(*x[:5], stream=s)["o"]
         torch.cuda.synchronize()
         assert torch.equal(o, want) and torch.cuda.current_stream() == torch.cuda.default_stream()
+
+
+def test_recurrence_scratch_belongs_to_the_stream_of_the_call(cuda_device):
+    """The same of carve_fwd and carve_bwd, which this file's mixers stand beside."""
+    def inputs(seed):
+        q, k, v, gl, wl, dO = delta_tensors((2, 1024), 4, 4, 128, 128, seed, cuda_device)
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        r = lambda *s: torch.randn(*s, generator=g, device=cuda_device)  # noqa: E731
+        return (q, k, v, 0.5 * r(2, 1024, 4, 128) - 3, r(2, 1024, 4, 128), wl.float(), 0.02 * r(4, 128, 8), 0.02 * r(4, 8, 128)), dO
+
+    def run(x, dO, stream):
+        out = carve.carve_fwd(*x, chunk=64, stream=stream)
+        return [out["o"], out["S_final"], *carve.carve_bwd(*x, out["saved"], dO, chunk=64, stream=stream).values()]
+
+    xs = [inputs(s) for s in (51, 52)]
+    alone = [run(*x, None) for x in xs]
+    assert all(torch.equal(y, z) for y, z in zip(alone[0], run(*xs[0], None)))   # deterministic
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    for _ in range(4):
+        got, junk = [], []
+        for x, s in zip(xs, streams):
+            got.append(run(*x, s))
+            junk += [torch.full((n,), float("nan"), device=cuda_device) for n in (1 << 16, 1 << 19, 1 << 20, 1 << 21, 1 << 22)]
+        torch.cuda.synchronize()
+        for a, b in zip(alone, got):
+            assert all(torch.equal(y, z) for y, z in zip(a, b))
