@@ -21,8 +21,9 @@ int tc_fwd_take_bad_seqlens();
 int tc_bwd_take_bad_seqlens();
 int gdr_take_bad_seqlens();
 int swa_take_bad_seqlens();
-int swa_fwd_take_timeout();
-int swa_bwd_take_timeout();
+int swa_fwd_take_status();   // bit 0: timeout, bit 1: bad offsets
+int swa_bwd_take_status();
+int swa_fill_take_bad_seqlens();
 int gdr_tc_fwd_take_timeout();
 int gdr_tc_bwd_take_timeout();
 int gdr_tc_fwd_take_bad_seqlens();
@@ -310,12 +311,12 @@ carve_status carve_step(const carve_dims *d, const void *q, const void *k, const
 
 carve_status carve_check(void *stream) {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return CARVE_ERR_CUDA;
-    const int t = carve::tc_fwd_take_timeout() | carve::tc_bwd_take_timeout() | carve::step_take_timeout() |
-                  carve::swa_fwd_take_timeout() | carve::swa_bwd_take_timeout() |
+    const int window = carve::swa_fwd_take_status() | carve::swa_bwd_take_status();
+    const int t = (window & 1) | carve::tc_fwd_take_timeout() | carve::tc_bwd_take_timeout() | carve::step_take_timeout() |
                   carve::gdr_tc_fwd_take_timeout() | carve::gdr_tc_bwd_take_timeout();
     const int bad = carve::simt_take_bad_seqlens() | carve::tc_fwd_take_bad_seqlens() | carve::tc_bwd_take_bad_seqlens() |
-                    carve::gdr_take_bad_seqlens() | carve::swa_take_bad_seqlens() | carve::gdr_tc_fwd_take_bad_seqlens() |
-                    carve::gdr_tc_bwd_take_bad_seqlens();
+                    (window & 2) | carve::swa_fill_take_bad_seqlens() | carve::gdr_take_bad_seqlens() |
+                    carve::swa_take_bad_seqlens() | carve::gdr_tc_fwd_take_bad_seqlens() | carve::gdr_tc_bwd_take_bad_seqlens();
     return t ? CARVE_ERR_TIMEOUT : bad ? CARVE_ERR_INVALID_ARG : CARVE_OK;
 }
 

@@ -14,7 +14,7 @@ struct Seqs {
 
     // rows [row0, row0 + len) of sequence n; a packed sequence that leaves [0, total] is empty
     // and *bad (when given) records it
-    __device__ __forceinline__ void rows(int n, long long &row0, int &len, int *bad = nullptr) const {
+    __device__ __forceinline__ void rows(int n, long long &row0, int &len, int *bad = nullptr, int mark = 1) const {
         if (!cu) {
             row0 = (long long)n * T;
             len = T;
@@ -26,7 +26,7 @@ struct Seqs {
         if (c0 < 0 || c1 < c0 || (long long)c1 > total) {
             row0 = 0;
             len = 0;
-            if (bad) atomicOr(bad, 1);
+            if (bad) atomicOr(bad, mark);
         }
     }
 
@@ -65,12 +65,15 @@ struct Seqs {
 };
 
 // Threads of one CTA together: records packed sequences whose offsets are out of range.
-__device__ __forceinline__ void check_seqs(const Seqs &s, int *bad) {
+__device__ __forceinline__ void check_seqs(const Seqs &s, int *bad, int mark = 1) {
     if (!s.cu) return;
     long long r;
     int len;
-    for (int n = threadIdx.x; n < s.N; n += blockDim.x) s.rows(n, r, len, bad);
+    for (int n = threadIdx.x; n < s.N; n += blockDim.x) s.rows(n, r, len, bad, mark);
 }
+// A kernel's status word for carve_check: bits of what happened.
+constexpr int kTimedOut = 1;     // a bounded wait gave up (never expected)
+constexpr int kBadOffsets = 2;   // a packed sequence's offsets are out of range
 
 struct GdrArgs {
     Seqs seq;
@@ -156,8 +159,10 @@ cudaError_t launch_swa_bwd_simt(const SwaArgs &a, cudaStream_t st);
 cudaError_t launch_swa_fwd_tc(const SwaArgs &a, cudaStream_t st);
 cudaError_t launch_swa_bwd_tc(const SwaArgs &a, cudaStream_t st);
 int swa_bwd_parts(const SwaArgs &a);
-int swa_fwd_take_timeout();
-int swa_bwd_take_timeout();
+int swa_fwd_take_status();
+int swa_bwd_take_status();
+int swa_fill_take_bad_seqlens();
+cudaError_t launch_swa_check(const Seqs &s, cudaStream_t st);   // the offsets alone (no rows)
 cudaError_t launch_swa_fill(bool bf16, const SwaArgs &a, cudaStream_t st);
 cudaError_t launch_swa_step(bool bf16, const SwaArgs &a, cudaStream_t st);
 int gdr_take_bad_seqlens();

@@ -84,6 +84,9 @@ carve::SwaArgs swa_args(const carve_swa_dims *d, const int32_t *cu) {
     return a;
 }
 
+// a call without rows: packed offsets are looked at all the same
+carve_status no_rows(const carve::Seqs &s, cudaStream_t st) { return s.cu ? status(carve::launch_swa_check(s, st)) : CARVE_OK; }
+
 // the backward's scratch: two floats a row and head (the CUDA-core path uses one), and the partial
 // dk, dv where the keys' pass is split
 int swa_parts(const carve_swa_dims *d, const carve::SwaArgs &a) { return d->io == CARVE_IO_BF16 ? carve::swa_bwd_parts(a) : 1; }
@@ -196,7 +199,7 @@ carve_status carve_swa_fwd(const carve_swa_dims *d, const int32_t *cu_seqlens, c
     carve::SwaArgs a = swa_args(d, cu_seqlens);
     a.q = q; a.k = k; a.v = v; a.o = o; a.lse = lse;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    if (rows == 0) return CARVE_OK;
+    if (rows == 0) return no_rows(a.seq, cs);
     return status(d->io == CARVE_IO_BF16 ? carve::launch_swa_fwd_tc(a, cs) : carve::launch_swa_fwd_simt(a, cs));
 }
 
@@ -219,8 +222,8 @@ carve_status carve_swa_bwd(const carve_swa_dims *d, const int32_t *cu_seqlens, c
         !ok_elem(lse, 4, rows) || !ok_ptr(dO, rows) || !ok_ptr(dq, rows) || !ok_ptr(dk, rows) || !ok_ptr(dv, rows) ||
         !ok_ptr(workspace))
         return CARVE_ERR_INVALID_ARG;
-    if (rows == 0) return CARVE_OK;
     carve::SwaArgs a = swa_args(d, cu_seqlens);
+    if (rows == 0) return no_rows(a.seq, static_cast<cudaStream_t>(stream));
     a.q = q; a.k = k; a.v = v; a.o = const_cast<void *>(o); a.lse = const_cast<float *>(lse);
     a.dO = dO; a.dq = dq; a.dk = dk; a.dv = dv; a.delta = static_cast<float *>(workspace);
     a.parts = swa_parts(d, a);
@@ -238,8 +241,8 @@ carve_status carve_swa_fill(const carve_swa_dims *d, const int32_t *cu_seqlens, 
     const long long rows = rows_of(d, packed);
     if (!ok_elem_opt(cu_seqlens) || !ok_ptr(k, rows) || !ok_ptr(v, rows) || !ok_ptr(k_cache) || !ok_ptr(v_cache))
         return CARVE_ERR_INVALID_ARG;
-    if (rows == 0) return CARVE_OK;
     carve::SwaArgs a = swa_args(d, cu_seqlens);
+    if (rows == 0) return no_rows(a.seq, static_cast<cudaStream_t>(stream));
     a.k = k; a.v = v; a.k_cache = k_cache; a.v_cache = v_cache;
     return status(carve::launch_swa_fill(d->io == CARVE_IO_BF16, a, static_cast<cudaStream_t>(stream)));
 }

@@ -89,6 +89,8 @@ __device__ __forceinline__ void store_rows(void *dst, const float4 (&acc)[D / 64
             *reinterpret_cast<float4 *>(static_cast<float *>(dst) + ((size_t)(row0 + ty) * H + h) * D + x + 64 * j) = acc[j];
 }
 
+__global__ void __launch_bounds__(NT) swa_check(Seqs s) { check_seqs(s, &g_swa_bad_seqlens); }
+
 enum Mode { FWD, DQ, DKV };
 
 // One CTA: BR rows of one (sequence, head), resident, and the tiles of the other side that they see (DKV:
@@ -238,6 +240,10 @@ cudaError_t bwd_t(const SwaArgs &a, cudaStream_t st) {
 
 }  // namespace
 
+cudaError_t launch_swa_check(const Seqs &s, cudaStream_t st) {
+    swa_check<<<1, NT, 0, st>>>(s);
+    return cudaGetLastError();
+}
 cudaError_t launch_swa_fwd_simt(const SwaArgs &a, cudaStream_t st) {
     return a.d == 64 ? launch<64, FWD>(a, st) : launch<128, FWD>(a, st);
 }

@@ -17,6 +17,19 @@
 #include "carve_mma.cuh"
 
 namespace carve {
+
+__device__ int g_swa_fill_bad_seqlens;   // set when a packed sequence's offsets are out of range
+
+int swa_fill_take_bad_seqlens() {
+    int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_swa_fill_bad_seqlens, sizeof(int)) != cudaSuccess) return 0;
+    if (v) {
+        const int z = 0;
+        cudaMemcpyToSymbol(g_swa_fill_bad_seqlens, &z, sizeof(int));
+    }
+    return v;
+}
+
 namespace {
 
 // ---- fill ------------------------------------------------------------------------------------
@@ -28,7 +41,7 @@ __global__ void __launch_bounds__(256) swa_fill_kernel(SwaArgs a, int row16, lon
     const int n = (int)(i / per), slot = (int)(i - (long long)n * per);
     long long row0;
     int len;
-    a.seq.rows(n, row0, len);
+    a.seq.rows(n, row0, len, slot == 0 && threadIdx.x % 32 == 0 ? &g_swa_fill_bad_seqlens : nullptr);
     int t = slot;
     if (slot >= a.sinks) {
         const int back = (int)((((long long)len - 1 - slot) % a.window + a.window) % a.window);

@@ -28,14 +28,14 @@
 
 namespace carve {
 
-__device__ int g_swa_bwd_timeout;   // set when a bounded wait gives up (never expected)
+__device__ int g_swa_bwd_status;   // kTimedOut, kBadOffsets
 
-int swa_bwd_take_timeout() {
+int swa_bwd_take_status() {
     int v = 0;
-    if (cudaMemcpyFromSymbol(&v, g_swa_bwd_timeout, sizeof(int)) != cudaSuccess) return 0;
+    if (cudaMemcpyFromSymbol(&v, g_swa_bwd_status, sizeof(int)) != cudaSuccess) return 0;
     if (v) {
         const int z = 0;
-        cudaMemcpyToSymbol(g_swa_bwd_timeout, &z, sizeof(int));
+        cudaMemcpyToSymbol(g_swa_bwd_status, &z, sizeof(int));
     }
     return v;
 }
@@ -58,6 +58,7 @@ struct BwdSmem {
 template <int D>
 __global__ void __launch_bounds__(256) swa_rows(SwaArgs a, long long rows) {
     constexpr int L = D / 8;
+    if (blockIdx.x == 0) check_seqs(a.seq, &g_swa_bwd_status, kBadOffsets);
     const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) / L;   // row * Hq + head
     const int x = threadIdx.x % L;
     float s = 0.f;
@@ -390,7 +391,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             if (w.n > 0) mbar_arrive_warp(&sm.accfree);
         }
     }
-    if (!ok && lane == 0) atomicOr(&g_swa_bwd_timeout, 1);
+    if (!ok && lane == 0) atomicOr(&g_swa_bwd_status, kTimedOut);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();

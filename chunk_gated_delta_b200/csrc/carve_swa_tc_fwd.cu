@@ -30,14 +30,14 @@
 
 namespace carve {
 
-__device__ int g_swa_timeout;   // set when a bounded wait gives up (never expected)
+__device__ int g_swa_fwd_status;   // kTimedOut, kBadOffsets
 
-int swa_fwd_take_timeout() {
+int swa_fwd_take_status() {
     int v = 0;
-    if (cudaMemcpyFromSymbol(&v, g_swa_timeout, sizeof(int)) != cudaSuccess) return 0;
+    if (cudaMemcpyFromSymbol(&v, g_swa_fwd_status, sizeof(int)) != cudaSuccess) return 0;
     if (v) {
         const int z = 0;
-        cudaMemcpyToSymbol(g_swa_timeout, &z, sizeof(int));
+        cudaMemcpyToSymbol(g_swa_fwd_status, &z, sizeof(int));
     }
     return v;
 }
@@ -411,7 +411,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             }
         }
     }
-    if (!ok && lane == 0) atomicOr(&g_swa_timeout, 1);
+    if (!ok && lane == 0) atomicOr(&g_swa_fwd_status, kTimedOut);
+    if (blockIdx.x == gridDim.x - 1) check_seqs(a.seq, &g_swa_fwd_status, kBadOffsets);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();

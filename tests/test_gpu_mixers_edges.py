@@ -195,3 +195,56 @@ def test_recurrence_scratch_belongs_to_the_stream_of_the_call(cuda_device):
         torch.cuda.synchronize()
         for a, b in zip(alone, got):
             assert all(torch.equal(y, z) for y, z in zip(a, b))
+
+
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+@pytest.mark.parametrize("cu", [(0, 40, 90), (0, 60, 50, 80), (-1, 40, 80), (90, 95), (0, 40, 2 ** 31 - 1)], ids=str)
+def test_bad_offsets_are_reported_by_every_packed_call(cuda_device, dt, cu):
+    """80 rows; a sequence that leaves them, or whose end lies before its start, counts as empty: its rows
+    stay as they were, and each call is reported once."""
+    N = len(cu) - 1
+    cu = torch.tensor(cu, dtype=torch.int32, device=cuda_device)
+    g = torch.Generator(device="cuda").manual_seed(61)
+    r = lambda *s: torch.randn(*s, generator=g, device=cuda_device).to(dt)  # noqa: E731
+    q, k, v, gl, dO = r(80, 2, 64), r(80, 2, 64) / 8, r(80, 2, 64), r(80, 2), r(80, 2, 64)
+
+    def reported(f, *a, **kw):
+        assert carve.carve_check() == 0
+        out = f(*a, **kw)
+        assert carve.carve_check() == 1 and carve.carve_check() == 0, f.__name__
+        return out
+
+    a = reported(carve.carve_gdr_fwd, q, k, v, gl, gl, cu_seqlens=cu)
+    reported(carve.carve_gdr_bwd, q, k, v, gl, gl, a["saved"], dO, cu_seqlens=cu)
+    marks = lambda: dict(o=torch.full_like(q, 7.0))  # noqa: E731
+    b = reported(carve.carve_swa_fwd, q, k, v, window=9, sinks=1, cu_seqlens=cu, out=marks())
+    grads = reported(carve.carve_swa_bwd, q, k, v, b["o"], b["lse"].nan_to_num(), dO, window=9, sinks=1, cu_seqlens=cu,
+                     out={n: torch.full_like(q, 7.0) for n in ("dq", "dk", "dv")})
+    kc = torch.full((N, 10, 2, 64), 7.0, dtype=dt, device=cuda_device)
+    vc = kc.clone()
+    reported(carve.carve_swa_fill, k, v, kc, vc, window=9, sinks=1, cu_seqlens=cu)
+    at = cu.tolist()
+    owned = torch.zeros(80, dtype=torch.bool)
+    for n in range(N):
+        good = 0 <= at[n] <= at[n + 1] <= 80
+        if good:
+            owned[at[n]:at[n + 1]] = True
+        assert (kc[n] == 7.0).all() != good and (vc[n] == 7.0).all() != good
+    for x in (b["o"], *grads.values()):
+        assert (x.cpu()[~owned] == 7.0).all()
+
+
+def test_bad_offsets_without_rows_are_reported(cuda_device):
+    q = torch.zeros(0, 2, 64, dtype=BF16, device=cuda_device)
+    kc = torch.full((2, 3, 2, 64), 7.0, dtype=BF16, device=cuda_device)
+    for ends, code in (((0, 0, 0), 0), ((0, 0, 1), 1), ((-1, -1, -1), 1)):
+        cu = torch.tensor(ends, dtype=torch.int32, device=cuda_device)
+        o = carve.carve_swa_fwd(q, q, q, window=3, cu_seqlens=cu)
+        assert carve.carve_check() == code
+        carve.carve_swa_bwd(q, q, q, o["o"], o["lse"], q, window=3, cu_seqlens=cu)
+        assert carve.carve_check() == code
+        carve.carve_swa_fill(q, q, kc, kc.clone(), window=3, cu_seqlens=cu)
+        assert carve.carve_check() == code and (kc == 7.0).all()
+        gl = torch.zeros(0, 2, dtype=BF16, device=cuda_device)
+        carve.carve_gdr_fwd(q, q, q, gl, gl, cu_seqlens=cu)
+        assert carve.carve_check() == code
