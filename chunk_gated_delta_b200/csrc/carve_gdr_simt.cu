@@ -35,8 +35,8 @@ constexpr int C = 32;          // tokens of a chunk
 constexpr int NT = 256;        // threads of a CTA, as 16 x 16
 constexpr int LC = C + 1;      // row stride of [C][C] and [C][32] tiles
 
-// per-tile operands (floats): Tm [C][C], A [C][C], G [C], w [C]
-constexpr int kPrep = 2 * C * C + 2 * C;
+// per-tile operands (floats): Tm [C][C], A [C][C], G [C], w [C], L [C] (G's low part)
+constexpr int kPrep = 2 * C * C + 3 * C;
 
 __device__ __forceinline__ float dot4(float4 a, float4 b, float c) { return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, fmaf(a.x, b.x, c)))); }
 // acc[i][j] += <row ty + 16 i of a, row tx + 16 j of b> over X terms (rows 16-byte aligned)
@@ -95,7 +95,7 @@ __device__ __forceinline__ void copy_f32(float *dst, int ld, const float *src, i
 template <int K, class IO>
 __global__ void __launch_bounds__(NT) gdr_simt_prep(GdrArgs a) {
     __shared__ __align__(16) float k[C][K + 4], q[C][K + 4];
-    __shared__ float M[C][LC], X[C][LC], G[C], w[C];
+    __shared__ float M[C][LC], X[C][LC], G[C], L[C], w[C];
     const int tile = blockIdx.x / a.Hv, h = blockIdx.x % a.Hv, tid = threadIdx.x;
     int n, c, len;
     long long row0;
@@ -110,15 +110,13 @@ __global__ void __launch_bounds__(NT) gdr_simt_prep(GdrArgs a) {
         if (tid < m) {
             const size_t at = (size_t)(row0 + tid) * a.Hv + h;
             const float x = ld_io(static_cast<const IO *>(a.g_logit) + at) + (a.tau ? a.tau[h] : 0.f);
-            la = -decay_amp(a.A_dec, h) * softplus_f(x);
+            la = least_log(-decay_amp(a.A_dec, h) * softplus_f(x));
             ww = sigmoid_f(ld_io(static_cast<const IO *>(a.w_logit) + at));
         }
-#pragma unroll
-        for (int off = 1; off < C; off <<= 1) {
-            const float up = __shfl_up_sync(0xffffffffu, la, off);
-            if (tid >= off) la += up;
-        }
+        float lo = 0.f;
+        sum2_scan(la, lo, tid);
         G[tid] = la;
+        L[tid] = lo;
         w[tid] = ww;
     }
     copies_wait();
@@ -127,10 +125,10 @@ __global__ void __launch_bounds__(NT) gdr_simt_prep(GdrArgs a) {
     float acc[2][2];
     zero(acc);
     mm_rows<K>(acc, &k[0][0], K + 4, &k[0][0], K + 4);
-    each(acc, [&](int t, int s, float x) { M[t][s] = s < t ? w[t] * expf(G[t] - G[s]) * x : 0.f; });
+    each(acc, [&](int t, int s, float x) { M[t][s] = s < t ? w[t] * expf(sum2_diff(G[t], L[t], G[s], L[s])) * x : 0.f; });
     zero(acc);
     mm_rows<K>(acc, &q[0][0], K + 4, &k[0][0], K + 4);
-    each(acc, [&](int t, int s, float x) { out[C * C + t * C + s] = s <= t ? expf(G[t] - G[s]) * x : 0.f; });
+    each(acc, [&](int t, int s, float x) { out[C * C + t * C + s] = s <= t ? expf(sum2_diff(G[t], L[t], G[s], L[s])) * x : 0.f; });
     __syncthreads();
     if (tid < C) {   // column tid of Tm by forward substitution, the column in registers
         float x[C];
@@ -144,6 +142,7 @@ __global__ void __launch_bounds__(NT) gdr_simt_prep(GdrArgs a) {
         }
         out[2 * C * C + tid] = G[tid];
         out[2 * C * C + C + tid] = w[tid];
+        out[2 * C * C + 2 * C + tid] = L[tid];
     }
     __syncthreads();
     each(acc, [&](int t, int s, float) { out[t * C + s] = X[t][s]; });
@@ -157,7 +156,7 @@ constexpr int VR = 16, ST = 128, LT = C + 4;
 
 template <int K>
 struct SweepStage {
-    float k[C][K + 4], q[C][K + 4], Tm[C][LT], A[C][LT], v[C][VR + 4], G[C], w[C];
+    float k[C][K + 4], q[C][K + 4], Tm[C][LT], A[C][LT], v[C][VR + 4], G[C], w[C], L[C];
 };
 template <int K>
 struct SweepSmem {
@@ -165,7 +164,7 @@ struct SweepSmem {
     float S[VR][K + 4], y[VR][LT], u[VR][LT], ue[VR][LT], x[C][VR + 4];
 };
 
-// tiles of a chunk: K, Q, Tm, A, G, w of (tile, h), and VR columns from v0 of `v` (values or dO); rows behind m: zero
+// tiles of a chunk: K, Q, Tm, A, G, w, L of (tile, h), and VR columns from v0 of `v` (values or dO); rows behind m: zero
 template <int K>
 __device__ __forceinline__ void copy_stage(SweepStage<K> &st, const GdrArgs &a, const void *v, int V, int v0, long long tile, long long row,
                                            int m, int h) {
@@ -189,6 +188,7 @@ __device__ __forceinline__ void copy_stage(SweepStage<K> &st, const GdrArgs &a, 
     if (threadIdx.x < C / 4) {
         copy16(st.G + 4 * threadIdx.x, p + 2 * C * C + 4 * threadIdx.x, true);
         copy16(st.w + 4 * threadIdx.x, p + 2 * C * C + C + 4 * threadIdx.x, true);
+        copy16(st.L + 4 * threadIdx.x, p + 2 * C * C + 2 * C + 4 * threadIdx.x, true);
     }
     copies_commit();
 }
@@ -287,13 +287,13 @@ __global__ void __launch_bounds__(ST) gdr_simt_sweep(GdrArgs a, bool save) {
             sm.y[v][t4 + i] = s.w[t4 + i] * (s.v[t4 + i][v] - eG * g[i]);
         }
         __syncthreads();
-        const float gl = s.G[C - 1];
+        const float gl = s.G[C - 1], ll = s.L[C - 1];
         float u[4] = {};
         rows4<C>(u, s.Tm[t4], LT, sm.y[v]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             sm.u[v][t4 + i] = u[i];
-            sm.ue[v][t4 + i] = u[i] * expf(gl - s.G[t4 + i]);
+            sm.ue[v][t4 + i] = u[i] * expf(sum2_diff(gl, ll, s.G[t4 + i], s.L[t4 + i]));
             if (save) keep[(size_t)V * K + (t4 + i) * V + v0 + v] = u[i];
         }
         __syncthreads();
@@ -338,12 +338,12 @@ __global__ void __launch_bounds__(ST) gdr_simt_bsweep(GdrArgs a) {
         if (c > 0) fetch(c - 1);
         float *out = reinterpret_cast<float *>(a.ws) + ((size_t)tile * a.Hv + h) * ((size_t)V * K + C * V);
         for (int i = threadIdx.x; i < VR * K; i += ST) out[(size_t)v0 * K + i] = sm.S[i / K][i % K];
-        const float gl = s.G[C - 1];
+        const float gl = s.G[C - 1], ll = s.L[C - 1];
         float d[4] = {};
         rows4<K>(d, s.k[t4], K + 4, sm.S[v]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            d[i] *= expf(gl - s.G[t4 + i]);
+            d[i] *= expf(sum2_diff(gl, ll, s.G[t4 + i], s.L[t4 + i]));
             sm.u[v][t4 + i] = s.v[t4 + i][v] * expf(s.G[t4 + i]);   // e^G dO
         }
         columns4(d, &s.A[0][t4], &s.v[0][v]);
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(ST) gdr_simt_bsweep(GdrArgs a) {
 template <int K, int V>
 struct GradSmem {
     float k[C][K + 4], q[C][K + 4], S[V][K], dO[C][V + 4], dY[C][V + 4], U[C][V + 4], v[C][V + 4];
-    float P1[C][LC], P2[C][LC], kk[C][LC], row[4][C], G[C], w[C], red[NT / 32];
+    float P1[C][LC], P2[C][LC], kk[C][LC], row[4][C], G[C], L[C], w[C], red[NT / 32];
 };
 
 // column j of a thread's K / 16: groups of four
@@ -444,10 +444,11 @@ __global__ void __launch_bounds__(NT) gdr_simt_grad(GdrArgs a) {
         if (tid < C) {
             sm.G[tid] = prep[2 * C * C + tid];
             sm.w[tid] = prep[2 * C * C + C + tid];
+            sm.L[tid] = prep[2 * C * C + 2 * C + tid];
         }
         copies_wait();
         __syncthreads();
-        const float gl = sm.G[C - 1];
+        const float gl = sm.G[C - 1], ll = sm.L[C - 1];
         float acc[2][2], x1[2][NK];
         // per-row partial sums of this thread's two rows: gate gradients
         float dG[2] = {0.f, 0.f}, dw[2] = {0.f, 0.f}, kb[2] = {0.f, 0.f}, lastp = 0.f;
@@ -495,7 +496,7 @@ __global__ void __launch_bounds__(NT) gdr_simt_grad(GdrArgs a) {
 #pragma unroll
             for (int j = 0; j < NK; ++j) {
                 const int t = tid / 16 + 16 * i, x = col4(j);
-                const float y = expf(gl - sm.G[t]) * x1[i][j];
+                const float y = expf(sum2_diff(gl, ll, sm.G[t], sm.L[t])) * x1[i][j];
                 dk[i][j] += y;
                 kb[i] += sm.k[t][x] * y;
             }
@@ -514,7 +515,7 @@ __global__ void __launch_bounds__(NT) gdr_simt_grad(GdrArgs a) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int t = tid / 16 + 16 * i, s = tid % 16 + 16 * j;
-                const float p = s <= t ? acc[i][j] * expf(sm.G[t] - sm.G[s]) : 0.f;
+                const float p = s <= t ? acc[i][j] * expf(sum2_diff(sm.G[t], sm.L[t], sm.G[s], sm.L[s])) : 0.f;
                 sm.P1[t][s] = p;
                 pr[i][j] = s < t ? p * kq[i][j] : 0.f;
             }
@@ -525,7 +526,7 @@ __global__ void __launch_bounds__(NT) gdr_simt_grad(GdrArgs a) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int t = tid / 16 + 16 * i, s = tid % 16 + 16 * j;
-                const float p = s < t ? -acc[i][j] * expf(sm.G[t] - sm.G[s]) : 0.f;
+                const float p = s < t ? -acc[i][j] * expf(sum2_diff(sm.G[t], sm.L[t], sm.G[s], sm.L[s])) : 0.f;
                 dw[i] += p * sm.kk[t][s];
                 sm.P2[t][s] = sm.w[t] * p;
                 pr[i][j] += sm.w[t] * p * sm.kk[t][s];
@@ -580,7 +581,7 @@ __global__ void __launch_bounds__(NT) gdr_simt_grad(GdrArgs a) {
                 const float x = ld_io(static_cast<const IO *>(a.g_logit) + at) + (a.tau ? a.tau[h] : 0.f);
                 const float amp = decay_amp(a.A_dec, h), w = sm.w[tid];
                 dlog = -amp * sigmoid_f(x) * g;
-                damp = -amp * softplus_f(x) * g;
+                damp = softplus_f(x) * (-amp * g);   // of a reset g is 0, and amp softplus may be beyond fp32
                 st_io(static_cast<IO *>(a.dg_logit) + at, dlog);
                 st_io(static_cast<IO *>(a.dw_logit) + at, sm.row[1][tid] * w * (1.f - w));
             }

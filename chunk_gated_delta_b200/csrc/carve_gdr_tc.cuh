@@ -25,10 +25,11 @@ constexpr uint32_t kTile64 = kC * 128;   // bytes of a 64-row block
 struct GdrPrep {
     __nv_bfloat16 t_hi[kC * 64], t_lo[kC * 64], A[kC * 64];
     float eG[kC], eK[kC], w[kC], G[kC];   // e^{G_t}, e^{G_C - G_t}, w_t, G_t log2 e
-    float eB[kC], pad[192];               // e^{G_r - G_t}, r the last of t's 16 tokens
+    float eB[kC], L[kC];                  // e^{G_r - G_t}, r the last of t's 16 tokens; G's low part
+    float pad[128];
 };
 static_assert(sizeof(GdrPrep) == 26624, "slots are copied in bulk, tiles on 1024-byte boundaries");
-constexpr uint32_t kVecBytes = 5 * kC * 4;   // eG .. eB
+constexpr uint32_t kVecBytes = 6 * kC * 4;   // eG .. L
 
 // Per (tile, value head): the state [V][K] and a token tile [64][V], bf16 operand layout.
 template <int K, int V>

@@ -65,7 +65,7 @@ struct PrepSmem {
         };
     };
     __nv_bfloat16 A[kC * 64];
-    float eG[kC], eK[kC], w[kC], G[kC], eB[kC], half;
+    float eG[kC], eK[kC], w[kC], G[kC], eB[kC], L[kC], half[2];
     uint64_t full, done;
     uint32_t tmem;
 };
@@ -210,27 +210,27 @@ __global__ void __launch_bounds__(128) gdr_tc_prep(GdrArgs a, const __grid_const
     // gates of a head and the running sums of log a, by warps 0 and 1; rows behind the end: log a = 0, w = 0
     auto gates = [&](int h) {
         if (tid >= kC) return;
-        float la = 0.f, w = 0.f;
+        float la = 0.f, lo = 0.f, w = 0.f;
         if (tid < m) {
             const size_t at = (size_t)(row + tid) * a.Hv + h;
             const float x = ld_io(static_cast<const __nv_bfloat16 *>(a.g_logit) + at) + (a.tau ? a.tau[h] : 0.f);
-            la = -1.4426950408889634f * decay_amp(a.A_dec, h) * softplus_f(x);
+            la = least_log(-1.4426950408889634f * decay_amp(a.A_dec, h) * softplus_f(x));
             w = sigmoid_f(ld_io(static_cast<const __nv_bfloat16 *>(a.w_logit) + at));
         }
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const float up = __shfl_up_sync(0xffffffffu, la, off);
-            if (lane >= off) la += up;
+        sum2_scan(la, lo, lane);
+        if (tid == 31) {
+            sm.half[0] = la;
+            sm.half[1] = lo;
         }
-        if (tid == 31) sm.half = la;
         asm volatile("bar.sync 1, 64;\n" ::: "memory");
-        if (warp == 1) la += sm.half;
+        if (warp == 1) sum2_add(la, lo, sm.half[0], sm.half[1]);
         sm.G[tid] = la;
+        sm.L[tid] = lo;
         sm.w[tid] = w;
         asm volatile("bar.sync 1, 64;\n" ::: "memory");
         sm.eG[tid] = exp2f(la);
-        sm.eK[tid] = exp2f(sm.G[kC - 1] - la);
-        sm.eB[tid] = exp2f(sm.G[tid | 15] - la);
+        sm.eK[tid] = exp2f(sum2_diff(sm.G[kC - 1], sm.L[kC - 1], la, lo));
+        sm.eB[tid] = exp2f(sum2_diff(sm.G[tid | 15], sm.L[tid | 15], la, lo));
     };
     gates(hk * share);   // the first head's while the tiles and their product are under way
     ok = ok && mbar_wait(&sm.done, 0, kSwaWait);
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(128) gdr_tc_prep(GdrArgs a, const __grid_const
             gates(h);
             __syncthreads();
         }
-        const float Gt = sm.G[t], f0 = key ? sm.w[t] : 1.f;
+        const float Gt = sm.G[t], Lt = sm.L[t], f0 = key ? sm.w[t] : 1.f;
 #pragma unroll 1
         for (int s0 = 0; s0 <= (t | 31); s0 += 16) {
             uint32_t g[16];
@@ -267,13 +267,13 @@ __global__ void __launch_bounds__(128) gdr_tc_prep(GdrArgs a, const __grid_const
             tmem_tie16(g);
             float y[16];
             if (s0 + 15 < (t & 32)) {   // all below the diagonal: one factor a row, one a column
-                const float f = f0 * ex2(Gt - sm.G[s0 + 15]);
+                const float f = f0 * ex2(sum2_diff(Gt, Lt, sm.G[s0 + 15], sm.L[s0 + 15]));
 #pragma unroll
                 for (int e = 0; e < 16; ++e) y[e] = here ? f * sm.eB[s0 + e] * __uint_as_float(g[e]) : 0.f;
             } else {
                 const int lim = here ? t + !key - s0 : 0;   // s < t, and s = t for queries
 #pragma unroll
-                for (int e = 0; e < 16; ++e) y[e] = e < lim ? f0 * ex2(Gt - sm.G[s0 + e]) * __uint_as_float(g[e]) : 0.f;
+                for (int e = 0; e < 16; ++e) y[e] = e < lim ? f0 * ex2(sum2_diff(Gt, Lt, sm.G[s0 + e], sm.L[s0 + e])) * __uint_as_float(g[e]) : 0.f;
             }
             if (!key) {
 #pragma unroll

@@ -75,6 +75,28 @@ __device__ __forceinline__ void check_seqs(const Seqs &s, int *bad, int mark = 1
 constexpr int kTimedOut = 1;     // a bounded wait gave up (never expected)
 constexpr int kBadOffsets = 2;   // a packed sequence's offsets are out of range
 
+// Running sums of log decays as hi + lo.  A decay between two tokens is the difference of two such sums, and
+// behind a token that resets the state (log a of -1e3, say) an fp32 sum of the whole chunk has lost the low
+// bits of the mild steps: the factors were off by 6e-5 there, 1e-3 at -1e4.  lo holds what the roundings of hi
+// drop (exactly, addition by addition), so a difference is good to 2^-40 of the largest step.
+__device__ __forceinline__ void sum2_add(float &hi, float &lo, float h, float l) {
+    const float s = hi + h, y = s - hi;
+    lo += l + ((hi - (s - y)) + (h - y));
+    hi = s;
+}
+// inclusive over the lanes of a warp
+__device__ __forceinline__ void sum2_scan(float &hi, float &lo, int lane) {
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const float h = __shfl_up_sync(0xffffffffu, hi, off), l = __shfl_up_sync(0xffffffffu, lo, off);
+        if (lane >= off) sum2_add(hi, lo, h, l);
+    }
+}
+__device__ __forceinline__ float sum2_diff(float hi, float lo, float hi0, float lo0) { return (hi - hi0) + (lo - lo0); }
+// log a, not below -1e4 (in either base: a decay of zero in fp32 long before), so that sums and their
+// differences are finite; a NaN stays one
+__device__ __forceinline__ float least_log(float la) { return la < -1e4f ? -1e4f : la; }
+
 struct GdrArgs {
     Seqs seq;
     int Hk, Hv;

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import chunk_gated_delta_b200 as carve
+from tests import mixer_reference as R
 from tests.test_gpu_mixers import TYPES, U, delta_inputs, ids, rel  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -248,3 +249,52 @@ def test_bad_offsets_without_rows_are_reported(cuda_device):
         gl = torch.zeros(0, 2, dtype=BF16, device=cuda_device)
         carve.carve_gdr_fwd(q, q, q, gl, gl, cu_seqlens=cu)
         assert carve.carve_check() == code
+
+
+def delta_definition(q, k, v, g, w, A_dec=None, tau=None, S0=None):
+    """mixer_reference.delta with a softplus whose gradient is finite for any logit (there it divides
+    e^x by 1 + e^x, which is no number between 710 and 1e9)."""
+    T, Hv, dv = v.shape
+    q, k = (y.repeat_interleave(Hv // k.shape[1], 1) for y in (q, k))
+    x = g if tau is None else g + tau
+    a = torch.exp(-torch.logaddexp(x, torch.zeros_like(x)) * (1.0 if A_dec is None else torch.exp(A_dec)))
+    w = torch.sigmoid(w)
+    S = torch.zeros(Hv, dv, k.shape[2], dtype=torch.float64) if S0 is None else S0
+    o = []
+    for t in range(T):
+        S = S * a[t][:, None, None]
+        S = S + (w[t][:, None] * (v[t] - (S * k[t][:, None, :]).sum(-1)))[:, :, None] * k[t][:, None, :]
+        o.append((S * q[t][:, None, :]).sum(-1))
+    return torch.stack(o), S
+
+
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+@pytest.mark.parametrize("logit", [30.0, 1e3, 1e4, 1e5, 3e38], ids=str)
+@pytest.mark.parametrize("full", [False, True], ids=["plain", "full"])
+def test_delta_tokens_that_reset_the_state(cuda_device, dt, logit, full):
+    """Mild decays (0.95 a token) with a token in ten that clears the state: what follows it within its chunk is
+    as accurate as elsewhere.  Tolerances as in test_gpu_mixers.py: fp32 1e-5; bf16 states 2e-5, results 4 u
+    and 8 u."""
+    T, Hk, Hv, dk, dv = 200, 2, 4, 128, 64
+    s = delta_inputs(T, Hk, Hv, dk, dv, dt, 71)
+    g = torch.Generator().manual_seed(72)
+    r = lambda *n: torch.randn(*n, generator=g, dtype=torch.float32).double()  # noqa: E731
+    s["g"] = torch.where(torch.rand(T, Hv, generator=g) < 0.1, torch.tensor(logit, dtype=dt).double(), s["g"])
+    A_dec, tau, S0, dS = (0.3 * r(Hv), 0.5 * r(Hv), 0.2 * r(Hv, dv, dk), r(Hv, dv, dk)) if full else (None,) * 4
+    dev = lambda x: None if x is None else x.float().to(cuda_device)  # noqa: E731
+    x = [s[n].to(dt).to(cuda_device)[None] for n in ("q", "k", "v", "g", "w", "dO")]
+    more = dict(A_dec=dev(A_dec), tau=dev(tau))
+    out = carve.carve_gdr_fwd(*x[:5], S0=dev(S0[None]) if full else None, **more)
+    gr = carve.carve_gdr_bwd(*x[:5], out["saved"], x[5], dS_final=dev(dS[None]) if full else None, **more)
+    inp = dict(q=s["q"], k=s["k"], v=s["v"], g=s["g"], w=s["w"], A_dec=A_dec, tau=tau, S0=S0)
+    want_o, want_S = delta_definition(**inp)
+    wg = R.grads(delta_definition, inp, (s["dO"], dS))
+    u, f32 = U[BF16], dt == torch.float32
+    pairs = dict(o=(out["o"][0], want_o, 4 * u), S=(out["S_final"][0], want_S, 2e-5), dq=(gr["dq"][0], wg["q"], 4 * u),
+                 dk=(gr["dk"][0], wg["k"], 8 * u), dv=(gr["dv"][0], wg["v"], 4 * u), dg=(gr["dg_logit"][0], wg["g"], 8 * u),
+                 dw=(gr["dw_logit"][0], wg["w"], 8 * u))
+    if full:   # dS0 is nearly all cleared: one rounding of each chunk's factors
+        pairs.update(dS0=(gr["dS0"][0], wg["S0"], 4 * u), dA=(gr["dA_dec"], wg["A_dec"], 8 * u), dtau=(gr["dtau"], wg["tau"], 8 * u))
+    for n, (got, want, lim) in pairs.items():
+        lim = (8e-5 if n in ("dA", "dtau") else 1e-5) if f32 else lim
+        assert rel(got, want) <= lim, (n, rel(got, want), lim)
