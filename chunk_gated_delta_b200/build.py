@@ -57,14 +57,16 @@ def bind_stale() -> bool:
 
 
 def _bind(verbose):
-    """Compiles and links the binding beside libcarve.so, which it finds in its own folder."""
+    """Compiles and links the binding beside libcarve.so, which it finds in its own folder: by name, since by path
+    (the library has no soname) a copied tree would load this one's."""
     torch = os.path.dirname(importlib.util.find_spec("torch").origin)
     inc = os.path.join(torch, "include")
     cuda = os.path.dirname(os.path.dirname(os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")))
     tmp = BIND + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-w", "-I", inc, "-I",
            os.path.join(inc, "torch", "csrc", "api", "include"), "-I", os.path.join(cuda, "include"), "-I",
-           sysconfig.get_paths()["include"], "-o", tmp, BIND_SRC, LIB, "-Wl,-rpath,$ORIGIN", "-L", os.path.join(torch, "lib"),
+           sysconfig.get_paths()["include"], "-o", tmp, BIND_SRC, "-L", PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN",
+           "-L", os.path.join(torch, "lib"),
            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
     if verbose:
         print(" ".join(cmd), file=sys.stderr)

@@ -1,0 +1,30 @@
+"""The mixers' binding as a built file: which library it loads, when it is built again.  No GPU."""
+import os
+import shutil
+import subprocess
+import sys
+
+import pytest
+
+from chunk_gated_delta_b200 import build
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    build.build()
+
+
+def test_a_copied_tree_loads_its_own_library(tmp_path):
+    """The package copied elsewhere: its binding uses the library that lies beside it, the one that the
+    package's other calls use, so that their status words are the same ones."""
+    pkg = tmp_path / "chunk_gated_delta_b200"
+    pkg.mkdir()
+    for f in os.listdir(build.PKG):
+        if f.endswith((".py", ".so")):
+            shutil.copy(os.path.join(build.PKG, f), pkg / f)
+    code = ("from chunk_gated_delta_b200 import mixers, load, library_path\n"
+            "load(); mixers._bind()\n"
+            "print(*sorted({l.split()[-1] for l in open('/proc/self/maps') if 'libcarve.so' in l}))\n")
+    env = {k: v for k, v in os.environ.items() if k != "PYTHONPATH"}
+    got = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, env=env, capture_output=True, text=True, check=True).stdout.split()
+    assert got == [str(pkg / "libcarve.so")]
