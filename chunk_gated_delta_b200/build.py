@@ -1,5 +1,6 @@
 """Builds libcarve.so (the C-ABI library of include/carve.h and carve_mixers.h) in-tree for sm_100a with nvcc, and
-_carve_bind.so (the host side of the mixers' Python calls, against PyTorch's headers) with g++.
+_carve_bind.so (the host side of the mixers' Python calls, against PyTorch's headers) with g++.  Without PyTorch
+the library is built alone; with another PyTorch or Python than the last time the binding is built anew.
 
 Each .cu file is compiled to an object in its own process (in parallel), then the objects are
 linked into the shared library; an object is rebuilt only when its source, a header or this
@@ -7,6 +8,7 @@ file is newer than it."""
 from __future__ import annotations
 
 import glob
+import importlib.metadata
 import importlib.util
 import os
 import subprocess
@@ -19,6 +21,7 @@ ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libcarve.so")
 OBJ = os.path.join(PKG, "_build")
 BIND = os.path.join(PKG, "_carve_bind.so")
+BIND_FOR = os.path.join(PKG, "_carve_bind.for")   # what the built binding fits
 BIND_SRC = os.path.join(PKG, "csrc", "carve_bind.cpp")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2"]
@@ -48,9 +51,22 @@ def stale() -> bool:
     return any(os.path.getmtime(p) > t for p in deps())
 
 
+def bind_for() -> str | None:
+    """What a binding fits, beside its sources: this PyTorch and this Python; None without PyTorch."""
+    try:
+        return f"torch {importlib.metadata.version('torch')} {sysconfig.get_config_var('EXT_SUFFIX')}"
+    except importlib.metadata.PackageNotFoundError:
+        return None
+
+
 def bind_stale() -> bool:
-    if not os.path.exists(BIND):
+    if bind_for() is None:   # nothing to build it against, or to call it from
+        return False
+    if not os.path.exists(BIND) or not os.path.exists(BIND_FOR):
         return True
+    with open(BIND_FOR) as f:
+        if f.read() != bind_for():
+            return True
     t = os.path.getmtime(BIND)
     return any(os.path.getmtime(p) > t for p in [BIND_SRC, os.path.abspath(__file__)] +
                glob.glob(os.path.join(ROOT, "include", "*.h")))
@@ -72,6 +88,9 @@ def _bind(verbose):
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True)
     os.replace(tmp, BIND)
+    with open(tmp, "w") as f:
+        f.write(bind_for())
+    os.replace(tmp, BIND_FOR)
 
 
 def _compile(src, nvcc, force, verbose):
@@ -102,7 +121,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     tmp = LIB + f".tmp{os.getpid()}"
     subprocess.run([nvcc, "-shared", *ARCH, "-o", tmp, *objs], check=True)
     os.replace(tmp, LIB)
-    if force or bind_stale():
+    if bind_stale() or (force and bind_for()):
         _bind(verbose)
     return LIB
 
