@@ -19,15 +19,8 @@ int step_take_timeout();
 int simt_take_bad_seqlens();
 int tc_fwd_take_bad_seqlens();
 int tc_bwd_take_bad_seqlens();
-int gdr_take_bad_seqlens();
-int swa_take_bad_seqlens();
-int swa_fwd_take_status();   // bit 0: timeout, bit 1: bad offsets
-int swa_bwd_take_status();
-int swa_fill_take_bad_seqlens();
-int gdr_tc_fwd_take_timeout();
-int gdr_tc_bwd_take_timeout();
-int gdr_tc_fwd_take_bad_seqlens();
-int gdr_tc_bwd_take_bad_seqlens();
+int gdr_take_status();   // of the mixers' kernels: bit 0 timeout, bit 1 bad offsets
+int swa_take_status();
 cudaError_t launch_selftest_timeout(uint32_t iterations, cudaStream_t st);
 cudaError_t launch_bwd_simt(int K, int V, bool bf16, const BwdArgs &a, float *dA, float *dB, cudaStream_t st);
 cudaError_t launch_fwd_exact(int K, int V, bool bf16, const FwdArgs &a, cudaStream_t st);
@@ -311,12 +304,9 @@ carve_status carve_step(const carve_dims *d, const void *q, const void *k, const
 
 carve_status carve_check(void *stream) {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return CARVE_ERR_CUDA;
-    const int window = carve::swa_fwd_take_status() | carve::swa_bwd_take_status();
-    const int t = (window & 1) | carve::tc_fwd_take_timeout() | carve::tc_bwd_take_timeout() | carve::step_take_timeout() |
-                  carve::gdr_tc_fwd_take_timeout() | carve::gdr_tc_bwd_take_timeout();
-    const int bad = carve::simt_take_bad_seqlens() | carve::tc_fwd_take_bad_seqlens() | carve::tc_bwd_take_bad_seqlens() |
-                    (window & 2) | carve::swa_fill_take_bad_seqlens() | carve::gdr_take_bad_seqlens() |
-                    carve::swa_take_bad_seqlens() | carve::gdr_tc_fwd_take_bad_seqlens() | carve::gdr_tc_bwd_take_bad_seqlens();
+    const int mixers = carve::gdr_take_status() | carve::swa_take_status();
+    const int t = (mixers & 1) | carve::tc_fwd_take_timeout() | carve::tc_bwd_take_timeout() | carve::step_take_timeout();
+    const int bad = (mixers & 2) | carve::simt_take_bad_seqlens() | carve::tc_fwd_take_bad_seqlens() | carve::tc_bwd_take_bad_seqlens();
     return t ? CARVE_ERR_TIMEOUT : bad ? CARVE_ERR_INVALID_ARG : CARVE_OK;
 }
 

@@ -187,7 +187,14 @@ int swa_fill_take_bad_seqlens();
 cudaError_t launch_swa_check(const Seqs &s, cudaStream_t st);   // the offsets alone (no rows)
 cudaError_t launch_swa_fill(bool bf16, const SwaArgs &a, cudaStream_t st);
 cudaError_t launch_swa_step(bool bf16, const SwaArgs &a, cudaStream_t st);
+int gdr_tc_fwd_take_timeout();
+int gdr_tc_bwd_take_timeout();
 int gdr_take_bad_seqlens();
+int gdr_tc_fwd_take_bad_seqlens();
+int gdr_tc_bwd_take_bad_seqlens();
 int swa_take_bad_seqlens();
+// kTimedOut, kBadOffsets of all kernels of a mixer since the last call (0 when none ran)
+int gdr_take_status();
+int swa_take_status();
 
 }  // namespace carve

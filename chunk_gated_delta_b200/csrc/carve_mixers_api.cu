@@ -2,10 +2,29 @@
 // and kernel dispatch.  Nothing here allocates, frees or synchronises.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 
 #include "../../include/carve_mixers.h"
 #include "carve_mixers.cuh"
+
+namespace carve {
+
+// Whether this process has launched kernels of a mixer: carve_check reads their status words only then
+// (each word is a synchronous copy of 13 us).  Never taken back: a captured graph may launch them again.
+std::atomic<bool> g_gdr_used{false}, g_swa_used{false};
+
+int gdr_take_status() {
+    if (!g_gdr_used.load(std::memory_order_relaxed)) return 0;
+    return (gdr_tc_fwd_take_timeout() | gdr_tc_bwd_take_timeout() ? kTimedOut : 0) |
+           (gdr_take_bad_seqlens() | gdr_tc_fwd_take_bad_seqlens() | gdr_tc_bwd_take_bad_seqlens() ? kBadOffsets : 0);
+}
+int swa_take_status() {
+    if (!g_swa_used.load(std::memory_order_relaxed)) return 0;
+    return swa_fwd_take_status() | swa_bwd_take_status() | (swa_take_bad_seqlens() | swa_fill_take_bad_seqlens() ? kBadOffsets : 0);
+}
+
+}  // namespace carve
 
 namespace {
 
@@ -128,6 +147,7 @@ carve_status carve_gdr_fwd(const carve_gdr_dims *d, const int32_t *cu_seqlens, c
         !ok_elem_opt(A_dec) || !ok_elem_opt(tau) ||
         !ok_opt(S0) || !ok_opt(S_final) || !ok_opt(saved) || !ok_opt(workspace) || (!saved && !workspace))
         return CARVE_ERR_INVALID_ARG;
+    carve::g_gdr_used.store(true, std::memory_order_relaxed);
     carve::GdrArgs a{};
     a.seq = seqs(d, cu_seqlens, packed);
     a.Hk = d->Hk; a.Hv = d->Hv;
@@ -157,6 +177,7 @@ carve_status carve_gdr_bwd(const carve_gdr_dims *d, const int32_t *cu_seqlens, c
         !ok_elem_opt(tau) || !ok_elem_opt(dA_dec) || !ok_elem_opt(dtau) || (A_dec == nullptr) != (dA_dec == nullptr) ||
         (tau == nullptr) != (dtau == nullptr))
         return CARVE_ERR_INVALID_ARG;
+    carve::g_gdr_used.store(true, std::memory_order_relaxed);
     carve::GdrArgs a{};
     a.seq = seqs(d, cu_seqlens, packed);
     a.Hk = d->Hk; a.Hv = d->Hv;
@@ -196,6 +217,7 @@ carve_status carve_swa_fwd(const carve_swa_dims *d, const int32_t *cu_seqlens, c
     if (!ok_elem_opt(cu_seqlens) || !ok_ptr(q, rows) || !ok_ptr(k, rows) || !ok_ptr(v, rows) || !ok_ptr(o, rows) ||
         !ok_elem_opt(lse))
         return CARVE_ERR_INVALID_ARG;
+    carve::g_swa_used.store(true, std::memory_order_relaxed);
     carve::SwaArgs a = swa_args(d, cu_seqlens);
     a.q = q; a.k = k; a.v = v; a.o = o; a.lse = lse;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
@@ -222,6 +244,7 @@ carve_status carve_swa_bwd(const carve_swa_dims *d, const int32_t *cu_seqlens, c
         !ok_elem(lse, 4, rows) || !ok_ptr(dO, rows) || !ok_ptr(dq, rows) || !ok_ptr(dk, rows) || !ok_ptr(dv, rows) ||
         !ok_ptr(workspace))
         return CARVE_ERR_INVALID_ARG;
+    carve::g_swa_used.store(true, std::memory_order_relaxed);
     carve::SwaArgs a = swa_args(d, cu_seqlens);
     if (rows == 0) return no_rows(a.seq, static_cast<cudaStream_t>(stream));
     a.q = q; a.k = k; a.v = v; a.o = const_cast<void *>(o); a.lse = const_cast<float *>(lse);
@@ -241,6 +264,7 @@ carve_status carve_swa_fill(const carve_swa_dims *d, const int32_t *cu_seqlens, 
     const long long rows = rows_of(d, packed);
     if (!ok_elem_opt(cu_seqlens) || !ok_ptr(k, rows) || !ok_ptr(v, rows) || !ok_ptr(k_cache) || !ok_ptr(v_cache))
         return CARVE_ERR_INVALID_ARG;
+    carve::g_swa_used.store(true, std::memory_order_relaxed);
     carve::SwaArgs a = swa_args(d, cu_seqlens);
     if (rows == 0) return no_rows(a.seq, static_cast<cudaStream_t>(stream));
     a.k = k; a.v = v; a.k_cache = k_cache; a.v_cache = v_cache;
