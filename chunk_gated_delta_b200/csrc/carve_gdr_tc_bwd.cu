@@ -884,6 +884,8 @@ cudaError_t bwd_t(const GdrArgs &a, cudaStream_t st) {
     }
     if (e != cudaSuccess) return e;
     sweep<<<a.seq.N * a.Hv, kSweepThreads, sb, st>>>(a, mq, mk, md, mdv);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
     const long long tiles = a.seq.n_tiles(kC), items = tiles * a.Hk;
     if (items) e = launch_after(true, grad, (unsigned)(items < sm_count() ? items : sm_count()), kSweepThreads, gb, st, a, mq, mk, md, mdq, mdk);
     if (e != cudaSuccess) return e;

@@ -617,6 +617,8 @@ cudaError_t fwd_t(const GdrArgs &a, bool save, cudaStream_t st) {
         if (e == cudaSuccess) e = set_smem_once(reinterpret_cast<const void *>(prep), bytes);
         if (e != cudaSuccess) return e;
         prep<<<(unsigned)(a.seq.n_tiles(kC) * a.Hk), 128, bytes, st>>>(a, mq, mk);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
     }
     return save ? sweep_t<K, V, true>(a, mq, mk, mv, mo, rows > 0, st) : sweep_t<K, V, false>(a, mq, mk, mv, mo, rows > 0, st);
 }
