@@ -7,6 +7,7 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <pybind11/stl.h>
+#include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/utils/pybind.h>
 
 #include <climits>
@@ -187,21 +188,22 @@ Tensor buffer(const char *name, const Opt &given, const char *sized_by, size_t n
     return *given;
 }
 
-// a result: out[key], or a new tensor that is put there
-Tensor result(py::dict &out, const char *key, at::IntArrayRef shape, const at::TensorOptions &options) {
-    const py::str k(key);
-    if (out.contains(k)) return out[k].cast<Tensor>();
-    Tensor x = at::empty(shape, options);
-    out[k] = x;
-    return x;
-}
 py::dict copy_of(const py::object &out) {
     return out.is_none() ? py::dict() : py::reinterpret_steal<py::dict>(PyDict_Copy(py::dict(out).ptr()));
 }
+// out[key], if there is one; None counts as none
 Opt given(const py::dict &out, const char *key) {
     const py::str k(key);
     if (!out.contains(k) || out[k].is_none()) return std::nullopt;
+    if (!THPVariable_Check(py::object(out[k]).ptr())) throw py::type_error(std::string(key) + " must be a tensor");
     return out[k].cast<Tensor>();
+}
+// a result: the caller's, or a new tensor that is put there
+Tensor result(py::dict &out, const char *key, at::IntArrayRef shape, const at::TensorOptions &options) {
+    if (const Opt x = given(out, key)) return *x;
+    Tensor x = at::empty(shape, options);
+    out[py::str(key)] = x;
+    return x;
 }
 
 // ---- the scalar-gated delta rule ----------------------------------------------------------

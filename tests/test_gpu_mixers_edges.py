@@ -298,3 +298,17 @@ def test_delta_tokens_that_reset_the_state(cuda_device, dt, logit, full):
     for n, (got, want, lim) in pairs.items():
         lim = (8e-5 if n in ("dA", "dtau") else 1e-5) if f32 else lim
         assert rel(got, want) <= lim, (n, rel(got, want), lim)
+
+
+def test_out_may_hold_none_and_refuses_what_is_no_tensor(cuda_device):
+    x = delta_tensors((1, 70), 2, 2, 64, 64, 45, cuda_device)
+    q, k, v, dO = window_tensors((1, 70), 2, 2, 64, 45, cuda_device)
+    want = carve.carve_gdr_fwd(*x[:5])
+    got = carve.carve_gdr_fwd(*x[:5], out=dict(o=None, S_final=None, saved=None))
+    assert torch.equal(got["o"], want["o"]) and torch.equal(got["S_final"], want["S_final"])
+    a = carve.carve_swa_fwd(q, k, v, window=9, out=dict(o=None, lse=None))
+    g = carve.carve_swa_bwd(q, k, v, a["o"], a["lse"], dO, window=9, out=dict(dq=None))
+    assert torch.equal(g["dq"], carve.carve_swa_bwd(q, k, v, a["o"], a["lse"], dO, window=9)["dq"])
+    for out in (dict(o=[1.0]), dict(S_final=np.zeros(3)), dict(saved="x"), [1, 2], 5):
+        with pytest.raises(TypeError):
+            carve.carve_gdr_fwd(*x[:5], out=out)
