@@ -7,7 +7,7 @@ import torch
 
 import chunk_gated_delta_b200 as carve
 from tests import mixer_reference as R
-from tests.test_gpu_mixers import TYPES, U, delta_inputs, ids, rel  # noqa: F401
+from tests.test_gpu_mixers import TYPES, U, delta_inputs, ids, near, rel, window_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -312,3 +312,112 @@ def test_out_may_hold_none_and_refuses_what_is_no_tensor(cuda_device):
     for out in (dict(o=[1.0]), dict(S_final=np.zeros(3)), dict(saved="x"), [1, 2], 5):
         with pytest.raises(TypeError):
             carve.carve_gdr_fwd(*x[:5], out=out)
+
+
+@pytest.mark.parametrize("Hk,Hv,dk,dv,seed", [(1, 2, 128, 128, 81), (2, 2, 64, 128, 82), (1, 1, 128, 64, 83), (2, 4, 64, 64, 84)])
+@pytest.mark.parametrize("kind", ["mild", "resets"])
+def test_delta_bf16_by_the_number_of_its_roundings(cuda_device, Hk, Hv, dk, dv, seed, kind):
+    """A rounding to bf16 is off by at most u, evenly spread, so u / sqrt(3) in the L2 norm; n independent
+    ones sqrt(n) times that, and half as much again where terms of either sign cancel.  n, the result's own
+    among them: o (A) 2; dq (S0, U, P1) 4; dk (S0, dS1, U, dY, P1, P2) 7; dv (A) 2; gates' g (S0, dS1, U, dY) 5,
+    w (U, dY) 3.  The gates' gradients by blocks of 16 tokens and heads too, so that a term that only some
+    tokens have cannot hide; amplitude and bias against the sum of their terms' sizes."""
+    T = 260
+    s = delta_inputs(T, Hk, Hv, dk, dv, BF16, seed)
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *n: torch.randn(*n, generator=g, dtype=torch.float32).double()  # noqa: E731
+    if kind == "resets":
+        s["g"] = torch.where(torch.rand(T, Hv, generator=g) < 0.03, torch.tensor(200.0, dtype=torch.float64), s["g"])
+    A_dec, tau, S0, dS = 0.3 * r(Hv), 0.5 * r(Hv), 0.2 * r(Hv, dv, dk), r(Hv, dv, dk)
+    dev = lambda x: x.float().to(cuda_device)  # noqa: E731
+    x = [s[n].to(BF16).to(cuda_device)[None] for n in ("q", "k", "v", "g", "w", "dO")]
+    more = dict(A_dec=dev(A_dec), tau=dev(tau))
+    out = carve.carve_gdr_fwd(*x[:5], S0=dev(S0[None]), **more)
+    gr = carve.carve_gdr_bwd(*x[:5], out["saved"], x[5], dS_final=dev(dS[None]), **more)
+    inp = dict(q=s["q"], k=s["k"], v=s["v"], g=s["g"], w=s["w"], A_dec=A_dec, tau=tau, S0=S0)
+    want_o, want_S = delta_definition(**inp)
+    wg = R.grads(delta_definition, inp, (s["dO"], dS))
+    u = U[BF16]
+    lim = lambda n: 1.5 * (n / 3) ** 0.5 * u  # noqa: E731
+    assert rel(out["S_final"][0], want_S) <= 2e-5
+    for name, got, want, n in (("o", out["o"], want_o, 2), ("dq", gr["dq"], wg["q"], 4), ("dk", gr["dk"], wg["k"], 7),
+                               ("dv", gr["dv"], wg["v"], 2), ("dg", gr["dg_logit"], wg["g"], 5), ("dw", gr["dw_logit"], wg["w"], 3)):
+        assert rel(got[0], want) <= lim(n), (name, rel(got[0], want), lim(n))
+    for name, got, want, n in (("dg", gr["dg_logit"], wg["g"], 5), ("dw", gr["dw_logit"], wg["w"], 3)):
+        err = got[0].double().cpu() - want
+        size = (want.square().mean(0)).sqrt()   # of a token's gradient, by head
+        for t in range(0, T, 16):
+            e, w = err[t:t + 16].norm(dim=0), want[t:t + 16].norm(dim=0)
+            # 16 tokens spread about twice as wide as all of them; a block whose own gradients are small still
+            # carries the roundings of what passes through it: half of an average token's for each
+            assert (e <= 2 * lim(n) * (w + 0.5 * size * 4)).all(), (name, t, (e / (w + 2 * size)).max().item())
+    softplus = torch.logaddexp(s["g"] + tau, torch.zeros(1, dtype=torch.float64))
+    slope = torch.sigmoid(s["g"] + tau)
+    for name, got, want, terms in (("dtau", gr["dtau"], wg["tau"], wg["g"]), ("dA", gr["dA_dec"], wg["A_dec"], wg["g"] / slope * softplus)):
+        assert ((got.double().cpu() - want).abs() <= lim(5) * terms.abs().sum(0)).all(), (name, got, want)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,W,sinks", [(4, 2, 128, 64, 4), (3, 3, 64, 33, 16), (2, 1, 64, 128, 1)])
+def test_window_gradients_of_sinks_in_sequences_far_beyond_the_window(cuda_device, Hq, Hkv, d, W, sinks):
+    """A sink's gradients sum over every query; bf16 against fp64, tolerances as in test_gpu_mixers.py."""
+    lens = (1500, 700)
+    seqs = [window_inputs(T, Hq, Hkv, d, BF16, 90 + n) for n, T in enumerate(lens)]
+    q, k, v, dO = (torch.cat([s[n] for s in seqs]).to(BF16).to(cuda_device) for n in ("q", "k", "v", "dO"))
+    at = dict(window=W, sinks=sinks, cu_seqlens=offsets(lens, cuda_device))
+    out = carve.carve_swa_fwd(q, k, v, **at)
+    gr = carve.carve_swa_bwd(q, k, v, out["o"], out["lse"], dO, **at)
+    row = 0
+    for T, s in zip(lens, seqs):
+        inp = {x: s[x] for x in ("q", "k", "v")}
+        want, lse = R.window(**inp, win=W, sinks=sinks)
+        wg = R.grads(lambda q, k, v: R.window(q, k, v, W, sinks)[:1], inp, (s["dO"],))
+        mass = R.window_masses(**inp, dO=s["dO"], win=W, sinks=sinks)
+        part = slice(row, row + T)
+        near(out["o"][part], want, mass["o"], 2, T, d, BF16)
+        assert (out["lse"][part].double().cpu() - lse).abs().max() <= 1e-4
+        near(gr["dv"][part], wg["v"], mass["dv"], 2, T * Hq // Hkv, d, BF16)
+        near(gr["dq"][part], wg["q"], mass["dq"], 3, T, d, BF16)
+        near(gr["dk"][part], wg["k"], mass["dk"], 3, T * Hq // Hkv, d, BF16)
+        row += T
+
+
+LARGEST = 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+@pytest.mark.parametrize("W,sinks,scale", [(LARGEST, 0, None), (1, LARGEST, None), (LARGEST, LARGEST, None), (40, 3, 0.0)], ids=str)
+def test_window_arguments_at_their_ends(cuda_device, dt, W, sinks, scale):
+    """The largest window and sink counts see everything before a token; scale 0 weighs all seen keys alike."""
+    T, Hq, Hkv, d = 300, 2, 1, 64
+    s = window_inputs(T, Hq, Hkv, d, dt, 95)
+    q, k, v, dO = (s[n].to(dt).to(cuda_device)[None] for n in ("q", "k", "v", "dO"))
+    at = dict(window=W, sinks=sinks, scale=scale)
+    out = carve.carve_swa_fwd(q, k, v, **at)
+    gr = carve.carve_swa_bwd(q, k, v, out["o"], out["lse"], dO, **at)
+    inp = {x: s[x] for x in ("q", "k", "v")}
+    want, lse = R.window(**inp, win=W, sinks=sinks, scale=scale)
+    wg = R.grads(lambda q, k, v: R.window(q, k, v, W, sinks, scale)[:1], inp, (s["dO"],))
+    mass = R.window_masses(**inp, dO=s["dO"], win=W, sinks=sinks, scale=scale)
+    near(out["o"][0], want, mass["o"], 2, T, d, dt)
+    assert (out["lse"][0].double().cpu() - lse).abs().max() <= 1e-4
+    near(gr["dv"][0], wg["v"], mass["dv"], 2, T * Hq // Hkv, d, dt)
+    near(gr["dq"][0], wg["q"], mass["dq"], 3, T, d, dt)
+    near(gr["dk"][0], wg["k"], mass["dk"], 3, T * Hq // Hkv, d, dt)
+
+
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+def test_window_steps_at_far_positions(cuda_device, dt):
+    """Positions beyond 2^32 reach the slots that they stand for: as at the small position of the same slot."""
+    W, sinks, Hq, Hkv, d = 37, 3, 4, 2, 64
+    g = torch.Generator(device="cuda").manual_seed(97)
+    r = lambda *s: torch.randn(*s, generator=g, device=cuda_device).to(dt)  # noqa: E731
+    q, k, v, kc, vc = r(3, Hq, d), r(3, Hkv, d), r(3, Hkv, d), r(3, sinks + W, Hkv, d), r(3, sinks + W, Hkv, d)
+    near_pos = torch.tensor([W + 5, W + 6, 2 * W + 1], device=cuda_device)
+    got = []
+    for far in (0, 2 ** 32 // W * W + W, 2 ** 50 // W * W):
+        a, b = kc.clone(), vc.clone()
+        got.append([carve.carve_swa_step(q, k, v, a, b, near_pos + far, window=W, sinks=sinks), a, b])
+    for x in got[1:]:
+        assert all(torch.equal(y, z) for y, z in zip(got[0], x))
+    for n, p in enumerate(near_pos.tolist()):
+        assert torch.equal(got[0][1][n, sinks + (p - sinks) % W], k[n])
