@@ -421,3 +421,45 @@ def test_window_steps_at_far_positions(cuda_device, dt):
         assert all(torch.equal(y, z) for y, z in zip(got[0], x))
     for n, p in enumerate(near_pos.tolist()):
         assert torch.equal(got[0][1][n, sinks + (p - sinks) % W], k[n])
+
+
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")], ids=str)
+@pytest.mark.parametrize("lens,first", [((70, 50, 30), 0), ((130, 1, 64, 3), 37)], ids=str)
+def test_a_sequence_that_is_not_finite_stays_alone(cuda_device, dt, bad, lens, first):
+    """Packed rows that start behind row 0; one sequence, and the rows of none, hold no finite value in any input.
+    The other sequences' results keep every bit, and the rows of no sequence stay as they were."""
+    cu = offsets(lens, cuda_device) + first
+    total, sick = first + sum(lens) + 5, 1
+    at = cu.tolist()
+    Hk, Hv, dk, dv = 2, 4, 128, 64
+    x = [y.to(dt) for y in delta_tensors((total,), Hk, Hv, dk, dv, 98, cuda_device)]
+    y = [z.to(dt) for z in window_tensors((total,), 4, 2, 64, 98, cuda_device)]
+
+    def spoil(t):
+        t = t.clone()
+        t[:first] = bad
+        t[at[sick]:at[sick + 1]] = bad
+        t[at[-1]:] = bad
+        return t
+
+    def run(x, y):
+        mark = lambda t: torch.full_like(t, 7.0)  # noqa: E731
+        out = carve.carve_gdr_fwd(*x[:5], cu_seqlens=cu, out=dict(o=mark(x[2])))
+        g = carve.carve_gdr_bwd(*x[:5], out["saved"], x[5], cu_seqlens=cu, out={n: mark(x[i]) for n, i in
+                                (("dq", 0), ("dk", 1), ("dv", 2), ("dg_logit", 3), ("dw_logit", 4))})
+        W = dict(window=20, sinks=2, cu_seqlens=cu)
+        b = carve.carve_swa_fwd(*y[:3], out=dict(o=mark(y[0])), **W)
+        gb = carve.carve_swa_bwd(*y[:3], b["o"], b["lse"], y[3], out=dict(dq=mark(y[0]), dk=mark(y[1]), dv=mark(y[2])), **W)
+        return [out["o"], *(g[n] for n in ("dq", "dk", "dv", "dg_logit", "dw_logit")), b["o"], *gb.values()], [out["S_final"], g["dS0"]]
+
+    rows, states = run(x, y)
+    rows2, states2 = run([spoil(t) for t in x], [spoil(t) for t in y])
+    for a, b in zip(rows, rows2):
+        assert (b[:first] == 7.0).all() and (b[at[-1]:] == 7.0).all()
+        for n in range(len(lens)):
+            if n != sick:
+                assert torch.equal(a[at[n]:at[n + 1]], b[at[n]:at[n + 1]])
+    for a, b in zip(states, states2):
+        for n in range(len(lens)):
+            assert n == sick or torch.equal(a[n], b[n])
