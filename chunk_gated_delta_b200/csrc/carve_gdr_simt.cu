@@ -92,7 +92,7 @@ __device__ __forceinline__ void copy_f32(float *dst, int ld, const float *src, i
 }
 
 // prep: Tm, A, G, w of one tile and value head
-template <int K, class IO>
+template <int K>
 __global__ void __launch_bounds__(NT) gdr_simt_prep(GdrArgs a) {
     __shared__ __align__(16) float k[C][K + 4], q[C][K + 4];
     __shared__ float M[C][LC], X[C][LC], G[C], L[C], w[C];
@@ -109,9 +109,9 @@ __global__ void __launch_bounds__(NT) gdr_simt_prep(GdrArgs a) {
         float la = 0.f, ww = 0.f;
         if (tid < m) {
             const size_t at = (size_t)(row0 + tid) * a.Hv + h;
-            const float x = ld_io(static_cast<const IO *>(a.g_logit) + at) + (a.tau ? a.tau[h] : 0.f);
+            const float x = static_cast<const float *>(a.g_logit)[at] + (a.tau ? a.tau[h] : 0.f);
             la = least_log(-decay_amp(a.A_dec, h) * softplus_f(x));
-            ww = sigmoid_f(ld_io(static_cast<const IO *>(a.w_logit) + at));
+            ww = sigmoid_f(static_cast<const float *>(a.w_logit)[at]);
         }
         float lo = 0.f;
         sum2_scan(la, lo, tid);
@@ -407,7 +407,7 @@ __device__ __forceinline__ float sum16(float x) {
 }
 
 // gradients of q, k (summed over the value heads of a key head, in order) and of the gates
-template <int K, int V, class IO>
+template <int K, int V>
 __global__ void __launch_bounds__(NT) gdr_simt_grad(GdrArgs a) {
     extern __shared__ __align__(16) unsigned char raw[];
     GradSmem<K, V> &sm = *reinterpret_cast<GradSmem<K, V> *>(raw);
@@ -578,12 +578,12 @@ __global__ void __launch_bounds__(NT) gdr_simt_grad(GdrArgs a) {
             float dlog = 0.f, damp = 0.f;
             if (tid < m) {
                 const size_t at = (size_t)(row + tid) * a.Hv + h;
-                const float x = ld_io(static_cast<const IO *>(a.g_logit) + at) + (a.tau ? a.tau[h] : 0.f);
+                const float x = static_cast<const float *>(a.g_logit)[at] + (a.tau ? a.tau[h] : 0.f);
                 const float amp = decay_amp(a.A_dec, h), w = sm.w[tid];
                 dlog = -amp * sigmoid_f(x) * g;
                 damp = softplus_f(x) * (-amp * g);   // of a reset g is 0, and amp softplus may be beyond fp32
-                st_io(static_cast<IO *>(a.dg_logit) + at, dlog);
-                st_io(static_cast<IO *>(a.dw_logit) + at, sm.row[1][tid] * w * (1.f - w));
+                static_cast<float *>(a.dg_logit)[at] = dlog;
+                static_cast<float *>(a.dw_logit)[at] = sm.row[1][tid] * w * (1.f - w);
             }
             if (a.dA_dec || a.dtau) {
 #pragma unroll
@@ -606,8 +606,8 @@ __global__ void __launch_bounds__(NT) gdr_simt_grad(GdrArgs a) {
             const int t = tid / 16 + 16 * i;
             const size_t at = ((size_t)(row + t) * a.Hk + hk) * K + col4(j);
             if (t < m) {
-                st_io(static_cast<IO *>(a.dq) + at, dq[i][j]);
-                st_io(static_cast<IO *>(a.dk) + at, dk[i][j]);
+                static_cast<float *>(a.dq)[at] = dq[i][j];
+                static_cast<float *>(a.dk)[at] = dk[i][j];
             }
         }
 }
@@ -649,10 +649,10 @@ GdrSizes gdr_simt_sizes(const Seqs &s, int Hv, int K, int V) {
 
 namespace {
 
-template <int K, int V, class IO>
+template <int K, int V>
 cudaError_t fwd_t(const GdrArgs &a, bool save, cudaStream_t st) {
     const long long tiles = a.seq.n_tiles(C);
-    if (tiles) gdr_simt_prep<K, IO><<<(unsigned)(tiles * a.Hv), NT, 0, st>>>(a);
+    if (tiles) gdr_simt_prep<K><<<(unsigned)(tiles * a.Hv), NT, 0, st>>>(a);
     auto kern = gdr_simt_sweep<K, V>;
     cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), sizeof(SweepSmem<K>));
     if (e != cudaSuccess) return e;
@@ -660,10 +660,10 @@ cudaError_t fwd_t(const GdrArgs &a, bool save, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-template <int K, int V, class IO>
+template <int K, int V>
 cudaError_t bwd_t(const GdrArgs &a, cudaStream_t st) {
     auto sweep = gdr_simt_bsweep<K, V>;
-    auto grad = gdr_simt_grad<K, V, IO>;
+    auto grad = gdr_simt_grad<K, V>;
     cudaError_t e = set_smem_once(reinterpret_cast<const void *>(sweep), sizeof(SweepSmem<K>));
     if (e == cudaSuccess) e = set_smem_once(reinterpret_cast<const void *>(grad), sizeof(GradSmem<K, V>));
     if (e != cudaSuccess) return e;
@@ -688,7 +688,7 @@ struct Fwd {
     cudaStream_t st;
     template <int K, int V>
     cudaError_t operator()() const {
-        return fwd_t<K, V, float>(a, save, st);
+        return fwd_t<K, V>(a, save, st);
     }
 };
 struct Bwd {
@@ -696,7 +696,7 @@ struct Bwd {
     cudaStream_t st;
     template <int K, int V>
     cudaError_t operator()() const {
-        return bwd_t<K, V, float>(a, st);
+        return bwd_t<K, V>(a, st);
     }
 };
 
