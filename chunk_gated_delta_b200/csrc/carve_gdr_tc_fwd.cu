@@ -170,7 +170,6 @@ __global__ void __launch_bounds__(128) gdr_tc_prep(GdrArgs a, const __grid_const
         if (threadIdx.x == 0) atomicOr(&g_gdr_timeout, 1);
         return;
     }
-    let_next_start();
     const int tile = blockIdx.x / a.Hk, hk = blockIdx.x % a.Hk, share = a.Hv / a.Hk;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     int n, c, len;
@@ -188,6 +187,7 @@ __global__ void __launch_bounds__(128) gdr_tc_prep(GdrArgs a, const __grid_const
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tm = sm.tmem;
+    let_next_start();   // not before the allocation: a sweep's CTA takes all tensor memory of its SM and waits for this kernel
     bool ok = true;
     if (warp == 3) {
         if (elect_one()) {

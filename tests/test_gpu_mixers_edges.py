@@ -463,3 +463,18 @@ def test_a_sequence_that_is_not_finite_stays_alone(cuda_device, dt, bad, lens, f
     for a, b in zip(states, states2):
         for n in range(len(lens)):
             assert n == sick or torch.equal(a[n], b[n])
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128)])
+def test_delta_prompts_on_many_streams_at_once(cuda_device, dk, dv):
+    """Preparations and sweeps of eight calls share the SMs and their tensor memory: each call's result is what
+    it is alone, and no wait runs out."""
+    xs = [delta_tensors((6, 300), 4, 8, dk, dv, 110 + n, cuda_device) for n in range(8)]
+    alone = [carve.carve_gdr_fwd(*x[:5], save_for_bwd=False) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    for _ in range(10):
+        got = [carve.carve_gdr_fwd(*x[:5], save_for_bwd=False, stream=s) for x, s in zip(xs, streams)]
+    torch.cuda.synchronize()
+    for a, b in zip(alone, got):
+        assert torch.equal(a["o"], b["o"]) and torch.equal(a["S_final"], b["S_final"])
