@@ -5,6 +5,7 @@
 // e^{G_t - G_s} (only s <= t, so never above 1):
 //   M[t,s] = w_t D[t,s] k_t.k_s (s < t),  Tm = (I + M)^-1,  A[t,s] = D[t,s] q_t.k_s (s <= t)
 //   R = V - e^G K S0^T,  U = Tm (w R),  O = e^G Q S0^T + A U,  S1 = e^{G_C} S0 + (e^{G_C - G} U)^T K
+// G is a sum in two floats (carve_mixers.cuh); its low part enters D as a factor of the row and one of the column.
 // The decay is one scalar a token, so it never touches a matrix operand: K, Q, V, dO enter the
 // products as the bf16 values that they are, and the factors act on fp32 accumulators.  Operands that
 // are results (S, w R, e^{G_C - G} U, Tm) are split into two bf16 terms, hi + lo (16 bits
@@ -25,11 +26,11 @@ constexpr uint32_t kTile64 = kC * 128;   // bytes of a 64-row block
 struct GdrPrep {
     __nv_bfloat16 t_hi[kC * 64], t_lo[kC * 64], A[kC * 64];
     float eG[kC], eK[kC], w[kC], G[kC];   // e^{G_t}, e^{G_C - G_t}, w_t, G_t log2 e
-    float eB[kC], L[kC];                  // e^{G_r - G_t}, r the last of t's 16 tokens; G's low part
+    float eB[kC], rL[kC];                 // e^{G_r - G_t}, r the last of t's 16 tokens; e^{-G_t's low part}
     float pad[128];
 };
 static_assert(sizeof(GdrPrep) == 26624, "slots are copied in bulk, tiles on 1024-byte boundaries");
-constexpr uint32_t kVecBytes = 6 * kC * 4;   // eG .. L
+constexpr uint32_t kVecBytes = 6 * kC * 4;   // eG .. rL
 
 // Per (tile, value head): the state [V][K] and a token tile [64][V], bf16 operand layout.
 template <int K, int V>

@@ -319,7 +319,7 @@ struct GradSmem {
     __nv_bfloat16 S0[V * K], S1[V * K];        // S0, dS1
     __nv_bfloat16 qk[2][K / 64][128 * 64];     // [stage]: Q, K, then dq, dk on their way out
     __nv_bfloat16 P[192 * 64];                 // zeros, P1, P2
-    float vec[2][6][kC];                       // [stage]: e^G, e^{G_C - G}, w, G, e^{G_r - G}, L
+    float vec[2][6][kC];                       // [stage]: e^G, e^{G_C - G}, w, G, e^{G_r - G}, e^{-low part of G}
     float dg[4][128], dw[kC], kb[4][kC], tot[3][128], col[4][kC], last[8];   // partial sums of a head
     uint64_t vfull[2], vfree[2], qkfull[2], qkfree[2], dfull, dfree, s0full, s0free, s1full, s1free, Dfull, Dfree, xfull,
         xfree, yfull, yfree, pready, pfull, afree, gready, gfree, oready[2], drain;   // oready: [stage]
@@ -729,8 +729,8 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
             for (int g = 0; g < share && ok; ++g, ++j) {
                 const int s = j & 1;
                 if (!(ok = wait(sm.vfull[s], j / 2))) break;
-                const float *eG = sm.vec[s][0], *eK = sm.vec[s][1], *G = sm.vec[s][3] + s0, *L = sm.vec[s][5] + s0;
-                const float Gt = sm.vec[s][3][t], Lt = sm.vec[s][5][t], sign = key ? -sm.vec[s][2][t] : 1.f;
+                const float *eG = sm.vec[s][0], *eK = sm.vec[s][1], *G = sm.vec[s][3] + s0, *rL = sm.vec[s][5] + s0;
+                const float Gt = sm.vec[s][3][t], sign = (key ? -sm.vec[s][2][t] : 1.f) * __frcp_rn(sm.vec[s][5][t]);
                 // pairs of the chunk: y = D (dO U^T) or -w D (dY U^T), times k.k or q.k
                 if (!(ok = wait(sm.Dfull, j))) break;
                 tc_fence_after_sync();
@@ -745,7 +745,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                     mbar_arrive_warp(&sm.Dfree);
                     float pr[16], own = 0.f, run = 0.f;
                     if (pairs == 2) {   // all of them below the diagonal: one factor a row, one a column
-                        const float f = here ? sign * ex2(sum2_diff(Gt, Lt, G[15], L[15])) : 0.f;
+                        const float f = here ? sign * ex2(Gt - G[15]) * rL[15] : 0.f;
                         const float *eB = sm.vec[s][4] + s0;
 #pragma unroll
                         for (int e = 0; e < 16; e += 4) {
@@ -763,7 +763,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
                         for (int e = 0; e < 16; ++e) {
                             const float x = __uint_as_float(D[e]);
                             own = t - s0 == e ? x : own;
-                            const float y = e < lim ? sign * ex2(sum2_diff(Gt, Lt, G[e], L[e])) * x : 0.f;
+                            const float y = e < lim ? sign * ex2(Gt - G[e]) * rL[e] * x : 0.f;
                             pr[e] = y * __uint_as_float(kk[e]);
                             D[e] = __float_as_uint(y);
                         }

@@ -65,7 +65,7 @@ struct PrepSmem {
         };
     };
     __nv_bfloat16 A[kC * 64];
-    float eG[kC], eK[kC], w[kC], G[kC], eB[kC], L[kC], half[2];
+    float eG[kC], eK[kC], w[kC], G[kC], eB[kC], rL[kC], half[2];
     uint64_t full, done;
     uint32_t tmem;
 };
@@ -225,12 +225,12 @@ __global__ void __launch_bounds__(128) gdr_tc_prep(GdrArgs a, const __grid_const
         asm volatile("bar.sync 1, 64;\n" ::: "memory");
         if (warp == 1) sum2_add(la, lo, sm.half[0], sm.half[1]);
         sm.G[tid] = la;
-        sm.L[tid] = lo;
+        sm.rL[tid] = exp2f(-lo);
         sm.w[tid] = w;
         asm volatile("bar.sync 1, 64;\n" ::: "memory");
         sm.eG[tid] = exp2f(la);
-        sm.eK[tid] = exp2f(sum2_diff(sm.G[kC - 1], sm.L[kC - 1], la, lo));
-        sm.eB[tid] = exp2f(sum2_diff(sm.G[tid | 15], sm.L[tid | 15], la, lo));
+        sm.eK[tid] = exp2f(sm.G[kC - 1] - la) * (sm.rL[tid] / sm.rL[kC - 1]);
+        sm.eB[tid] = exp2f(sm.G[tid | 15] - la) * (sm.rL[tid] / sm.rL[tid | 15]);
     };
     gates(hk * share);   // the first head's while the tiles and their product are under way
     ok = ok && mbar_wait(&sm.done, 0, kSwaWait);
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(128) gdr_tc_prep(GdrArgs a, const __grid_const
             gates(h);
             __syncthreads();
         }
-        const float Gt = sm.G[t], Lt = sm.L[t], f0 = key ? sm.w[t] : 1.f;
+        const float Gt = sm.G[t], f0 = (key ? sm.w[t] : 1.f) / sm.rL[t];   // D[t,s] = 2^{G_t - G_s} rL_s / rL_t
 #pragma unroll 1
         for (int s0 = 0; s0 <= (t | 31); s0 += 16) {
             uint32_t g[16];
@@ -267,13 +267,13 @@ __global__ void __launch_bounds__(128) gdr_tc_prep(GdrArgs a, const __grid_const
             tmem_tie16(g);
             float y[16];
             if (s0 + 15 < (t & 32)) {   // all below the diagonal: one factor a row, one a column
-                const float f = f0 * ex2(sum2_diff(Gt, Lt, sm.G[s0 + 15], sm.L[s0 + 15]));
+                const float f = f0 * ex2(Gt - sm.G[s0 + 15]) * sm.rL[s0 + 15];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) y[e] = here ? f * sm.eB[s0 + e] * __uint_as_float(g[e]) : 0.f;
             } else {
                 const int lim = here ? t + !key - s0 : 0;   // s < t, and s = t for queries
 #pragma unroll
-                for (int e = 0; e < 16; ++e) y[e] = e < lim ? f0 * ex2(sum2_diff(Gt, Lt, sm.G[s0 + e], sm.L[s0 + e])) * __uint_as_float(g[e]) : 0.f;
+                for (int e = 0; e < 16; ++e) y[e] = e < lim ? f0 * ex2(Gt - sm.G[s0 + e]) * sm.rL[s0 + e] * __uint_as_float(g[e]) : 0.f;
             }
             if (!key) {
 #pragma unroll
