@@ -54,8 +54,9 @@ __device__ __forceinline__ void zero_rows(void *tile, int first, int halves, uin
 }
 
 // The sweeps' register warps: four a lane quarter, each with a quarter of the columns (state) or 16
-// of the chunk's tokens.  Half as many threads with twice the columns spilled, and with shared memory
-// taken by the tiles a spill goes to L2.
+// of the chunk's tokens.  Half as many threads with twice the columns spilled (6.8 us a chunk), and with shared
+// memory taken by the tiles a spill goes to L2.  At d = 128 the sweeps still spill a little, 54 to 70 bytes a thread
+// forward, 120 backward.
 constexpr int kRegWarps = 16, kSweepThreads = (kRegWarps + 4) * 32;
 // Registers: 640 threads start with 96 (61440 in all); the register warps take 112 and the others go
 // down to 32 (512 x 112 + 128 x 32 = 61440), or 104 and 64.

@@ -7,7 +7,7 @@
 //   dY = dU Tm (three terms)         -> -w e^G dY, split; dV = w dY; dY
 //   dS0 = e^{G_C} dS1 + (e^G dO)^T Q - (w e^G dY)^T K   (hi, lo) -> split for the next chunk
 // It leaves dS1 and dY of every chunk in bf16.  Bound as the forward's sweep, by the chain and by what it
-// leaves: 8 sequences of 4096 tokens, 16 heads, d = 128 take 208 us.
+// leaves: 8 sequences of 4096 tokens, 16 heads, d = 128 take 214 us.
 //
 // gdr_tc_grad: with S0, U (forward) and dS1, dY known, the gradients of q, k and the gates have no
 // order: persistent CTAs take (tile, key head), all value heads of the key head in turn.  Tokens are the

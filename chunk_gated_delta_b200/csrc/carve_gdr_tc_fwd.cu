@@ -3,7 +3,7 @@
 // gdr_tc_prep: one CTA per (tile, key head) forms [Q; K] K^T with one M = 128 product and, for each
 // value head of the key head, the decayed A and M, Tm by blocked inversion (fp32 substitution on the
 // diagonal, three tf32 products off it), and the gate vectors.  It needs no state, so all tiles run
-// at once; instruction issue and latency bound it (8 sequences of 4096 tokens, 16 heads, d = 128: 109
+// at once; instruction issue and latency bound it (8 sequences of 4096 tokens, 16 heads, d = 128: 111
 // us, 4.5 TB/s; four CTAs an SM and gates after the product 123, with the inverse in plain fp32 and an
 // exponential a pair 204).
 //
@@ -17,7 +17,7 @@
 //   O = e^G Q S^T + U A^T (S, U hi, lo), two accumulators, off the chain
 // The chain of one chunk is three products and three register passes; what bounds the sweep is
 // their latency (B H units on 148 SMs, one chain each): 2.9 us a chunk, of which the products
-// take 1.2.  With the states kept (the sizes above: 227 us, 1.15 GB) HBM is as near, 5.1 TB/s.
+// take 1.2.  With the states kept (the sizes above: 230 us, 1.15 GB) HBM is as near, 5.0 TB/s.
 // Chunks of 64: the products of 128 tokens need 576 columns of tensor memory, and an inverse of four
 // times the work.
 // Warps 0-15 register passes, 16 copies in (TMA and bulk, two stages), 17 products, 18 and 19 copies out.  What

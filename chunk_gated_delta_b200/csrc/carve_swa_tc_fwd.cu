@@ -19,8 +19,8 @@
 // warps 17 and 18 issue the products of a tile each.  Persistent: a unit's copies and first products run
 // beside the last one's outputs (the two took a fifth of a CTA's time at W = 1024, a quarter at 512).
 // Softmax bounds it: 2000 cycles for 64 keys of both tiles, of which the exponentials need 1024 and the
-// products 1280.  8 sequences of 4096 tokens, 16 query and 4 key heads, d = 128, W = 1024: 314 us, 770
-// TFLOP/s of products; 4 of 2048, W = 512: 69 us.
+// products 1280.  8 sequences of 4096 tokens, 16 query and 4 key heads, d = 128, W = 1024: 310 us, 780
+// TFLOP/s of products; 4 of 2048, W = 512: 68 us.
 //
 // Blocks that a tile does not see are skipped; only blocks that a window edge or the diagonal
 // crosses are masked, by selection.  Value rows behind the sequence's end are zeroed in shared

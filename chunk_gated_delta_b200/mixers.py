@@ -71,8 +71,8 @@ def _lib():
 # ---- the scalar-gated delta rule ------------------------------------------------------------
 def carve_gdr_fwd(q, k, v, g_logit, w_logit, A_dec=None, tau=None, S0=None, cu_seqlens=None,
                   save_for_bwd: bool = True, out: dict | None = None, workspace=None, stream=None) -> dict:
-    """The scalar-gated delta rule over [B,T,Hk,dk] q, k and [B,T,Hv,dv] v with gates [B,T,Hv]
-    (or packed rows): a = exp(-e^A_dec softplus(g_logit + tau)), w = sigmoid(w_logit),
+    """The scalar-gated delta rule over [B,T,Hk,dk] q, k and [B,T,Hv,dv] v with gates [B,T,Hv] of the
+    same dtype (or packed rows): a = exp(-e^A_dec softplus(g_logit + tau)), w = sigmoid(w_logit),
     S_t = a S + w (v - a S k) k^T, o = S_t q.  A_dec, tau [Hv] float32 and S0 [B,Hv,dv,dk]
     float32 are optional.  Returns dict(o, S_final[, saved]); `out` may supply preallocated
     buffers under the same keys (S_final may be S0 itself)."""

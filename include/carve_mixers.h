@@ -13,10 +13,13 @@
  * Packed sequences: a non-NULL cu_seqlens (DEVICE int32 [B+1], non-decreasing) packs B sequences
  * along the token axis without padding: sequence n owns rows [cu[n], cu[n+1]) of [total_tokens,
  * heads, channels] tensors, and T is ignored.  Lengths from 0 are allowed; rows that belong to
- * no sequence are neither read nor written.  The offsets live on the device: a sequence whose
+ * no sequence reach no result and are not written.  The offsets live on the device: a sequence whose
  * rows fall outside [0, total_tokens] is treated as empty and the next carve_check returns
  * CARVE_ERR_INVALID_ARG (results are undefined, but nothing outside the buffers is touched).
+ * Every packed call looks at its offsets, one without rows too.
  * With cu_seqlens NULL, tensors are [B, T, heads, channels] and total_tokens is ignored.
+ *
+ * Outputs overlap no input, except where a call says so.
  *
  * Inputs are expected to be finite.  A non-finite value reaches, beside the tokens that see it,
  * at most the other tokens of its own sequence that share a compute tile with them; it never
@@ -45,7 +48,8 @@ extern "C" {
  *   S0, S_final       [B, Hv, dv, dk] float, nullable
  * Gradients have the layout and dtype of their tensor.  dk, dv in {64, 128}; Hv a multiple of
  * Hk; any T >= 0 (token pointers may be NULL when there are no rows).  Keys are meant to be
- * L2-normalised (the recurrence is contractive then); q is used as given (no scale). */
+ * L2-normalised (the recurrence is contractive then); q is used as given (no scale).  A logit of any
+ * finite size may reset the state: log decays below -1e4 count as -1e4, zero either way. */
 typedef struct {
     int B, T, Hk, Hv, dk, dv;
     int io;                 /* carve_io */
