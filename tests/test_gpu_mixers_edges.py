@@ -478,3 +478,67 @@ def test_delta_prompts_on_many_streams_at_once(cuda_device, dk, dv):
     torch.cuda.synchronize()
     for a, b in zip(alone, got):
         assert torch.equal(a["o"], b["o"]) and torch.equal(a["S_final"], b["S_final"])
+
+
+def test_tensors_beyond_2_to_the_31_elements(cuda_device):
+    """Packed rows, states and caches whose last elements lie behind 2^31 (caches 2^32): the last sequence's results
+    are the ones that it gives alone, bit for bit."""
+    H, d, tail = 16, 128, 500
+    rows = 2 ** 31 // (H * d) + 4000
+    first = rows - tail
+    g = torch.Generator(device="cuda").manual_seed(120)
+
+    def normal(*s):
+        return torch.empty(*s, dtype=BF16, device=cuda_device).normal_(generator=g)
+
+    last = lambda xs: [x[first:].clone() for x in xs]  # noqa: E731
+    cu = offsets((first, tail), cuda_device)
+    x = [normal(rows, H, d) for _ in range(3)] + [normal(rows, H), normal(rows, H), normal(rows, H, d)]
+    for i in (0, 1):
+        x[i] /= d ** 0.5
+    at = dict(window=64, sinks=0)   # without sinks, which every query of the long sequence would see
+    b = carve.carve_swa_fwd(*x[:3], cu_seqlens=cu, **at)
+    gb = carve.carve_swa_bwd(*x[:3], b["o"], b["lse"], x[5], cu_seqlens=cu, **at)
+    y = last(x)
+    one = offsets((tail,), cuda_device)
+    c = carve.carve_swa_fwd(*y[:3], cu_seqlens=one, **at)
+    assert torch.equal(b["o"][first:], c["o"]) and torch.equal(b["lse"][first:], c["lse"])
+    gc = carve.carve_swa_bwd(*y[:3], c["o"], c["lse"], y[5], cu_seqlens=one, **at)
+    # dk, dv: a pass of few keys is summed in parts, so equal but for the rounding of the result (half a step each)
+    assert torch.equal(gb["dq"][first:], gc["dq"])
+    for n in ("dk", "dv"):
+        assert rel(gb[n][first:], gc[n].double().cpu()) <= 2 * U[BF16], n
+    del b, gb
+    a = delta_both(x, cu)
+    z = delta_both(y, one)
+    for n in ("o", "dq", "dk", "dv", "dg_logit", "dw_logit"):
+        assert torch.equal(a[n][first:], z[n]), n
+    for n in ("S", "dS0"):
+        assert torch.equal(a[n][1:], z[n]), n
+    del a, x
+    B, W, Hkv = 33, 65536 * 2, 8
+    kc = torch.zeros(B, W, Hkv, d, dtype=BF16, device=cuda_device)
+    assert kc.numel() > 2 ** 32
+    vc = torch.zeros_like(kc)
+    kc[-1].normal_(generator=g)
+    vc[-1].normal_(generator=g)
+    q, k, v = normal(B, 2 * Hkv, d), normal(B, Hkv, d), normal(B, Hkv, d)
+    pos = torch.full((B,), W - 1, dtype=torch.int64, device=cuda_device)
+    pos[:-1] = 0
+    k1, v1 = kc[-1:].clone(), vc[-1:].clone()
+    o = carve.carve_swa_step(q, k, v, kc, vc, pos, window=W)
+    o1 = carve.carve_swa_step(q[-1:].clone(), k[-1:].clone(), v[-1:].clone(), k1, v1, pos[-1:].clone(), window=W)
+    # one sequence alone may be split over more parts: a rounding of the result, and of each part's p
+    assert rel(o[-1:], o1.double().cpu()) <= 2 * U[BF16]
+    assert torch.equal(kc[-1:], k1) and torch.equal(vc[-1:], v1)
+    del kc, vc, k1, v1
+    S = torch.zeros(9000, 16, 128, 128, device=cuda_device)
+    assert S.numel() > 2 ** 31
+    S[-1].normal_(generator=g)
+    S1 = S[-1:].clone()
+    t = [normal(9000, 16, 128) / 11, normal(9000, 16, 128) / 11, normal(9000, 16, 128), normal(9000, 16), normal(9000, 16)]
+    o = carve.carve_gdr_step(*t, S)
+    o1 = carve.carve_gdr_step(*(y[-1:].clone() for y in t), S1)
+    assert torch.equal(o[-1:], o1) and torch.equal(S[-1:], S1)
+    del S, t, o
+    torch.cuda.empty_cache()   # some 60 GB that the next tests do not need
